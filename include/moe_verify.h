@@ -307,6 +307,168 @@ int expand_drafts(const int32_t *parent, int32_t N, const float *P, const uint32
                   float t_ar, float t_exp, const float *c_draft, int32_t nt, int32_t *S, int32_t *count,
                   void *stream);
 
+/* ------------------------------------------------------------------------
+ * 4-bit K/V cache of the verified tokens ([EcoSpec] tree-attention verify
+ * mask; [S2-MoE] component 3: draft writes are tentative, the accepted
+ * tokens' K/V is committed).
+ *
+ * The cache is a pool of pages of `page` rows (tokens), shared by sequences
+ * through a page table.  K and V are held in OCP MX style: blocks of 32
+ * consecutive elements along the head dimension share a scale 2^(e - 127)
+ * (one byte e), each element is an e2m1 code (0, .5, 1, 1.5, 2, 3, 4, 6 and
+ * a sign in bit 3).  The scale of a block is the smallest power of two
+ * 2^-100 .. 2^125 with max|x| <= 6 * 2^n, elements are rounded to nearest, ties to
+ * the even code, and saturate at 6.
+ *   data [num_pages][Hkv][page / 16] tiles of 17 D bytes (device, 16-byte
+ *   aligned, kv4_cache_bytes bytes; needs no initialisation).  A tile holds
+ *   16 rows i = 0..15 in matrix-core operand order:
+ *     8 D bytes  K codes: element d of row i in byte i * D/2 + d/2, even d in
+ *                the low half
+ *     D/2        K scales: block b of row i in byte 16 b + i
+ *     8 D        V codes: element d of row i, w = D / 32, in byte
+ *                (64 (i/4) + 4 (d/(2w)) + i%4) w + (d%(2w))/2, even d low
+ *     D/2        V scales: block b of row i in byte 16 b + i
+ *   D is 64, 128 or 256; page a power of two, 16 .. 4096. */
+typedef struct {
+    void *data;
+    int32_t num_pages, page, Hkv, D;
+} moe_kv4_cache;
+
+/* The rows of one call, grouped by sequence as in moe_bias: call row t =
+ * seg_off[s] + j is row j of sequence s and has the cache position len[s] + j.
+ *   table [nseq, max_pages] i32 (device): page of positions page * i ..
+ *         page * (i + 1) - 1 of sequence s in table[s][i].  Entries outside
+ *         [0, num_pages) hold no rows: nothing is written to them and
+ *         nothing is seen in them, nor past the table's end.
+ *   len   [nseq] i32 (device): rows of each sequence before this call's
+ *         (negative counts as 0)
+ *   seg_off (host) [nseq + 1], 0 = seg_off[0] <= ... <= seg_off[nseq] = T,
+ *         read during the call only; 1 <= nseq <= MOE_MAX_SEGMENTS. */
+typedef struct {
+    const int32_t *table;
+    int32_t max_pages;
+    const int32_t *len;
+    int32_t nseq;
+    const int32_t *seg_off;
+} moe_kv4_rows;
+
+/* Bytes of a cache's data; 0 for invalid sizes. */
+size_t kv4_cache_bytes(int32_t num_pages, int32_t page, int32_t Hkv, int32_t D);
+
+/* Quantises K and V rows into the cache.
+ *   k, v [T, Hkv, D] in dtype MOE_F32 or MOE_BF16; consecutive tokens are
+ *         k_stride / v_stride elements apart (>= Hkv * D; slices of a fused
+ *         projection), 16-byte aligned rows
+ *   path [T], count [nseq] i32 (device), or both NULL.  NULL: row j of
+ *         sequence s is written to position len[s] + j (a prompt, or the
+ *         tentative rows of a draft tree).  Else the commit of an accepted
+ *         path, as accept_drafts returns it: for i < count[s], row
+ *         path[seg_off[s] + i] of the sequence is written to position
+ *         len[s] + i (entries outside the sequence's rows are skipped).
+ *   k_out, v_out [T, Hkv, D] in dtype (dense), or both NULL: the values that
+ *         the codes stand for, for every row of the call; only without path.
+ * Positions written twice in one call (a page listed twice) hold either row.
+ * Limits: 1 <= T <= 2^20.  Errors: EINVAL, ENOTSUP (D, dtype). */
+int kv4_append(const moe_kv4_cache *cache, const moe_kv4_rows *rows, const void *k, const void *v,
+               int64_t k_stride, int64_t v_stride, int32_t T, int32_t dtype, const int32_t *path,
+               const int32_t *count, void *k_out, void *v_out, void *stream);
+
+/* Workspace bytes of kv4_attend (host computation); 0 for invalid input. */
+size_t kv4_attend_workspace_bytes(const moe_kv4_cache *cache, const moe_kv4_rows *rows, int32_t T, int32_t Hq,
+                                  int32_t dtype);
+
+/* Attention of the verified tokens over the cache, their own rows included
+ * (append them first):
+ *   out[t, h] = sum_p softmax_p(scale * q[t, h] . K[p, h / (Hq / Hkv)]) V[p, ...]
+ * over the positions p that t sees: all of its sequence's rows before this
+ * call, itself, and its ancestors among the call's rows.  A token that sees
+ * nothing (every page outside the pool) gets zeros.
+ *   q [T, Hq, D] in dtype MOE_F32 or MOE_BF16, tokens q_stride elements apart
+ *         (16-byte aligned rows); out [T, Hq, D] in dtype, dense
+ *   parent (host) [T], read during the call only: parent of each row inside
+ *         its sequence (row j has a parent in [0, j); the first row -1), or
+ *         NULL for chains (each row sees all rows before it)
+ *   ws    16-byte aligned, kv4_attend_workspace_bytes bytes, no initialisation
+ * Sums and softmax statistics are float32.  bf16: probabilities enter the
+ * second product rounded to bf16.  float32: q and the probabilities enter
+ * the products as three bf16 terms (24 bits).
+ * Limits: 1 <= T <= MOE_MAX_TOKENS, Hq a multiple of Hkv. */
+int kv4_attend(const moe_kv4_cache *cache, const moe_kv4_rows *rows, const void *q, int64_t q_stride, int32_t T,
+               int32_t Hq, int32_t dtype, float scale, const int32_t *parent, void *out, void *ws,
+               size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Drawing and accepting draft tokens.  Both use the filtered distribution of
+ * a row of logits l [V], defined in 64 bits:
+ *   the tokens with l > -inf (NaN counts as -inf, +inf as the largest float)
+ *   are ranked by (l desc, index asc); w_i = exp((l_i - l_first) / temperature);
+ *   the first n are kept, n the smallest (at least 1) of
+ *     top_k (off when <= 0),
+ *     the least number whose weights sum to >= top_p * (sum of the first
+ *       top_k) (off when >= 1),
+ *     the number with w_i >= min_p (off when <= 0);
+ *   temperature <= 0 keeps the first only.
+ * p_i = w_i / (sum of the kept).  A draw with a number u in [0, 1) takes the
+ * lowest kept index whose running sum in index order exceeds u * sum; a row
+ * without tokens gives -1.
+ * Weights are summed as integers in units of 2^-45 of the first's weight, so
+ * results do not depend on the order of summation. */
+typedef struct {
+    const float *temperature; /* [T] device, or NULL: 1 */
+    const int32_t *top_k;     /* [T] device, or NULL: off */
+    const float *top_p;       /* [T] device, or NULL: off */
+    const float *min_p;       /* [T] device, or NULL: off */
+} moe_sampling;
+
+/* Workspace bytes of sample_tokens and accept_drafts for T rows of V logits;
+ * 0 for invalid input. */
+size_t sample_workspace_bytes(int32_t T, int32_t V);
+
+/* One draw per row: a draft step, or a step without drafts.
+ *   logits [T, V] in dtype MOE_F32 or MOE_BF16, rows `stride` elements apart
+ *   f      (host) filters, or NULL: none, temperature 1
+ *   u      [T] f32 in [0, 1) (device)
+ *   token  [T] i32 out;  prob [T] f32 out or NULL: the token's probability
+ *          (0 with token -1; the draft confidence that select_drafts,
+ *          expand_drafts and gate_depths take)
+ *   probs  [T, V] f32 out (dense) or NULL: the whole distribution (the
+ *          draft_probs of accept_drafts)
+ *   ws     256-byte aligned, sample_workspace_bytes bytes, no initialisation
+ * Limits: 0 <= T <= 65535, 1 <= V <= 2^18. */
+int sample_tokens(const void *logits, int64_t stride, int32_t T, int32_t V, int32_t dtype, const moe_sampling *f,
+                  const float *u, int32_t *token, float *prob, float *probs, void *ws, size_t ws_bytes,
+                  void *stream);
+
+/* Acceptance of drafts from the target's logits.  The rows of a call are
+ * grouped by sequence (seg_off as in moe_kv4_rows); row 0 of a sequence is
+ * its root (the last token that stands already), the others are drafts.
+ * logits[t] are the target's for the token after row t.
+ *   tokens [T] i32 (device): token of each row (roots' are not read)
+ *   parent (host) [T] as in kv4_attend, or NULL: chains
+ *   draft_probs NULL: the target draws after each row with u[t]; from the
+ *          root on, a child holding the drawn token (of equal ones the
+ *          first) is accepted, until none does, and that draw is the last
+ *          token.
+ *   draft_probs [T, V] f32 (device, dense), chains only: row t is the
+ *          distribution that the draft after row t was drawn from (not read
+ *          for a sequence's last row).  The draft x is accepted if
+ *          u[t] * q(x) < p(x); at the first that is not, the last token is
+ *          drawn with u_final[s] from max(p - q, 0) (from p if that is zero
+ *          everywhere), after the last draft from p.
+ *   u      [T] f32, u_final [nseq] f32 in [0, 1) (device; u_final only with
+ *          draft_probs, else NULL)
+ *   count  [nseq] i32 out: tokens that the sequence gains, accepted drafts
+ *          + 1 (0 for a sequence without rows)
+ *   out    [T] i32 out: the gained tokens of sequence s from seg_off[s] on,
+ *          then -1
+ *   path   [T] i32 out: the rows (inside the sequence) whose K/V are to be
+ *          kept, the root first: count[s] entries from seg_off[s] on, then -1
+ * Limits: 1 <= T <= MOE_MAX_TOKENS, 1 <= V <= 2^18. */
+int accept_drafts(const void *logits, int64_t stride, int32_t T, int32_t V, int32_t dtype, const moe_sampling *f,
+                  const int32_t *tokens, int32_t nseq, const int32_t *seg_off, const int32_t *parent,
+                  const float *draft_probs, const float *u, const float *u_final, int32_t *out, int32_t *path,
+                  int32_t *count, void *ws, size_t ws_bytes, void *stream);
+
 /* Message for the calling thread's last non-zero return ("" if none). */
 const char *moe_last_error(void);
 

@@ -15,6 +15,12 @@ Entry points (same names as the C ABI in include/moe_verify.h):
   union_stats_segments(topk_idx, E, offsets) -> (per, total)
   gate_depths(c, Epred, t_base, t_exp) -> d
   workspace_bytes(layer, T, bias=None)
+  kv4_cache(num_pages, page, Hkv, D)  -> KV4Cache
+  kv4_append(cache, k, v, table, lengths, offsets, path=None, count=None, return_stored=False)
+  kv4_attend(cache, q, table, lengths, offsets, parent=None, scale=None) -> out
+  sample_tokens(logits, u, temperature, top_k, top_p, min_p, return_probs=False) -> (token, prob, probs)
+  accept_drafts(logits, tokens, offsets, u, parent=None, draft_probs=None, u_final=None, ...)
+                                      -> (out, path, count)
 """
 from __future__ import annotations
 
@@ -35,9 +41,11 @@ MAX_SEGMENTS = 64
 STAGE_NAMES = ("router", "route", "gate_up", "down", "combine")
 EXPORTED = ("moe_pack_weights", "moe_verify_workspace_bytes", "moe_verify_layer", "union_stats",
             "select_drafts", "select_drafts_static", "expand_drafts", "union_stats_segments", "gate_depths",
-            "moe_stream_read", "moe_last_error", "moe_verify_layer_noalloc")
+            "moe_stream_read", "moe_last_error", "moe_verify_layer_noalloc", "kv4_cache_bytes", "kv4_append",
+            "kv4_attend_workspace_bytes", "kv4_attend", "sample_workspace_bytes", "sample_tokens", "accept_drafts")
 
 _vp, _i32, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float
+_i64, _size = ctypes.c_int64, ctypes.c_size_t
 
 
 class _Layer(ctypes.Structure):
@@ -54,6 +62,18 @@ class _Aux(ctypes.Structure):
     _fields_ = [("logits", _vp), ("topk_idx", _vp), ("topk_w", _vp), ("union_size", _vp),
                 ("union_experts", _vp), ("csr_ptr", _vp), ("csr_tok", _vp), ("csr_w", _vp),
                 ("pstar", _vp), ("pstar_size", _vp), ("events", _vp)]
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [("data", _vp), ("num_pages", _i32), ("page", _i32), ("Hkv", _i32), ("D", _i32)]
+
+
+class _KvRows(ctypes.Structure):
+    _fields_ = [("table", _vp), ("max_pages", _i32), ("len", _vp), ("nseq", _i32), ("seg_off", _vp)]
+
+
+class _Sampling(ctypes.Structure):
+    _fields_ = [("temperature", _vp), ("top_k", _vp), ("top_p", _vp), ("min_p", _vp)]
 
 
 _lib = None
@@ -91,6 +111,22 @@ def lib() -> ctypes.CDLL:
         L.moe_pack_weights.restype = ctypes.c_int
         L.moe_stream_read.argtypes = [_vp, ctypes.c_size_t, _vp, _vp]
         L.moe_stream_read.restype = ctypes.c_int
+        cp, rp, fp = ctypes.POINTER(_KvCache), ctypes.POINTER(_KvRows), ctypes.POINTER(_Sampling)
+        L.kv4_cache_bytes.argtypes = [_i32, _i32, _i32, _i32]
+        L.kv4_cache_bytes.restype = _size
+        L.kv4_append.argtypes = [cp, rp, _vp, _vp, _i64, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp]
+        L.kv4_append.restype = ctypes.c_int
+        L.kv4_attend_workspace_bytes.argtypes = [cp, rp, _i32, _i32, _i32]
+        L.kv4_attend_workspace_bytes.restype = _size
+        L.kv4_attend.argtypes = [cp, rp, _vp, _i64, _i32, _i32, _i32, _f32, _vp, _vp, _vp, _size, _vp]
+        L.kv4_attend.restype = ctypes.c_int
+        L.sample_workspace_bytes.argtypes = [_i32, _i32]
+        L.sample_workspace_bytes.restype = _size
+        L.sample_tokens.argtypes = [_vp, _i64, _i32, _i32, _i32, fp, _vp, _vp, _vp, _vp, _vp, _size, _vp]
+        L.sample_tokens.restype = ctypes.c_int
+        L.accept_drafts.argtypes = [_vp, _i64, _i32, _i32, _i32, fp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                    _vp, _size, _vp]
+        L.accept_drafts.restype = ctypes.c_int
         L.moe_last_error.argtypes = []
         L.moe_last_error.restype = ctypes.c_char_p
         _lib = L
@@ -616,3 +652,281 @@ def gate_depths(c, Epred, t_base: float, t_exp: float, stream=None):
     _check(lib().gate_depths(c.data_ptr(), Epred.data_ptr(), S, D1 - 1, int(Epred.shape[2]), t_base, t_exp,
                              d.data_ptr(), s))
     return d
+
+
+# ---------------------------------------------------------------------------
+# Serving operators: the 4-bit K/V cache, drawing and accepting draft tokens
+# ---------------------------------------------------------------------------
+def _int_array(values, n: Optional[int] = None, name: str = "offsets"):
+    """Host int32 array of a sequence of ints (read by the C side during the call)."""
+    if hasattr(values, "tolist"):
+        if hasattr(values, "device") and values.device.type != "cpu":
+            raise ValueError(f"{name} is read on the host: give a list, an array or a CPU tensor")
+        values = values.tolist()
+    if n is not None and len(values) != n:
+        raise ValueError(f"{name} must have {n} entries, got {len(values)}")
+    return (ctypes.c_int32 * len(values))(*values)
+
+
+def _dense(t, name: str, dtype, shape, device) -> None:
+    """_check_tensor for one torch dtype, without building names on the way."""
+    if getattr(t, "dtype", None) != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+        _check_tensor(t, name, (str(dtype).replace("torch.", ""),), shape=shape, device=device)
+
+
+def _rows_dtype(t, name: str, dims: int):
+    """MOE_F32 / MOE_BF16 of a device tensor [T, ...] whose rows are dense,
+    and the elements between rows (size-1 dimensions have no stride)."""
+    import torch
+    if getattr(t, "dtype", None) not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{name} must be a float32 or bfloat16 tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a device tensor, got {t.device}")
+    row = 1
+    for d in range(dims - 1, 0, -1):
+        if t.shape[d] != 1 and t.stride(d) != row:
+            raise ValueError(f"{name} must have dense rows; only the distance between rows is free")
+        row *= t.shape[d]
+    stride = t.stride(0) if t.shape[0] > 1 else row
+    if stride < row:
+        raise ValueError(f"{name} has overlapping rows")
+    return MOE_F32 if t.dtype == torch.float32 else MOE_BF16, stride
+
+
+class _on_device:
+    """Makes `device` current during a launch, as torch's own operators do."""
+
+    def __init__(self, device):
+        import torch
+        self.guard = torch.cuda.device(device) if torch.cuda.current_device() != device.index else None
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *a):
+        if self.guard is not None:
+            self.guard.__exit__(*a)
+
+
+def _aligned_ws(nbytes: int, device):
+    import torch
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+@dataclass
+class KV4Cache:
+    """A pool of K/V pages held in 4 bits (layout in include/moe_verify.h):
+    data is a contiguous uint8 device tensor of num_pages * Hkv * page / 16 *
+    17 D bytes, of any shape.  One per layer; page tables and lengths are
+    common to the layers."""
+    data: object
+    page: int
+    Hkv: int
+    D: int
+
+    @property
+    def page_bytes(self) -> int:
+        return self.Hkv * (self.page // 16) * 17 * self.D
+
+    @property
+    def num_pages(self) -> int:
+        return self.data.numel() // self.page_bytes
+
+    def _c(self, device) -> _KvCache:
+        import torch
+        d = self.data
+        if getattr(d, "dtype", None) != torch.uint8 or not d.is_contiguous() or d.device != device:
+            raise ValueError(f"cache.data must be a contiguous uint8 tensor on {device}")
+        if self.page < 16 or self.Hkv < 1 or self.D < 32:
+            raise ValueError(f"cache sizes page={self.page}, Hkv={self.Hkv}, D={self.D} are not a cache's")
+        if d.numel() == 0 or d.numel() % self.page_bytes:
+            raise ValueError(f"cache.data has {d.numel()} bytes, pages have {self.page_bytes}")
+        return _KvCache(d.data_ptr(), self.num_pages, self.page, self.Hkv, self.D)
+
+
+def kv4_cache(num_pages: int, page: int, Hkv: int, D: int, device=None) -> KV4Cache:
+    """Allocate a cache of num_pages pages (uninitialised)."""
+    import torch
+    n = lib().kv4_cache_bytes(num_pages, page, Hkv, D)
+    if n == 0:
+        raise MoeError(-1, lib().moe_last_error().decode())
+    data = torch.empty((num_pages, Hkv, page // 16, 17 * D), dtype=torch.uint8, device=device or "cuda")
+    return KV4Cache(data=data, page=page, Hkv=Hkv, D=D)
+
+
+def _kv_rows(table, lengths, offsets, device):
+    import torch
+    if getattr(table, "dtype", None) != torch.int32 or table.dim() != 2 or not table.is_contiguous() or table.device != device:
+        raise ValueError(f"table must be a contiguous int32 [nseq, max_pages] tensor on {device}")
+    n = int(table.shape[0])
+    off = _int_array(offsets, n + 1)
+    _dense(lengths, "lengths", torch.int32, (n,), device)
+    r = _KvRows(table.data_ptr(), int(table.shape[1]), lengths.data_ptr(), n, ctypes.addressof(off))
+    r._keep = off
+    return r, n
+
+
+def kv4_append(cache: KV4Cache, k, v, table, lengths, offsets, *, path=None, count=None, return_stored: bool = False,
+               stream=None):
+    """Quantise rows k, v [T, Hkv, D] (float32 or bfloat16; slices of a fused
+    projection may keep their distance between tokens) into the cache.  The
+    call's rows are grouped by sequence: offsets (host) [nseq + 1]; row j of
+    sequence s goes to position lengths[s] + j, page table[s].  table [nseq,
+    max_pages] and lengths [nseq] are int32 device tensors.
+
+    path [T], count [nseq] (int32, device; accept_drafts' results): write
+    only the accepted rows, row path[offsets[s] + i] to position lengths[s] +
+    i for i < count[s].  return_stored: the values that the codes stand for,
+    (k, v) [T, Hkv, D]; else None."""
+    import torch
+    dtype, ks = _rows_dtype(k, "k", 3)
+    vt, vs = _rows_dtype(v, "v", 3)
+    dev, T = k.device, int(k.shape[0])
+    c = cache._c(dev)
+    if tuple(k.shape[1:]) != (cache.Hkv, cache.D) or v.shape != k.shape or vt != dtype or v.device != dev:
+        raise ValueError(f"k and v must be [T, {cache.Hkv}, {cache.D}] tensors of one type and device")
+    r, n = _kv_rows(table, lengths, offsets, dev)
+    if (path is None) != (count is None):
+        raise ValueError("path and count come together")
+    if path is not None:
+        _dense(path, "path", torch.int32, (T,), dev)
+        _dense(count, "count", torch.int32, (n,), dev)
+        if return_stored:
+            raise ValueError("return_stored is for whole calls, without path")
+    out = [torch.empty((T, cache.Hkv, cache.D), dtype=k.dtype, device=dev) for _ in range(2)] if return_stored else [None, None]
+    with _on_device(dev):
+        s = _launch_stream(stream, dev, out)
+        _check(lib().kv4_append(ctypes.byref(c), ctypes.byref(r), k.data_ptr(), v.data_ptr(), ks, vs, T, dtype, _ptr(path),
+                                _ptr(count), _ptr(out[0]), _ptr(out[1]), s))
+    return tuple(out) if return_stored else None
+
+
+def kv4_attend(cache: KV4Cache, q, table, lengths, offsets, *, parent=None, scale: Optional[float] = None, out=None,
+               workspace=None, stream=None):
+    """Attention of the verified tokens q [T, Hq, D] (float32 or bfloat16)
+    over the cache, in which their own rows are already (kv4_append with the
+    same table, lengths and offsets).  A token sees its sequence's rows before
+    the call, itself and its ancestors: parent (host) [T] inside the sequence,
+    -1 for its first row; None for chains.  scale: default D ** -0.5.
+    Returns out [T, Hq, D] in q's type.  workspace: a uint8 device tensor of
+    kv4_attend_workspace_bytes, one per stream; None allocates."""
+    import torch
+    dtype, qs = _rows_dtype(q, "q", 3)
+    dev, T, Hq = q.device, int(q.shape[0]), int(q.shape[1])
+    if q.shape[2] != cache.D:
+        raise ValueError(f"q must be [T, Hq, {cache.D}]")
+    c = cache._c(dev)
+    r, _ = _kv_rows(table, lengths, offsets, dev)
+    par = None if parent is None else _int_array(parent, T, "parent")
+    L = lib()
+    with _on_device(dev):
+        need = L.kv4_attend_workspace_bytes(ctypes.byref(c), ctypes.byref(r), T, Hq, dtype)
+        if need == 0:
+            raise MoeError(-1, L.moe_last_error().decode())
+        owned = []
+        if workspace is None:
+            workspace = _aligned_ws(need, dev)
+            owned.append(workspace)
+        else:
+            _check_tensor(workspace, "workspace", ("uint8",), numel=need, device=dev, at_least=True)
+        if out is None:
+            out = torch.empty((T, Hq, cache.D), dtype=q.dtype, device=dev)
+            owned.append(out)
+        else:
+            _dense(out, "out", q.dtype, tuple(q.shape), dev)
+        s = _launch_stream(stream, dev, owned)
+        _check(L.kv4_attend(ctypes.byref(c), ctypes.byref(r), q.data_ptr(), qs, T, Hq, dtype,
+                            cache.D ** -0.5 if scale is None else scale,
+                            None if par is None else ctypes.addressof(par), out.data_ptr(), workspace.data_ptr(),
+                            workspace.numel(), s))
+    return out
+
+
+def _filters(T: int, dev, temperature, top_k, top_p, min_p) -> _Sampling:
+    import torch
+    for name, t, d in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
+                       ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+        if t is not None:
+            _dense(t, name, d, (T,), dev)
+    return _Sampling(_ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p))
+
+
+def _sampling_ws(T: int, V: int, dev, workspace, owned):
+    need = lib().sample_workspace_bytes(T, V)
+    if need == 0:
+        raise MoeError(-1, lib().moe_last_error().decode())
+    if workspace is None:
+        workspace = _aligned_ws(need, dev)
+        owned.append(workspace)
+    else:
+        _check_tensor(workspace, "workspace", ("uint8",), numel=need, device=dev, at_least=True)
+    return workspace
+
+
+def sample_tokens(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None, return_probs: bool = False,
+                  workspace=None, stream=None):
+    """Draw one token per row of logits [T, V] (float32 or bfloat16, rows may
+    be further apart) with the numbers u [T] float32 in [0, 1).  temperature,
+    top_p, min_p [T] float32 and top_k [T] int32 are device tensors, None for
+    off (include/moe_verify.h defines the filters).  Returns (token [T]
+    int32, prob [T] float32, probs [T, V] float32 or None): the drawn token,
+    its probability, and with return_probs the whole filtered distribution."""
+    import torch
+    dtype, stride = _rows_dtype(logits, "logits", 2)
+    dev, T, V = logits.device, int(logits.shape[0]), int(logits.shape[1])
+    _dense(u, "u", torch.float32, (T,), dev)
+    f = _filters(T, dev, temperature, top_k, top_p, min_p)
+    token = torch.empty(T, dtype=torch.int32, device=dev)
+    prob = torch.empty(T, dtype=torch.float32, device=dev)
+    probs = torch.empty((T, V), dtype=torch.float32, device=dev) if return_probs else None
+    owned = [token, prob, probs]
+    ws = _sampling_ws(T, V, dev, workspace, owned)
+    with _on_device(dev):
+        s = _launch_stream(stream, dev, owned)
+        _check(lib().sample_tokens(logits.data_ptr(), stride, T, V, dtype, ctypes.byref(f), u.data_ptr(), token.data_ptr(),
+                                   prob.data_ptr(), _ptr(probs), ws.data_ptr(), ws.numel(), s))
+    return token, prob, probs
+
+
+def accept_drafts(logits, tokens, offsets, u, *, parent=None, draft_probs=None, u_final=None, temperature=None, top_k=None,
+                  top_p=None, min_p=None, workspace=None, stream=None):
+    """Accept drafts from the target's logits [T, V] for the verified tokens
+    [T] int32, grouped by sequence: offsets (host) [nseq + 1], row 0 of a
+    sequence its root.  parent (host) [T] makes the drafts of a sequence a
+    tree, None a chain.  Without draft_probs a draft is accepted where it
+    equals the target's own draw (numbers u [T]); with draft_probs [T, V]
+    float32 (chains) by the ratio of the two distributions, the last token
+    drawn with u_final [nseq].  Filters as in sample_tokens.  Returns (out [T]
+    int32: the gained tokens of each sequence from its offset on, path [T]
+    int32: the rows to keep, count [nseq] int32: how many)."""
+    import torch
+    dtype, stride = _rows_dtype(logits, "logits", 2)
+    dev, T, V = logits.device, int(logits.shape[0]), int(logits.shape[1])
+    _dense(tokens, "tokens", torch.int32, (T,), dev)
+    _dense(u, "u", torch.float32, (T,), dev)
+    off = _int_array(offsets)
+    n = len(off) - 1
+    if n < 1:
+        raise ValueError("offsets must have at least 2 entries")
+    par = None if parent is None else _int_array(parent, T, "parent")
+    if (draft_probs is None) != (u_final is None):
+        raise ValueError("draft_probs and u_final come together")
+    if draft_probs is not None:
+        _dense(draft_probs, "draft_probs", torch.float32, (T, V), dev)
+        _dense(u_final, "u_final", torch.float32, (n,), dev)
+    f = _filters(T, dev, temperature, top_k, top_p, min_p)
+    out = torch.empty(T, dtype=torch.int32, device=dev)
+    path = torch.empty(T, dtype=torch.int32, device=dev)
+    count = torch.empty(n, dtype=torch.int32, device=dev)
+    owned = [out, path, count]
+    ws = _sampling_ws(T, V, dev, workspace, owned)
+    with _on_device(dev):
+        s = _launch_stream(stream, dev, owned)
+        _check(lib().accept_drafts(logits.data_ptr(), stride, T, V, dtype, ctypes.byref(f), tokens.data_ptr(), n,
+                                   ctypes.addressof(off), None if par is None else ctypes.addressof(par), _ptr(draft_probs),
+                                   u.data_ptr(), _ptr(u_final), out.data_ptr(), path.data_ptr(), count.data_ptr(),
+                                   ws.data_ptr(), ws.numel(), s))
+    return out, path, count

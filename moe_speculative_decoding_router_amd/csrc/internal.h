@@ -110,8 +110,10 @@ hipError_t launch_gate_depths(const float *c, const uint32_t *Ep, int S, int Dma
                               float t_exp, int32_t *d, hipStream_t s);
 
 // Host helpers of the C ABI (moe_verify.cpp): the error message of the
-// calling thread, and the validation plus workspace size of a verify call.
+// calling thread, the current device's size, and the validation plus
+// workspace size of a verify call.
 int set_error(int code, const char *msg);
+int device_cu_count();  // compute units of the current device
 int verify_needs(const ::moe_layer *layer, int T, const ::moe_bias *bias, size_t *need);
 
 // Limits used by the kernels.

@@ -168,6 +168,8 @@ namespace moe {
 
 int set_error(int code, const char *msg) { return fail(code, "%s", msg); }
 
+int device_cu_count() { return cu_count(); }
+
 int verify_needs(const moe_layer *layer, int T, const moe_bias *bias, size_t *need) {
     const int rc = validate_layer(layer, T, bias);
     if (rc != MOE_OK) return rc;

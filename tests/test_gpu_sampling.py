@@ -1,0 +1,288 @@
+"""sample_tokens and accept_drafts against the float64 oracle.
+
+Tokens must be equal.  The kernels sum weights in units of 2^-45 of the
+largest, so a running sum is off by at most V 2^-46 of the first weight;
+a draw whose number lies nearer than that to a step may fall on either side,
+and `margin` asserts that no seeded draw here does.  Probabilities are
+computed in float64 and rounded once: 2^-24 relative, and V 2^-46 for the sum."""
+import numpy as np
+import pytest
+
+from oracle import sampling as osa
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+import moe_speculative_decoding_router_amd as m  # noqa: E402
+
+DEV = torch.device("cuda:0")
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+
+
+def logits_of(rng, T, V, dtype, scale=2.0, steep=1.3, stride=None):
+    x = 5 + scale * rng.normal(size=(T, V)) - steep * np.log1p(V * rng.random((T, V)))
+    big = torch.zeros((T, stride or V))
+    big[:, :V] = torch.from_numpy(x.astype(np.float32))
+    xd = big.to(DT[dtype]).to(DEV)[:, :V]
+    return xd.double().cpu().numpy(), xd
+
+
+def host(t, T, off):
+    return [off] * T if t is None else t.tolist()
+
+
+def check(x, xd, u, temperature=None, top_k=None, top_p=None, min_p=None, probs=True):
+    T, V = x.shape
+    args = [None if a is None else dev(np.asarray(a, dtype=d)) for a, d in
+            ((temperature, np.float32), (top_k, np.int32), (top_p, np.float32), (min_p, np.float32))]
+    ud = dev(np.asarray(u, dtype=np.float32))
+    tok, prob, full = m.sample_tokens(xd, ud, temperature=args[0], top_k=args[1], top_p=args[2], min_p=args[3],
+                                      return_probs=probs)
+    tok, prob = tok.cpu().numpy(), prob.cpu().numpy()
+    t, k, p, mp = (host(a, T, o) for a, o in zip(args, (1.0, 0, 1.0, 0.0)))
+    un = ud.double().cpu().numpy()
+    for i in range(T):
+        w, n = osa.kept_weights(x[i], t[i], k[i], p[i], mp[i])
+        ref = osa.draw(w, un[i])
+        if n == 0:
+            assert tok[i] == -1 and prob[i] == 0
+            assert not probs or (full[i] == 0).all()
+            continue
+        assert tok[i] == ref, (i, tok[i], ref, n, osa.margin(w, un[i]))
+        q = w / w.sum()
+        assert abs(prob[i] - q[ref]) <= (2.0 ** -24 + V * 2.0 ** -46) * q[ref]
+        if probs:
+            got = full[i].double().cpu().numpy()
+            assert (np.abs(got - q) <= (2.0 ** -24 + V * 2.0 ** -46) * q + 2.0 ** -149).all()
+    return tok
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [1, 2, 63, 64, 65, 1000, 4097, 20011])
+def test_mixed_filters(V, dtype):
+    rng = np.random.default_rng(V)
+    T = 24
+    x, xd = logits_of(rng, T, V, dtype)
+    check(x, xd, rng.random(T), rng.choice([0.3, 0.7, 1.0, 2.5], T), rng.choice([0, 1, 5, 50, 900, 10 ** 6], T),
+          rng.choice([0.0, 0.3, 0.9, 0.99, 1.0], T), rng.choice([0.0, 0.02, 0.3, 1.0], T))
+
+
+@pytest.mark.parametrize("kw", [{}, {"temperature": 0.8}, {"top_k": 40}, {"top_p": 0.9}, {"min_p": 0.05},
+                                {"top_k": 6000, "top_p": 0.999}, {"top_p": 0.99999, "temperature": 3.0}])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_one_filter_large(kw, dtype):
+    rng = np.random.default_rng(len(kw) + len(dtype))
+    T, V = 5, 100003
+    x, xd = logits_of(rng, T, V, dtype, stride=V + 7)
+    check(x, xd, rng.random(T), **{k: [v] * T for k, v in kw.items()})
+
+
+def test_largest_vocabulary_and_many_rows():
+    rng = np.random.default_rng(1)
+    x, xd = logits_of(rng, 2, 1 << 18, "f32")
+    check(x, xd, rng.random(2), top_p=[0.95, 0.2])
+    x, xd = logits_of(rng, 700, 300, "f32")
+    check(x, xd, rng.random(700), top_p=[0.8] * 700, probs=False)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_ties(dtype):
+    """Equal values: the lower index is ranked first, whole rows of one value included."""
+    rng = np.random.default_rng(3)
+    V, T = 9001, 12
+    x = rng.integers(-3, 4, size=(T, V)).astype(np.float64)
+    x[:4] = 1.5
+    x[4, ::2] = -0.0
+    xd = dev(x.astype(np.float32)).to(DT[dtype])
+    u = rng.random(T)
+    check(x, xd, u, top_k=[1, 2, 100, 9000, 7000, 3000, 1, 50, 500, 5000, 8999, 9001])
+    check(x, xd, u, top_p=[0.1, 0.5, 0.99999, 1.0] * 3)
+    check(x, xd, u, top_k=[4000] * T, top_p=[0.5] * T)
+    # equal weights: the steps are exact, and u on a step belongs to the next token
+    four = np.zeros((5, 4))
+    assert check(four, dev(four.astype(np.float32)), [0.0, 0.25, 0.5, 0.75, 1 - 2.0 ** -24]).tolist() == [0, 1, 2, 3, 3]
+    assert check(four, dev(four.astype(np.float32)), [0.0, 0.49, 0.5, 0.75, 0.9], top_k=[2] * 5).tolist() == [0, 0, 1, 1, 1]
+    assert check(four, dev(four.astype(np.float32)), [0.9] * 5, top_p=[0.25, 0.26, 0.5, 0.75, 1.0]).tolist() == [0, 1, 1, 2, 3]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_masked_rows(dtype):
+    rng = np.random.default_rng(4)
+    V, T = 5003, 10
+    x = rng.normal(size=(T, V)) * 3
+    x[0] = -np.inf
+    x[1] = -np.inf
+    x[1, 4321] = -7.0
+    x[2, rng.random(V) < 0.99] = -np.inf
+    x[3] = np.nan
+    x[4, 100] = np.inf
+    x[5, [7, 4000]] = np.inf
+    x[6, ::3] = np.nan
+    x[7] = -3.3895313892515355e38              # the lowest finite value of both types
+    x[8, 1:] = -3.3895313892515355e38
+    x[9, 0], x[9, 1] = 3.3895313892515355e38, -3.3895313892515355e38
+    xd = dev(x.astype(np.float32)).to(DT[dtype])
+    x = xd.double().cpu().numpy()
+    u = rng.random(T)
+    for kw in ({}, {"top_k": 3}, {"top_p": 0.9}, {"top_k": 10, "top_p": 0.7, "min_p": 0.1}, {"temperature": 0.0}):
+        check(x, xd, u, **{k: [v] * T for k, v in kw.items()})
+
+
+def test_temperatures_and_edges_of_the_filters():
+    rng = np.random.default_rng(5)
+    V = 3001
+    x, xd = logits_of(rng, 8, V, "f32")
+    u = rng.random(8)
+    check(x, xd, u, temperature=[0.0, -1.0, 1e-30, 1e-3, 50.0, 1e30, 1.0, 1.0])
+    check(x, xd, u, top_p=[0.0, -1.0, 1.0, 2.0, 1e-30, 1 - 2.0 ** -24, 0.5, 0.5])
+    check(x, xd, u, min_p=[0.0, -1.0, 1.0, 2.0, 1e-30, 0.5, 0.9, 1e-3])
+    check(x, xd, u, top_k=[0, -5, 1, 2, V - 1, V, V + 1, 2 ** 31 - 1])
+    top = x.argmax(1)
+    assert (check(x, xd, u, temperature=[0.0] * 8, top_p=[0.5] * 8) == top).all()
+    # numbers outside [0, 1) stay inside the row
+    for bad in (1.0, 2.0, -1.0, np.nan, np.inf):
+        tok = m.sample_tokens(xd, dev(np.full(8, bad, dtype=np.float32)))[0]
+        assert ((tok >= 0) & (tok < V)).all()
+
+
+def test_no_rows():
+    tok, prob, probs = m.sample_tokens(torch.empty((0, 100), device=DEV), torch.empty(0, device=DEV), return_probs=True)
+    assert tok.shape == (0,) and prob.shape == (0,) and probs.shape == (0, 100)
+
+
+# ---------------------------------------------------------------------------
+# Acceptance
+# ---------------------------------------------------------------------------
+def expect(results, offsets, T):
+    out, path, count = np.full(T, -1), np.full(T, -1), np.zeros(len(offsets) - 1, dtype=int)
+    for s, r in enumerate(results):
+        if r is None:
+            continue
+        o, p = r
+        count[s] = len(o)
+        out[offsets[s]:offsets[s] + len(o)] = o
+        path[offsets[s]:offsets[s] + len(p)] = p
+    return out, path, count
+
+
+def compare(got, want):
+    for g, w in zip(got, want):
+        assert np.array_equal(g.cpu().numpy(), w), (g.cpu().numpy(), w)
+
+
+@pytest.mark.parametrize("dtype,V", [("f32", 50), ("bf16", 4099), ("f32", 60001)])
+@pytest.mark.parametrize("kind", ["chain", "tree"])
+def test_accept_by_match(dtype, V, kind):
+    rng = np.random.default_rng(V)
+    counts = [5, 0, 1, 15, 7, 2, 30, 4]
+    offsets = [0] + [int(c) for c in np.cumsum(counts)]
+    T = offsets[-1]
+    x, xd = logits_of(rng, T, V, dtype, scale=1.0, steep=1.5)
+    u = rng.random(T).astype(np.float32)
+    parent, tokens = [], np.zeros(T, dtype=np.int32)
+    temp, topp = np.full(T, 0.7, dtype=np.float32), np.full(T, 0.9, dtype=np.float32)
+    drawn = np.array([osa.draw(osa.kept_weights(x[t], temp[t], 0, topp[t])[0], float(u[t])) for t in range(T)])
+    for s, n in enumerate(counts):
+        par = [-1] + [int(rng.integers(0, j)) if kind == "tree" else j - 1 for j in range(1, n)] if n else []
+        parent += par
+        for j in range(1, n):    # most drafts hit, some miss, some repeat a sibling
+            hit = drawn[offsets[s] + par[j]]
+            tokens[offsets[s] + j] = hit if rng.random() < 0.8 else int(rng.integers(0, V))
+    res = [osa.accept_match(drawn[a:b], tokens[a:b], parent[a:b]) if b > a else None for a, b in zip(offsets, offsets[1:])]
+    got = m.accept_drafts(xd, dev(tokens), offsets, dev(u), parent=parent if kind == "tree" else None,
+                          temperature=dev(temp), top_p=dev(topp))
+    compare(got, expect(res, offsets, T))
+    assert max(len(r[0]) for r in res if r) > 2     # something was accepted
+
+
+@pytest.mark.parametrize("dtype,V", [("f32", 40), ("bf16", 5001), ("f32", 80021)])
+@pytest.mark.parametrize("filtered", [False, True])
+def test_accept_by_ratio(dtype, V, filtered):
+    rng = np.random.default_rng(V + filtered)
+    counts = [5, 1, 0, 9, 2, 6, 6, 6, 6, 3]
+    offsets = [0] + [int(c) for c in np.cumsum(counts)]
+    T = offsets[-1]
+    x, xd = logits_of(rng, T, V, dtype)
+    y = x + 0.6 * rng.normal(size=x.shape)
+    q = np.exp(y - y.max(1, keepdims=True))
+    q = (q / q.sum(1, keepdims=True)).astype(np.float32)
+    u, uf = rng.random(T).astype(np.float32), rng.random(len(counts)).astype(np.float32)
+    tokens = np.zeros(T, dtype=np.int32)
+    for s, n in enumerate(counts):
+        for j in range(1, n):
+            t = offsets[s] + j
+            tokens[t] = rng.choice(V, p=q[t - 1].astype(np.float64) / q[t - 1].astype(np.float64).sum())
+    q[offsets[5]:offsets[6]] = 0.0                                  # a drafter without mass: p alone decides
+    tokens[offsets[7] + 1], tokens[offsets[8] + 2] = V, -1          # drafts outside the vocabulary are rejected
+    kw = dict(top_k=np.full(T, 200, dtype=np.int32), top_p=np.full(T, 0.95, dtype=np.float32)) if filtered else {}
+    w = [osa.kept_weights(x[t], 1.0, 200 if filtered else 0, float(np.float32(0.95)) if filtered else 1.0)[0] for t in range(T)]
+    p = np.array([a / a.sum() for a in w])
+    res = [osa.accept_chain(p[a:b], q[a:b].astype(np.float64), tokens[a:b], u[a:b].astype(np.float64), float(uf[s]))
+           if b > a else None for s, (a, b) in enumerate(zip(offsets, offsets[1:]))]
+    got = m.accept_drafts(xd, dev(tokens), offsets, dev(u), draft_probs=dev(q), u_final=dev(uf),
+                          **{k: dev(v) for k, v in kw.items()})
+    compare(got, expect(res, offsets, T))
+
+
+def test_accept_equal_distributions_and_masked_rows():
+    """q = p accepts everything; rows without tokens give -1 and accept nothing."""
+    rng = np.random.default_rng(6)
+    V, n = 700, 6
+    x, xd = logits_of(rng, n, V, "f32")
+    q = m.sample_tokens(xd, torch.zeros(n, device=DEV), return_probs=True)[2]
+    tokens = dev(np.array([0] + [int(q[t].argmax()) for t in range(n - 1)], dtype=np.int32))
+    u = dev(np.full(n, 0.999, dtype=np.float32))
+    out, path, count = m.accept_drafts(xd, tokens, [0, n], u, draft_probs=q, u_final=u[:1])
+    assert count.tolist() == [n] and path.tolist() == list(range(n)) and out[:n - 1].tolist() == tokens[1:].tolist()
+    xd[2] = -float("inf")
+    out, path, count = m.accept_drafts(xd, tokens, [0, n], u, draft_probs=q, u_final=u[:1])
+    assert count.tolist() == [3] and out.tolist() == tokens[1:3].tolist() + [-1] * 4
+    tokens[3] = -1
+    out, path, count = m.accept_drafts(xd, tokens, [0, n], u)
+    assert (out[count[0] - 1:] == -1).all() or count[0] < 3
+
+
+def test_captured_and_two_streams():
+    rng = np.random.default_rng(7)
+    V, offsets = 40009, [0, 5, 10]
+    x, xd = logits_of(rng, 10, V, "f32")
+    u, uf = dev(rng.random(10).astype(np.float32)), dev(rng.random(2).astype(np.float32))
+    topp = dev(np.full(10, 0.9, dtype=np.float32))
+    tokens = dev(rng.integers(0, V, 10).astype(np.int32))
+    ws = torch.empty(m.lib().sample_workspace_bytes(10, V), dtype=torch.uint8, device=DEV)
+
+    def step(w=None, st=None, x=xd):
+        tok, prob, q = m.sample_tokens(x, u, top_p=topp, return_probs=True, workspace=w, stream=st)
+        acc = m.accept_drafts(x, tokens, offsets, u, draft_probs=q, u_final=uf, top_p=topp, workspace=w, stream=st)
+        mat = m.accept_drafts(x, tok, offsets, u, top_p=topp, workspace=w, stream=st)
+        return (tok, prob, q) + acc + mat
+
+    step(ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step(ws)
+    for i in range(4):
+        xd.copy_(torch.roll(xd, 1, 0) * (1.1 - 0.1 * i))
+        u.copy_(torch.roll(u, 1))
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
+    other = xd.flip(0).contiguous()
+    want = [step(x=z) for z in (xd, other)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        both = [step(st=st, x=z) for z, st in zip((xd, other), streams)]
+        torch.cuda.synchronize()
+        for b, w in zip(both, want):
+            for p, q in zip(b, w):
+                assert torch.equal(p, q)
