@@ -7,17 +7,17 @@
 // are computed in float64 and summed as integers in units of 2^-45: a sum
 // does not depend on its order, and 2^18 weights of at most 1 fit 63 bits.
 //
-// A row is cut into chunks of consecutive tokens, a workgroup each.  Without
+// A row is cut into chunks of 4096 tokens, a workgroup each.  Without
 // filters two launches draw: part_kernel (each chunk's largest value and its
 // sum relative to it, one pass over the logits) and join_kernel (a workgroup
 // a row: the chunk that holds the draw, then the token).  With filters:
-//   max_kernel   the row's largest value
-//   hist_kernel  a histogram of the distance from it (1 / 32 nat a bin): the
-//                bins above which every token is kept, and the few that the
-//                thresholds lie in (top-k, top-p rows only)
-//   draw_kernel  sums of the kept, a list of the tokens in those few bins;
-//                the row's last workgroup sorts the list, fixes the threshold
-//                and draws
+//   max_kernel      the row's largest value
+//   hist_kernel     a histogram of the distance from it (1 / 32 nat a bin): the
+//                   bins above which every token is kept, and the few that
+//                   the thresholds lie in (top-k, top-p)
+//   gather_kernel   sums of the kept, a list of the tokens in those few bins
+//   resolve_kernel  a workgroup a row: sorts the list, fixes the threshold and
+//                   draws
 // A row whose list would be too long (flat or tied rows, large top-k with
 // distant tails) is resolved by a radix descent over the whole row instead.
 #include "common.h"
@@ -26,14 +26,15 @@
 namespace moe {
 namespace {
 
-constexpr int kRowThreads = 1024;
+constexpr int kThreads = 256;            // of the kernels with a workgroup a chunk
+constexpr int kRowThreads = 512;         // of those with a workgroup a row
+constexpr int kChunk = 4096;             // tokens
 constexpr int kRowWaves = kRowThreads / 64;
-constexpr int kTile = 4 * kRowThreads;  // tokens that a workgroup loads at once, 4 a thread
-constexpr int kMaxChunks = 64;          // of a row (2^18 tokens in tiles)
-constexpr int kBins = 1024;             // the last holds all that lies beyond
-constexpr int kList = 8192;             // tokens in the bins of the thresholds
+constexpr int kMaxChunks = 64;           // of a row of 2^18 tokens: a lane each
+constexpr int kBins = 1024;              // the last holds all that lies beyond
+constexpr int kList = 8192;              // tokens in the bins of the thresholds
 constexpr double kUnit = 35184372088832.0;         // 2^45
-constexpr double kUnitP = 1152921504606846976.0;   // 2^60, of probabilities (their sum is 1)
+constexpr double kUnitP = 2251799813685248.0;       // 2^51, of probabilities (their sum is 1)
 
 // What a row's filter comes to.
 struct RowState {
@@ -64,19 +65,22 @@ __device__ __forceinline__ unsigned key_of(float x) {
 
 __device__ __forceinline__ float of_key(unsigned k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
 
-// exp for arguments <= 0: 2^(j / 64) from a table of 64 in LDS, e^r of the
-// rest |r| <= ln 2 / 128 by its series to r^5 (the next term is 3e-17).
+// exp for arguments <= 0: 2^(j / 128) from a table in LDS and the exponent,
+// e^r of the rest |r| <= ln 2 / 256 by its series to r^4 (the next term is
+// 1e-15 of the result).  j comes out of the low bits of a sum with 1.5 2^52;
+// below -700 the result stays e^-700, which is 0 in every use.
 struct ExpTable {
-    double t[64];
-    __device__ void fill() {  // by the first wave; a barrier follows
-        if (threadIdx.x < 64) t[threadIdx.x] = exp2((double)threadIdx.x / 64.0);
+    double t[128];
+    __device__ void fill() {  // a barrier follows
+        if (threadIdx.x < 128) t[threadIdx.x] = exp2((double)threadIdx.x / 128.0);
     }
     __device__ __forceinline__ double operator()(double d) const {
-        const double j = rint(d * (64.0 * 1.4426950408889634074));
-        const double r = fma(j, -0.69314718055994530942 / 64.0, d);
-        const double e = fma(r, fma(r, fma(r, fma(r, fma(r, 1.0 / 120.0, 1.0 / 24.0), 1.0 / 6.0), 0.5), 1.0), 1.0);
-        const int i = (int)j;  // saturates; far arguments give 0
-        return ldexp(e * t[i & 63], i >> 6);
+        d = fmax(d, -700.0);
+        const double s = fma(d, 128.0 * 1.4426950408889634074, 6755399441055744.0);
+        const int i = (int)__double_as_longlong(s);
+        const double r = fma(s - 6755399441055744.0, -0.69314718055994530942 / 128.0, d);
+        const double e = fma(r, fma(r, fma(r, fma(r, 1.0 / 24.0, 1.0 / 6.0), 0.5), 1.0), 1.0) * t[i & 127];
+        return __longlong_as_double(__double_as_longlong(e) + ((long long)(i >> 7) << 52));
     }
 };
 
@@ -127,6 +131,7 @@ __device__ int pick(int V, F f, W want, uint64_t *sums, int *found, uint64_t *to
     if (threadIdx.x == 0) *found = -1;
     __syncthreads();
     uint64_t total = 0, before = 0;
+#pragma unroll
     for (int w = 0; w < kRowWaves; ++w) {
         if (w < wave) before += sums[w];
         total += sums[w];
@@ -192,17 +197,19 @@ __device__ void descend(const ExpTable &et, const void *row, int V, float first,
             atomicAdd(&h.mass[b], (unsigned long long)units(weight(et, x, first, invt)));
         }
         __syncthreads();
-        // thread t owns bins 2047 - 2t and 2046 - 2t, from the top
-        const int b0 = 2047 - 2 * tid;
-        const uint64_t c0 = h.cnt[b0], c1 = h.cnt[b0 - 1], m0 = h.mass[b0], m1 = h.mass[b0 - 1];
-        uint64_t ci = wave_scan_u64(c0 + c1), mi = wave_scan_u64(m0 + m1);
-        if (lane == 63) h.wcnt[wave] = ci, h.wsum[wave] = mi;
-        __syncthreads();
-        for (int w = 0; w < wave; ++w) ci += h.wcnt[w], mi += h.wsum[w];
-        uint64_t ca = above_cnt + ci - c0 - c1, ma = above_mass + mi - m0 - m1;
+        // thread t owns 4 bins, the first thread the highest
+        constexpr int kOwn = 2048 / kRowThreads;
+        const int b0 = 2047 - kOwn * tid;
+        uint64_t cs = 0, ms = 0;
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            const uint64_t c = y ? c1 : c0, m = y ? m1 : m0;
+        for (int y = 0; y < kOwn; ++y) cs += h.cnt[b0 - y], ms += h.mass[b0 - y];
+        uint64_t ca = above_cnt + wave_scan_u64(cs) - cs, ma = above_mass + wave_scan_u64(ms) - ms;
+        if (lane == 63) h.wcnt[wave] = ca + cs - above_cnt, h.wsum[wave] = ma + ms - above_mass;
+        __syncthreads();
+        for (int w = 0; w < wave; ++w) ca += h.wcnt[w], ma += h.wsum[w];
+#pragma unroll
+        for (int y = 0; y < kOwn; ++y) {
+            const uint64_t c = h.cnt[b0 - y], m = h.mass[b0 - y];
             const uint64_t lo = by_count ? ca : ma, hi = lo + (by_count ? c : m);
             if (lo < want && want <= hi) h.bin = b0 - y, h.above_cnt = ca, h.above_mass = ma;
             ca += c;
@@ -241,13 +248,13 @@ __device__ __forceinline__ Filter filter_of(const SampleArgs &a, int t) {
 
 // Counters of a row: workgroups done, list length.  Zeroed by the first kernel.
 struct Header {
-    int hist_done, draw_done, chain_done, listed;
+    int hist_done, chain_done, listed, pad;
 };
 
 // hist_kernel's result: bins below `sure` are kept, those up to `end` listed.
 struct Plan {
     int sure, end, slow, pad;
-    uint64_t above_cnt, above_mass, mass;  // of the sure bins, of all
+    uint64_t above_mass, mass;  // of the sure bins, of all
 };
 
 // Arrays of one batch of rows, C chunks each.
@@ -259,10 +266,12 @@ struct Work {
     uint64_t *sum;     // [rows][C]
     Header *head;      // [rows]
     Plan *plan;        // [rows]
-    uint64_t *list;    // [rows][kList] ~key, index
-    unsigned *hcnt;    // [rows][C][kBins]
-    uint64_t *hmass;   // [rows][C][kBins]
+    uint64_t *list;    // [rows][L] ~key, index
+    unsigned *hcnt;    // [rows][H][kBins]
+    uint64_t *hmass;   // [rows][H][kBins]
     int row0, C;
+    int E, H;          // chunks of a histogram, histograms of a row
+    int L;             // entries of a list, min(kList, V) at least
 };
 
 template <typename T>
@@ -295,16 +304,15 @@ __device__ __forceinline__ void load4(const void *row, int i, int V, float (&x)[
         if (F32) {
             const f32x4 v = *reinterpret_cast<const f32x4_any *>((const float *)row + i);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = clean(v[e]);
+            for (int e = 0; e < 4; ++e) x[e] = v[e];
         } else {
             const u32x2 v = *reinterpret_cast<const u32x2_any *>((const uint16_t *)row + i);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                x[e] = clean(__uint_as_float(e & 1 ? v[e >> 1] & 0xffff0000u : v[e >> 1] << 16));
+            for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(e & 1 ? v[e >> 1] & 0xffff0000u : v[e >> 1] << 16);
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = i + e < V ? value<F32>(row, i + e) : -INFINITY;
+        for (int e = 0; e < 4; ++e) x[e] = i + e < V ? (F32 ? ((const float *)row)[i + e] : bf16_to_f32(((const uint16_t *)row)[i + e])) : -INFINITY;
     }
 }
 
@@ -313,12 +321,21 @@ __device__ __forceinline__ const void *row_of(const SampleArgs &a, int t) {
     return (const char *)a.logits + (size_t)t * a.stride * (F32 ? 4 : 2);
 }
 
-// The chunk's values; thread tid holds tokens 4 tid .. 4 tid + 3 of each tile.
-template <int E, bool F32>
-__device__ __forceinline__ void load_chunk(const SampleArgs &a, int t, int c, float (&x)[E][4]) {
+// A chunk by NT threads: thread tid holds tokens token_at(c, e) .. + 3.
+template <int NT>
+__device__ __forceinline__ int token_at(int c, int e) {
+    return c * kChunk + 4 * (e * NT + (int)threadIdx.x);
+}
+
+template <int NT, bool F32>
+__device__ __forceinline__ void load_chunk(const SampleArgs &a, int t, int c, float (&x)[kChunk / 4 / NT][4]) {
     const void *row = row_of<F32>(a, t);
 #pragma unroll
-    for (int e = 0; e < E; ++e) load4<F32>(row, (c * E + e) * kTile + 4 * threadIdx.x, a.V, x[e]);
+    for (int e = 0; e < kChunk / 4 / NT; ++e) load4<F32>(row, token_at<NT>(c, e), a.V, x[e]);
+#pragma unroll
+    for (int e = 0; e < kChunk / 4 / NT; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[e][i] = clean(x[e][i]);
 }
 
 __device__ __forceinline__ unsigned wave_max_u32(unsigned v) {
@@ -327,81 +344,85 @@ __device__ __forceinline__ unsigned wave_max_u32(unsigned v) {
     return v;
 }
 
-// Sum over the block; every thread gets it.  `sh` [kRowWaves] is free afterwards.
+// Over a block of NT threads; every thread gets the result, `sh` [NT / 64] is
+// free afterwards.
+template <int NT>
 __device__ __forceinline__ uint64_t block_sum_u64(uint64_t v, uint64_t *sh) {
     v = wave_sum_u64(v);
     if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
     __syncthreads();
     v = 0;
 #pragma unroll
-    for (int w = 0; w < kRowWaves; ++w) v += sh[w];
+    for (int w = 0; w < NT / 64; ++w) v += sh[w];
     __syncthreads();
     return v;
 }
 
+template <int NT>
 __device__ __forceinline__ unsigned block_max_u32(unsigned v, unsigned *sh) {
     v = wave_max_u32(v);
     if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kRowWaves; ++w) v = max(v, sh[w]);
+    for (int w = 0; w < NT / 64; ++w) v = max(v, sh[w]);
     __syncthreads();
     return v;
 }
 
-// Largest key of the row from its chunks' (any thread; C <= 64).
-__device__ __forceinline__ unsigned row_key(const unsigned *kmax, int C) {
-    const int lane = threadIdx.x & 63;
-    return wave_max_u32(lane < C ? kmax[lane] : 0u);
+// The first of up to 64 masses, one a lane, whose running sum exceeds `want`,
+// which is below their sum; leaves what lies before it in `before`.
+__device__ __forceinline__ int lane_of_mass(uint64_t m, uint64_t want, uint64_t &before) {
+    const uint64_t incl = wave_scan_u64(m);
+    const int l = __ffsll((unsigned long long)__ballot(incl > want)) - 1;
+    before = l < 0 ? 0 : (uint64_t)__shfl((unsigned long long)(incl - m), l < 0 ? 0 : l);
+    return l;
 }
 
 // In chunk c, the lowest token whose running mass f(value, token), in index
-// order, exceeds `want`; the last with mass if none does.  All threads get it.
-template <int E, bool F32, typename F>
+// order, exceeds `want`; the last with mass if none does.  A block of NT
+// threads, all of which get it.
+template <int NT, bool F32, typename F>
 __device__ int find_in_chunk(const SampleArgs &a, int t, int c, uint64_t want, F f, uint64_t *sums, int *found) {
+    constexpr int E = kChunk / 4 / NT, W = NT / 64;
+    static_assert(E * W <= 64, "a part a lane");
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     float x[E][4];
-    load_chunk<E, F32>(a, t, c, x);
-    uint64_t m[E][4];
+    load_chunk<NT, F32>(a, t, c, x);
     int last = -1;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         uint64_t s = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int at = (c * E + e) * kTile + 4 * tid + i;
-            m[e][i] = at < a.V ? f(x[e][i], at) : 0;
-            if (m[e][i]) last = at;
-            s += m[e][i];
+            const int at = token_at<NT>(c, e) + i;
+            const uint64_t m = at < a.V ? f(x[e][i], at) : 0;
+            if (m) last = at;
+            s += m;
         }
         s = wave_sum_u64(s);
-        if (lane == 0) sums[e * kRowWaves + wave] = s;
+        if (lane == 0) sums[e * W + wave] = s;
     }
     if (tid == 0) *found = -1;
     __syncthreads();
-    uint64_t run = 0;
-    int part = -1;
-    for (int p = 0; p < E * kRowWaves; ++p) {  // the same in every thread
-        if (run + sums[p] > want) {
-            part = p;
-            break;
-        }
-        run += sums[p];
-    }
+    uint64_t run;
+    const int part = lane_of_mass(lane < E * W ? sums[lane] : 0, want, run);  // the same in every wave
     if (part < 0) {
         atomicMax(found, last);
-    } else if ((part & (kRowWaves - 1)) == wave) {
+    } else if (part % W == wave) {
+        float y[4];
+        const int at = token_at<NT>(c, part / W);
+        load4<F32>(row_of<F32>(a, t), at, a.V, y);
+        uint64_t m[4], s = 0;
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (e == part / kRowWaves) {
-                const uint64_t s = m[e][0] + m[e][1] + m[e][2] + m[e][3], incl = wave_scan_u64(s);
-                uint64_t b = run + incl - s;
-                if (b <= want && want < b + s) {
-                    int i = 0;
-                    while (b + m[e][i] <= want) b += m[e][i++];
-                    *found = (c * E + e) * kTile + 4 * tid + i;
-                }
-            }
+        for (int i = 0; i < 4; ++i) {
+            m[i] = at + i < a.V ? f(clean(y[i]), at + i) : 0;
+            s += m[i];
+        }
+        const uint64_t b0 = run + wave_scan_u64(s) - s;
+        if (b0 <= want && want < b0 + s) {
+            const uint64_t b1 = b0 + m[0], b2 = b1 + m[1], b3 = b2 + m[2];
+            *found = at + (want < b1 ? 0 : want < b2 ? 1 : want < b3 ? 2 : 3);
+        }
     }
     __syncthreads();
     const int r = *found;
@@ -409,25 +430,33 @@ __device__ int find_in_chunk(const SampleArgs &a, int t, int c, uint64_t want, F
     return r;
 }
 
+__device__ __forceinline__ void finish_row(const SampleArgs &a, const ExpTable &et, const RowState &st, RowState *states, int t,
+                                           float x, int32_t *token, float *prob) {
+    states[t] = st;
+    if (token) token[t] = st.token;
+    if (prob) prob[t] = st.token < 0 ? 0.f : (float)(kept_weight(et, st, x, st.token) * kUnit / st.sum);
+}
+
 // ---------------------------------------------------------------------------
 // Without filters
 // ---------------------------------------------------------------------------
-template <int E, bool F32>
-__global__ __launch_bounds__(kRowThreads) void part_kernel(SampleArgs a, Work w) {
+template <bool F32>
+__global__ __launch_bounds__(kThreads) void part_kernel(SampleArgs a, Work w) {
+    constexpr int E = kChunk / 4 / kThreads;
     __shared__ ExpTable et;
-    __shared__ unsigned sk[kRowWaves];
-    __shared__ uint64_t ss[kRowWaves];
+    __shared__ unsigned sk[kThreads / 64];
+    __shared__ uint64_t ss[kThreads / 64];
     const int c = blockIdx.x, t = w.row0 + blockIdx.y;
-    const Filter f = filter_of(a, t);
     float x[E][4];
-    load_chunk<E, F32>(a, t, c, x);
+    load_chunk<kThreads, F32>(a, t, c, x);
+    const Filter f = filter_of(a, t);
     et.fill();
-    unsigned k = 0;
+    float v = -INFINITY;
 #pragma unroll
     for (int e = 0; e < E; ++e)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) k = max(k, key_of(x[e][i]));
-    k = block_max_u32(k, sk);
+        for (int i = 0; i < 4; ++i) v = fmaxf(v, x[e][i]);
+    const unsigned k = block_max_u32<kThreads>(key_of(v), sk);
     const float top = of_key(k);
     uint64_t s = 0;
 #pragma unroll
@@ -435,7 +464,7 @@ __global__ __launch_bounds__(kRowThreads) void part_kernel(SampleArgs a, Work w)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (x[e][i] != -INFINITY) s += f.one ? (uint64_t)(x[e][i] == top) : units(weight(et, x[e][i], top, f.invt));
-    s = block_sum_u64(s, ss);
+    s = block_sum_u64<kThreads>(s, ss);
     if (threadIdx.x == 0) {
         w.kmax[blockIdx.y * w.C + c] = k;
         w.sum[blockIdx.y * w.C + c] = s;
@@ -443,96 +472,81 @@ __global__ __launch_bounds__(kRowThreads) void part_kernel(SampleArgs a, Work w)
     }
 }
 
-// A workgroup a row.  The chunks' sums are relative to their own largest
-// values and joined in float64 in chunk order; the draw is made inside its
-// chunk in that chunk's units.
-template <int E, bool F32>
-__global__ __launch_bounds__(kRowThreads) void join_kernel(SampleArgs a, Work w, const float *u, int32_t *token,
-                                                           float *prob) {
+// The chunks' sums are relative to their own largest values and joined in
+// float64 in chunk order; the draw is made inside its chunk in that chunk's
+// units.
+template <bool F32>
+__global__ __launch_bounds__(kThreads) void join_kernel(SampleArgs a, Work w, const float *u, int32_t *token, float *prob) {
     __shared__ ExpTable et;
-    __shared__ uint64_t sums[E * kRowWaves];
-    __shared__ double part[kMaxChunks];
+    __shared__ uint64_t sums[kMaxChunks];
     __shared__ int found;
-    const int t = w.row0 + blockIdx.x, tid = threadIdx.x;
+    const int t = w.row0 + blockIdx.x, lane = threadIdx.x & 63;
+    const unsigned kc = lane < w.C ? w.kmax[blockIdx.x * w.C + lane] : 0;
+    const uint64_t sc = lane < w.C ? w.sum[blockIdx.x * w.C + lane] : 0;
     const Filter f = filter_of(a, t);
-    const unsigned *kmax = w.kmax + blockIdx.x * w.C;
+    const float uu = u ? u[t] : 0.f;
     et.fill();
-    const unsigned km = row_key(kmax, w.C);
+    const unsigned km = wave_max_u32(kc);
     __syncthreads();
     RowState st{f.invt, 0.0, of_key(km), 1u, a.V, -1, 0.0};
-    if (tid < w.C) {
-        const unsigned k = kmax[tid];
-        // rows that keep one token: only the chunks with the largest value count
-        part[tid] = k == 0 || (f.one && k != km) ? 0.0 : (double)w.sum[blockIdx.x * w.C + tid] * weight(et, of_key(k), st.first, f.invt);
-    }
-    __syncthreads();
-    int c = 0, lastc = 0;
-    double total = 0.0, before = 0.0;
-    for (int i = 0; i < w.C; ++i) total += part[i];
-    const float uu = u ? u[t] : 0.f;
-    const double want = f.one || !(uu > 0.f) ? 0.0 : (double)uu * total;
-    double run = 0.0;
-    bool hit = false;
-    for (int i = 0; i < w.C; ++i) {
-        if (part[i] > 0.0) {
-            if (!hit) lastc = i, before = run;
-            hit |= run + part[i] > want;
-        }
-        run += part[i];
-    }
-    c = lastc;
+    float x = 0.f;
     if (km) {
-        const unsigned kc = kmax[c];
+        // rows that keep one token: only chunks with the largest value count
         const float top = of_key(kc);
-        // u beyond the last step leaves a want above the chunk's sum: its last token
-        const double scale = f.one ? 1.0 : weight(et, top, st.first, f.invt);
-        const double inside = fmin((want - before) / scale, 9.0e18);
-        st.token = find_in_chunk<E, F32>(
+        const double scale = kc == 0 || (f.one && kc != km) ? 0.0 : f.one ? 1.0 : weight(et, top, st.first, f.invt);
+        const double part = (double)sc * scale;
+        double incl = part;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const double o = __shfl_up(incl, d);
+            if (lane >= d) incl += o;
+        }
+        const double total = __shfl(incl, 63);
+        const double want = f.one || !(uu > 0.f) ? 0.0 : (double)uu * total;
+        uint64_t hit = __ballot(part > 0.0 && incl > want);
+        const uint64_t some = __ballot(part > 0.0);
+        // a number past the last step takes the last token with weight
+        const int c = hit ? __ffsll((unsigned long long)hit) - 1 : 63 - __clzll((long long)some);
+        const double inside = fmin((want - __shfl(incl - part, c)) / __shfl(scale, c), 9.0e18);
+        const float topc = __shfl(top, c);
+        st.token = find_in_chunk<kThreads, F32>(
             a, t, c, inside > 0.0 ? (uint64_t)inside : 0,
-            [&](float x, int) {
-                return x == -INFINITY ? (uint64_t)0 : f.one ? (uint64_t)(x == top) : units(weight(et, x, top, f.invt));
+            [&](float v, int) {
+                return v == -INFINITY ? (uint64_t)0 : f.one ? (uint64_t)(v == topc) : units(weight(et, v, topc, f.invt));
             },
             sums, &found);
         st.sum = f.one ? kUnit : total;
         if (f.one) st.key = km, st.last = st.token;
+        x = value<F32>(row_of<F32>(a, t), st.token);
     }
-    if (tid == 0) {
-        w.states[t] = st;
-        if (token) token[t] = st.token;
-        if (prob)
-            prob[t] = st.token < 0 ? 0.f
-                                   : (float)(kept_weight(et, st, value<F32>(row_of<F32>(a, t), st.token), st.token) * kUnit / st.sum);
-    }
+    if (threadIdx.x == 0) finish_row(a, et, st, w.states, t, x, token, prob);
 }
 
 // ---------------------------------------------------------------------------
 // With filters
 // ---------------------------------------------------------------------------
-template <int E, bool F32>
-__global__ __launch_bounds__(kRowThreads) void max_kernel(SampleArgs a, Work w) {
-    __shared__ unsigned sk[kRowWaves];
-    __shared__ int sn[kRowWaves];
-    const int c = blockIdx.x, t = w.row0 + blockIdx.y, tid = threadIdx.x;
+template <bool F32>
+__global__ __launch_bounds__(kThreads) void max_kernel(SampleArgs a, Work w) {
+    constexpr int E = kChunk / 4 / kThreads;
+    __shared__ unsigned sk[kThreads / 64];
+    __shared__ uint64_t sn[kThreads / 64];
+    const int c = blockIdx.x, t = w.row0 + blockIdx.y;
     float x[E][4];
-    load_chunk<E, F32>(a, t, c, x);
-    unsigned k = 0;
+    load_chunk<kThreads, F32>(a, t, c, x);
+    float v = -INFINITY;
     int n = 0;
 #pragma unroll
     for (int e = 0; e < E; ++e)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const unsigned q = key_of(x[e][i]);
-            k = max(k, q);
-            n += q != 0;
+            v = fmaxf(v, x[e][i]);
+            n += x[e][i] != -INFINITY;
         }
-    n = wave_sum_int(n);
-    if ((tid & 63) == 0) sn[tid >> 6] = n;
-    k = block_max_u32(k, sk);
-    if (tid == 0) {
-        n = 0;
-        for (int i = 0; i < kRowWaves; ++i) n += sn[i];
+    const unsigned k = block_max_u32<kThreads>(key_of(v), sk);
+    const uint64_t all = block_sum_u64<kThreads>((uint64_t)n, sn);
+    if (threadIdx.x == 0) {
         w.kmax[blockIdx.y * w.C + c] = k;
-        w.count[blockIdx.y * w.C + c] = n;
+        w.count[blockIdx.y * w.C + c] = (int)all;
         if (c == 0) w.head[blockIdx.y] = Header{0, 0, 0, 0};
     }
 }
@@ -546,7 +560,7 @@ struct Kind {
 __device__ __forceinline__ Kind kind_of(const Filter &f, const Work &w, int row) {
     const int lane = threadIdx.x & 63;
     Kind k;
-    k.km = row_key(w.kmax + row * w.C, w.C);
+    k.km = wave_max_u32(lane < w.C ? w.kmax[row * w.C + lane] : 0u);
     const int n = wave_sum_int(lane < w.C ? w.count[row * w.C + lane] : 0);
     k.by_k = !f.one && f.topk > 0 && f.topk < n;
     k.by_p = !f.one && f.topp < 1.f && k.km;
@@ -558,70 +572,162 @@ __device__ __forceinline__ int bin_of(float x, float first, double invt) {
 }
 
 // The weights of the last bin are below 2^-45 / 2 and have no units, so a
-// top-p threshold never lies in it.
-template <int E, bool F32>
-__global__ __launch_bounds__(kRowThreads) void hist_kernel(SampleArgs a, Work w) {
+// top-p threshold never lies in it.  A workgroup takes w.E chunks.
+template <bool F32>
+__global__ __launch_bounds__(kThreads) void hist_kernel(SampleArgs a, Work w) {
+    constexpr int E = kChunk / 4 / kThreads, B = kBins / kThreads;
     __shared__ ExpTable et;
     __shared__ unsigned cnt[kBins];
     __shared__ unsigned long long mass[kBins];
-    __shared__ uint64_t wc[kRowWaves], wm[kRowWaves];
+    __shared__ uint64_t wc[kThreads / 64], wm[kThreads / 64];
     __shared__ int sh;
-    static_assert(kBins == kRowThreads, "a bin a thread");
-    const int c = blockIdx.x, row = blockIdx.y, t = w.row0 + row, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int hc = blockIdx.x, row = blockIdx.y, t = w.row0 + row, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const Filter f = filter_of(a, t);
     const Kind kind = kind_of(f, w, row);
     if (!kind.by_k && !kind.by_p) return;  // the whole row's workgroups
-    float x[E][4];
-    load_chunk<E, F32>(a, t, c, x);
     et.fill();
-    cnt[tid] = 0;
-    mass[tid] = 0;
+#pragma unroll
+    for (int y = 0; y < B; ++y) cnt[y * kThreads + tid] = 0, mass[y * kThreads + tid] = 0;
     __syncthreads();
     const float first = of_key(kind.km);
+    for (int c = hc * w.E; c < min(w.C, (hc + 1) * w.E); ++c) {
+        float x[E][4];
+        load_chunk<kThreads, F32>(a, t, c, x);
 #pragma unroll
-    for (int e = 0; e < E; ++e)
+        for (int e = 0; e < E; ++e)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (x[e][i] == -INFINITY) continue;
-            const int b = bin_of(x[e][i], first, f.invt);
-            if (b == kBins - 1) continue;
-            atomicAdd(&cnt[b], 1u);
-            if (!kind.by_k) atomicAdd(&mass[b], (unsigned long long)units(weight(et, x[e][i], first, f.invt)));
-        }
-    __syncthreads();
-    const size_t at = ((size_t)row * w.C + c) * kBins + tid;
-    put(w.hcnt + at, cnt[tid]);
-    if (!kind.by_k) put(w.hmass + at, (uint64_t)mass[tid]);
-    if (!last_of(&w.head[row].hist_done, w.C, &sh)) return;
-    uint64_t n = 0, m = 0;
-    for (int i = 0; i < w.C; ++i) {
-        const size_t p = ((size_t)row * w.C + i) * kBins + tid;
-        n += get(w.hcnt + p);
-        if (!kind.by_k) m += get(w.hmass + p);
+            for (int i = 0; i < 4; ++i) {
+                if (x[e][i] == -INFINITY) continue;
+                const int b = bin_of(x[e][i], first, f.invt);
+                if (b == kBins - 1) continue;
+                atomicAdd(&cnt[b], 1u);
+                if (!kind.by_k) atomicAdd(&mass[b], (unsigned long long)units(weight(et, x[e][i], first, f.invt)));
+            }
     }
-    uint64_t ni = wave_scan_u64(n), mi = wave_scan_u64(m);
-    if (lane == 63) wc[wave] = ni, wm[wave] = mi;
     __syncthreads();
-    uint64_t total = 0;
-    for (int i = 0; i < kRowWaves; ++i) {
-        if (i < wave) ni += wc[i], mi += wm[i];
+    const size_t at = (size_t)row * w.H * kBins;
+#pragma unroll
+    for (int y = 0; y < B; ++y) {
+        const int b = y * kThreads + tid;
+        put(w.hcnt + at + hc * kBins + b, cnt[b]);
+        if (!kind.by_k) put(w.hmass + at + hc * kBins + b, (uint64_t)mass[b]);
+    }
+    if (!last_of(&w.head[row].hist_done, w.H, &sh)) return;
+    // the row's histogram: thread tid joins bins tid, tid + 256, ..., then owns B consecutive ones
+#pragma unroll
+    for (int y = 0; y < B; ++y) {
+        const int b = y * kThreads + tid;
+        unsigned n = 0;
+        uint64_t m = 0;
+#pragma unroll 4
+        for (int i = 0; i < w.H; ++i) {
+            n += get(w.hcnt + at + i * kBins + b);
+            if (!kind.by_k) m += get(w.hmass + at + i * kBins + b);
+        }
+        cnt[b] = n;
+        mass[b] = m;
+    }
+    __syncthreads();
+    uint64_t n = 0, m = 0;
+#pragma unroll
+    for (int y = 0; y < B; ++y) n += cnt[B * tid + y], m += mass[B * tid + y];
+    uint64_t nb = wave_scan_u64(n) - n, mb = kind.by_k ? 0 : wave_scan_u64(m) - m;
+    if (lane == 63) wc[wave] = nb + n, wm[wave] = mb + m;
+    __syncthreads();
+    uint64_t total = 0, counted = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 64; ++i) {
+        if (i < wave) nb += wc[i], mb += wm[i];
+        counted += wc[i];
         total += wm[i];
     }
     const uint64_t want = kind.by_k ? (uint64_t)f.topk : max((uint64_t)1, (uint64_t)ceil((double)f.topp * (double)total));
-    const uint64_t hi = kind.by_k ? ni : mi, lo = hi - (kind.by_k ? n : m);
-    if (lo < want && want <= hi) {
-        Plan p;
-        p.sure = kind.by_k ? 0 : tid;  // by_k: the sum of the first top_k comes from the list
-        p.end = tid;
-        p.slow = (kind.by_k ? ni : n) > (uint64_t)kList;
-        p.pad = 0;
-        p.above_cnt = kind.by_k ? 0 : ni - n;
-        p.above_mass = kind.by_k ? 0 : mi - m;
-        p.mass = total;
-        w.plan[row] = p;
+#pragma unroll
+    for (int y = 0; y < B; ++y) {
+        const uint64_t c = cnt[B * tid + y], v = mass[B * tid + y];
+        const uint64_t lo = kind.by_k ? nb : mb, hi = lo + (kind.by_k ? c : v);
+        if (lo < want && want <= hi) {
+            Plan p;
+            p.sure = kind.by_k ? 0 : B * tid + y;  // by_k: the sum of the first top_k comes from the list
+            p.end = B * tid + y;
+            p.slow = (kind.by_k ? hi : c) > (uint64_t)kList;
+            p.pad = 0;
+            p.above_mass = mb;
+            p.mass = total;
+            w.plan[row] = p;
+        }
+        nb += c;
+        mb += v;
     }
-    // by_k with the threshold in the last bin: no thread above has it
-    if (tid == kBins - 1 && kind.by_k && want > ni) w.plan[row] = Plan{0, kBins - 1, 1, 0, 0, 0, 0};
+    // the threshold of top_k in the last bin
+    if (tid == 0 && kind.by_k && want > counted) w.plan[row] = Plan{0, kBins - 1, 1, 0, 0, 0};
+}
+
+template <bool F32>
+__global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a, Work w) {
+    constexpr int E = kChunk / 4 / kThreads;
+    __shared__ ExpTable et;
+    __shared__ uint64_t sums[kThreads / 64];
+    __shared__ int sh;
+    const int c = blockIdx.x, row = blockIdx.y, t = w.row0 + row, tid = threadIdx.x;
+    const Filter f = filter_of(a, t);
+    const Kind kind = kind_of(f, w, row);
+    const bool planned = kind.by_k || kind.by_p;
+    Plan p{kBins, -1, 0, 0, 0, 0};
+    if (planned) p = w.plan[row];
+    if (p.slow) return;
+    float x[E][4];
+    load_chunk<kThreads, F32>(a, t, c, x);
+    et.fill();
+    if (tid == 0) sh = f.one ? INT_MAX : 0;
+    __syncthreads();
+    const float first = of_key(kind.km);
+    uint64_t sum = 0;
+    if (f.one) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (kind.km && key_of(x[e][i]) == kind.km) atomicMin(&sh, token_at<kThreads>(c, e) + i);
+        __syncthreads();
+        sum = (uint64_t)sh;
+    } else {
+        int mine = 0;
+        unsigned in = 0;  // which of the thread's tokens go to the list
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (x[e][i] == -INFINITY) continue;
+                const int b = planned ? bin_of(x[e][i], first, f.invt) : 0;
+                if (b < p.sure) {
+                    const double wt = weight(et, x[e][i], first, f.invt);
+                    if (wt >= f.minp) sum += units(wt);
+                } else if (b <= p.end) {
+                    ++mine;
+                    in |= 1u << (4 * e + i);
+                }
+            }
+        if (p.sure) sum = block_sum_u64<kThreads>(sum, sums);
+        if (planned) {
+            int at = 0;
+            if (mine) at = atomicAdd(&sh, mine);
+            __syncthreads();
+            if (tid == 0 && sh) sh = __hip_atomic_fetch_add(&w.head[row].listed, sh, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __syncthreads();
+            if (mine) {
+                at += sh;
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if ((in >> (4 * e + i)) & 1 && at < w.L)
+                            w.list[(size_t)row * w.L + at++] =
+                                ((uint64_t)~key_of(x[e][i]) << 32) | (unsigned)(token_at<kThreads>(c, e) + i);
+            }
+        }
+    }
+    if (tid == 0) w.sum[row * w.C + c] = sum;
 }
 
 // The row's filter by radix descent, by one workgroup.
@@ -654,145 +760,97 @@ __device__ void descend_row(const ExpTable &et, const SampleArgs &a, const void 
         [&](uint64_t n) { return min(ties, n) - 1; }, sums, found, &total);
 }
 
+// Bitonic sort of `size` (a power of two >= 64) list entries, ascending:
+// key descending, index ascending.  Strides up to 64 stay inside the 128
+// entries of a wave and need no barrier of the block.
+__device__ void sort_list(uint64_t *list, int size) {
+    for (int k = 2; k <= size; k <<= 1)
+        for (int j = k >> 1; j > 0; j >>= 1) {
+            if (j > 64 || (j == 64 && k > 128)) __syncthreads();
+            for (int i = threadIdx.x; i < size / 2; i += kRowThreads) {
+                const int lo = ((i & ~(j - 1)) << 1) | (i & (j - 1)), hi = lo | j;
+                const uint64_t x0 = list[lo], x1 = list[hi];
+                if ((x0 > x1) == ((lo & k) == 0)) list[lo] = x1, list[hi] = x0;
+            }
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
+    __syncthreads();
+}
+
 union DrawShared {
     uint64_t list[kList];
     Histogram h;
 };
 
-template <int E, bool F32>
-__global__ __launch_bounds__(kRowThreads) void draw_kernel(SampleArgs a, Work w, const float *u, int32_t *token,
-                                                           float *prob) {
+template <bool F32>
+__global__ __launch_bounds__(kRowThreads) void resolve_kernel(SampleArgs a, Work w, const float *u, int32_t *token, float *prob) {
     __shared__ ExpTable et;
     __shared__ DrawShared s;
-    __shared__ uint64_t sums[(E > 1 ? E : 1) * kRowWaves];
+    __shared__ uint64_t sums[kMaxChunks];
     __shared__ unsigned long long cs[kMaxChunks];
-    __shared__ int sh, found;
-    __shared__ unsigned lkey;
-    __shared__ int lidx;
-    const int c = blockIdx.x, row = blockIdx.y, t = w.row0 + row, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    __shared__ int found;
+    const int row = blockIdx.x, t = w.row0 + row, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const Filter f = filter_of(a, t);
     const Kind kind = kind_of(f, w, row);
     const bool planned = kind.by_k || kind.by_p;
-    float x[E][4];
-    load_chunk<E, F32>(a, t, c, x);
-    et.fill();
-    if (tid == 0) sh = 0, found = INT_MAX;
-    Plan p{kBins, -1, 0, 0, 0, 0, 0};
+    const float uu = u ? u[t] : 0.f;
+    Plan p{kBins, -1, 0, 0, 0, 0};
     if (planned) p = w.plan[row];
+    et.fill();
+    if (tid < kMaxChunks) cs[tid] = tid < w.C && !p.slow ? w.sum[row * w.C + tid] : 0;
     RowState st{f.invt, f.one ? 0.0 : f.minp, of_key(kind.km), 1u, a.V, -1, 0.0};
-    __syncthreads();
-
-    // ---- the chunk: sums of the sure, list of the others ----
-    uint64_t sum = 0;
-    if (f.one) {
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-#pragma unroll
-            for (int i = 3; i >= 0; --i)
-                if (kind.km && key_of(x[e][i]) == kind.km) atomicMin(&found, (c * E + e) * kTile + 4 * tid + i);
-        __syncthreads();
-        sum = (uint64_t)found;
-    } else if (!p.slow) {
-        int mine = 0;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (x[e][i] == -INFINITY) continue;
-                const int b = planned ? bin_of(x[e][i], st.first, f.invt) : 0;
-                if (b < p.sure) {
-                    const double wt = weight(et, x[e][i], st.first, f.invt);
-                    if (wt >= st.minp) sum += units(wt);
-                } else if (b <= p.end) {
-                    ++mine;
-                }
-            }
-        sum = block_sum_u64(sum, sums);
-        if (planned) {
-            int at = 0;
-            if (mine) at = atomicAdd(&sh, mine);
-            __syncthreads();
-            if (tid == 0 && sh) sh = __hip_atomic_fetch_add(&w.head[row].listed, sh, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            __syncthreads();
-            if (mine) {
-                at += sh;
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (x[e][i] == -INFINITY) continue;
-                        const int b = bin_of(x[e][i], st.first, f.invt);
-                        if (b >= p.sure && b <= p.end && at < kList)
-                            put(w.list + (size_t)row * kList + at++,
-                                ((uint64_t)~key_of(x[e][i]) << 32) | (unsigned)((c * E + e) * kTile + 4 * tid + i));
-                    }
-            }
-        }
-    }
-    if (tid == 0) put(w.sum + row * w.C + c, sum);
-    if (!last_of(&w.head[row].draw_done, w.C, &sh)) return;
-
-    // ---- the row, by its last workgroup ----
-    if (tid < kMaxChunks) cs[tid] = tid < w.C ? get(w.sum + row * w.C + tid) : 0;
+    float x = 0.f;
+    const void *r = row_of<F32>(a, t);
     __syncthreads();
     if (kind.km == 0) {
         // no token
     } else if (f.one) {
-        uint64_t lo = cs[0];
-        for (int i = 1; i < w.C; ++i) lo = min(lo, (uint64_t)cs[i]);
+        int lo = lane < w.C ? (int)cs[lane] : INT_MAX;
+#pragma unroll
+        for (int d = 32; d; d >>= 1) lo = min(lo, __shfl_xor(lo, d));
         st.key = kind.km;
-        st.last = st.token = (int)lo;
+        st.last = st.token = lo;
         st.sum = kUnit;
     } else if (p.slow) {
-        descend_row<F32>(et, a, row_of<F32>(a, t), f, kind, st, s.h, sums, &found);
+        descend_row<F32>(et, a, r, f, kind, st, s.h, sums, &found);
         uint64_t total;
-        const void *r = row_of<F32>(a, t);
         st.token = pick(
             a.V, [&](int i) { return units(kept_weight(et, st, value<F32>(r, i), i)); },
-            [&](uint64_t total) { return target(u ? u[t] : 0.f, total); }, sums, &found, &total);
+            [&](uint64_t total) { return target(uu, total); }, sums, &found, &total);
         st.sum = (double)total;
     } else {
         if (planned) {
-            // sort the list: key descending, index ascending
-            const int n = min(get(&w.head[row].listed), kList);
+            const int n = min(w.head[row].listed, w.L);
             int size = 64;
             while (size < n) size <<= 1;
-            for (int i = tid; i < size; i += kRowThreads) s.list[i] = i < n ? get(w.list + (size_t)row * kList + i) : ~0ull;
+            for (int i = tid; i < size; i += kRowThreads) s.list[i] = i < n ? w.list[(size_t)row * w.L + i] : ~0ull;
             __syncthreads();
-            for (int k = 2; k <= size; k <<= 1)
-                for (int j = k >> 1; j > 0; j >>= 1) {
-                    for (int i = tid; i < size / 2; i += kRowThreads) {
-                        const int lo = ((i & ~(j - 1)) << 1) | (i & (j - 1)), hi = lo | j;
-                        const uint64_t x0 = s.list[lo], x1 = s.list[hi];
-                        if ((x0 > x1) == ((lo & k) == 0)) s.list[lo] = x1, s.list[hi] = x0;
-                    }
-                    __syncthreads();
-                }
+            sort_list(s.list, size);
             // running weights of the list: thread tid holds `per` of them
             const int per = (size + kRowThreads - 1) / kRowThreads, b = tid * per;
-            auto unit_at = [&](int i) { return units(weight(et, of_key(~(unsigned)(s.list[i] >> 32)), st.first, f.invt)); };
-            const int e = min(b + per, n), nk = kind.by_k ? min(f.topk, n) : n;
+            auto weight_at = [&](int i) { return weight(et, of_key(~(unsigned)(s.list[i] >> 32)), st.first, f.invt); };
+            const int nk = kind.by_k ? min(f.topk, n) : n, e = min(b + per, nk);
             uint64_t mine = 0;
-            for (int i = b; i < e && i < nk; ++i) mine += unit_at(i);
-            uint64_t incl = wave_scan_u64(mine);
-            if (lane == 63) sums[wave] = incl;
-            __syncthreads();
-            uint64_t wk = 0;
-            for (int i = 0; i < kRowWaves; ++i) {
-                if (i < wave) incl += sums[i];
-                wk += sums[i];
-            }
-            __syncthreads();
-            // how many of the list are kept
+            if (kind.by_p)
+                for (int i = b; i < e; ++i) mine += units(weight_at(i));
             if (tid == 0) found = nk;
-            __syncthreads();
             if (kind.by_p) {
+                uint64_t incl = wave_scan_u64(mine), wk = 0;
+                if (lane == 63) sums[wave] = incl;
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < kRowWaves; ++i) {
+                    if (i < wave) incl += sums[i];
+                    wk += sums[i];
+                }
+                // how many of the list are kept
                 const uint64_t whole = kind.by_k ? wk : p.mass;
                 const uint64_t want = max((uint64_t)1, (uint64_t)ceil((double)f.topp * (double)whole));
                 uint64_t run = p.above_mass + incl - mine;
                 if (run < want && want <= run + mine)
-                    for (int i = b; i < e && i < nk; ++i) {
-                        run += unit_at(i);
+                    for (int i = b; i < e; ++i) {
+                        run += units(weight_at(i));
                         if (run >= want) {
                             found = i + 1;
                             break;
@@ -801,45 +859,36 @@ __global__ __launch_bounds__(kRowThreads) void draw_kernel(SampleArgs a, Work w,
             }
             __syncthreads();
             const int kept = found;
-            if (tid == 0 && kept > 0) {
-                lkey = ~(unsigned)(s.list[kept - 1] >> 32);
-                lidx = (int)(unsigned)s.list[kept - 1];
-            }
+            st.key = ~(unsigned)(s.list[kept - 1] >> 32);
+            st.last = (int)(unsigned)s.list[kept - 1];
             for (int i = b; i < e && i < kept; ++i) {
-                const double wt = weight(et, of_key(~(unsigned)(s.list[i] >> 32)), st.first, f.invt);
-                if (wt >= st.minp) atomicAdd(&cs[(unsigned)s.list[i] / (E * kTile)], (unsigned long long)units(wt));
+                const double wt = weight_at(i);
+                if (wt >= st.minp) atomicAdd(&cs[(unsigned)s.list[i] / kChunk], (unsigned long long)units(wt));
             }
             __syncthreads();
-            st.key = lkey;
-            st.last = lidx;
         }
-        uint64_t total = 0;
-        for (int i = 0; i < w.C; ++i) total += cs[i];
-        uint64_t want = target(u ? u[t] : 0.f, total);
-        int ch = 0;
-        while (ch + 1 < w.C && want >= cs[ch]) want -= cs[ch++];
-        st.token = find_in_chunk<E, F32>(
-            a, t, ch, want, [&](float v, int i) { return units(kept_weight(et, st, v, i)); }, sums, &found);
+        const uint64_t mc = cs[lane], total = wave_sum_u64(mc);
+        const uint64_t want = target(uu, total);
+        uint64_t before;
+        const int c = lane_of_mass(mc, want, before);
+        st.token = find_in_chunk<kRowThreads, F32>(
+            a, t, c, want - before, [&](float v, int i) { return units(kept_weight(et, st, v, i)); }, sums, &found);
         st.sum = (double)total;
     }
-    if (tid == 0) {
-        w.states[t] = st;
-        if (token) token[t] = st.token;
-        if (prob)
-            prob[t] = st.token < 0 ? 0.f
-                                   : (float)(kept_weight(et, st, value<F32>(row_of<F32>(a, t), st.token), st.token) * kUnit / st.sum);
-    }
+    if (st.token >= 0) x = value<F32>(r, st.token);
+    if (tid == 0) finish_row(a, et, st, w.states, t, x, token, prob);
 }
 
 // ---------------------------------------------------------------------------
 // The whole distribution of a row
 // ---------------------------------------------------------------------------
-template <int E, bool F32>
-__global__ __launch_bounds__(kRowThreads) void probs_kernel(SampleArgs a, Work w, float *probs) {
+template <bool F32>
+__global__ __launch_bounds__(kThreads) void probs_kernel(SampleArgs a, Work w, float *probs) {
+    constexpr int E = kChunk / 4 / kThreads;
     __shared__ ExpTable et;
     const int c = blockIdx.x, t = w.row0 + blockIdx.y;
     float x[E][4];
-    load_chunk<E, F32>(a, t, c, x);
+    load_chunk<kThreads, F32>(a, t, c, x);
     const RowState st = w.states[t];
     et.fill();
     __syncthreads();
@@ -847,7 +896,7 @@ __global__ __launch_bounds__(kRowThreads) void probs_kernel(SampleArgs a, Work w
     float *out = probs + (size_t)t * a.V;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        const int at = (c * E + e) * kTile + 4 * threadIdx.x;
+        const int at = token_at<kThreads>(c, e);
         f32x4 v;
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = (float)(kept_weight(et, st, x[e][i], at + i) * k);
@@ -866,20 +915,23 @@ __global__ __launch_bounds__(kRowThreads) void probs_kernel(SampleArgs a, Work w
 // ---------------------------------------------------------------------------
 // Drafts matched against the target's own draws: one thread a sequence.
 __global__ __launch_bounds__(64) void match_kernel(AcceptArgs c, const int32_t *drawn) {
-    const int s = threadIdx.x;
+    __shared__ int32_t tok[kMaxTokens], drew[kMaxTokens];
+    const int s = threadIdx.x, T = c.off[c.nseq];
+    if (s < T) tok[s] = c.tokens[s], drew[s] = drawn[s];
+    __syncthreads();
     if (s >= c.nseq) return;
     const int r0 = c.off[s], n = c.off[s + 1] - r0;
     int cur = 0, k = 0;
     if (n) {
         while (true) {
             c.path[r0 + k] = cur;
-            const int y = drawn[r0 + cur];
+            const int y = drew[r0 + cur];
             c.out[r0 + k] = y;
             ++k;
             int next = -1;
             if (y >= 0)
                 for (int j = cur + 1; j < n && next < 0; ++j)
-                    if (c.parent[r0 + j] == cur && c.tokens[r0 + j] == y) next = j;
+                    if (c.parent[r0 + j] == cur && tok[r0 + j] == y) next = j;
             if (next < 0) break;
             cur = next;
         }
@@ -891,28 +943,27 @@ __global__ __launch_bounds__(64) void match_kernel(AcceptArgs c, const int32_t *
 // Chains against the drafter's distributions.  Every workgroup of a sequence
 // finds the row of the last token (thread j tests draft j + 1), sums its
 // chunk of max(p - q, 0) there, or of p, and the last one draws.
-template <int E, bool F32>
+template <bool F32>
 __global__ __launch_bounds__(kRowThreads) void chain_kernel(SampleArgs a, AcceptArgs c, Work w) {
+    constexpr int E = kChunk / 4 / kRowThreads;
     __shared__ ExpTable et;
-    __shared__ uint64_t sums[(E > 1 ? E : 1) * kRowWaves];
-    __shared__ uint64_t cs[kMaxChunks];
+    __shared__ uint64_t sums[kMaxChunks];
     __shared__ int sh, found, row_sh;
-    const int ch = blockIdx.x, s = blockIdx.y, r0 = c.off[s], n = c.off[s + 1] - r0, tid = threadIdx.x;
+    const int ch = blockIdx.x, s = blockIdx.y, r0 = c.off[s], n = c.off[s + 1] - r0, tid = threadIdx.x, lane = tid & 63;
     if (n == 0) {
         if (ch == 0 && tid == 0) c.count[s] = 0;
         return;
     }
     et.fill();
     __syncthreads();
-    auto p_of = [&](const RowState &st, float x, int i) {
-        return st.sum > 0.0 ? kept_weight(et, st, x, i) * (kUnit / st.sum) : 0.0;
-    };
+    auto p_of = [&](const RowState &st, double k, float x, int i) { return kept_weight(et, st, x, i) * k; };
     if (tid < 64) {  // n <= 64
         bool stop = true;
         if (tid + 1 < n) {
             const int t = r0 + tid, x = c.tokens[t + 1];
-            if (x >= 0 && x < a.V) {
-                const double p = p_of(w.states[t], value<F32>(row_of<F32>(a, t), x), x);
+            const RowState st = w.states[t];
+            if (x >= 0 && x < a.V && st.sum > 0.0) {
+                const double p = p_of(st, kUnit / st.sum, value<F32>(row_of<F32>(a, t), x), x);
                 stop = !((double)c.u[t] * (double)c.q[(size_t)t * a.V + x] < p);
             }
         }
@@ -923,40 +974,39 @@ __global__ __launch_bounds__(kRowThreads) void chain_kernel(SampleArgs a, Accept
     const int j = row_sh, t = r0 + j;
     const bool rest = j + 1 < n;
     const RowState st = w.states[t];
+    const double scale = st.sum > 0.0 ? kUnit / st.sum : 0.0;
     const float *q = c.q + (size_t)t * a.V;
     auto mass = [&](float x, int i) {
-        const double v = fmax(p_of(st, x, i) - (rest ? (double)q[i] : 0.0), 0.0);
-        return (uint64_t)__double_as_longlong(fma(v, 2251799813685248.0, 4503599627370496.0)) & 0xFFFFFFFFFFFFFull;  // 2^51
+        const double v = fmax(p_of(st, scale, x, i) - (rest ? (double)q[i] : 0.0), 0.0);
+        return (uint64_t)__double_as_longlong(fma(v, kUnitP, 4503599627370496.0)) & 0xFFFFFFFFFFFFFull;
     };
     float x[E][4];
-    load_chunk<E, F32>(a, t, ch, x);
+    load_chunk<kRowThreads, F32>(a, t, ch, x);
     uint64_t sum = 0;
 #pragma unroll
     for (int e = 0; e < E; ++e)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int at = (ch * E + e) * kTile + 4 * tid + i;
+            const int at = token_at<kRowThreads>(ch, e) + i;
             if (at < a.V) sum += mass(x[e][i], at);
         }
-    sum = block_sum_u64(sum, sums);
+    sum = block_sum_u64<kRowThreads>(sum, sums);
     if (tid == 0) put(w.sum + r0 * w.C + ch, sum);
     if (!last_of(&w.head[r0].chain_done, w.C, &sh)) return;
-    if (tid < kMaxChunks) cs[tid] = tid < w.C ? get(w.sum + r0 * w.C + tid) : 0;
-    __syncthreads();
-    uint64_t total = 0;
-    for (int i = 0; i < w.C; ++i) total += cs[i];
+    const uint64_t mc = lane < w.C ? get(w.sum + r0 * w.C + lane) : 0, total = wave_sum_u64(mc);
     const float u = c.u_final[s];
     int tok;
     if (total) {
-        uint64_t want = target(u, total);
-        int k = 0;
-        while (k + 1 < w.C && want >= cs[k]) want -= cs[k++];
-        tok = find_in_chunk<E, F32>(a, t, k, want, mass, sums, &found);
+        const uint64_t want = target(u, total);
+        uint64_t before;
+        const int k = lane_of_mass(mc, want, before);
+        tok = find_in_chunk<kRowThreads, F32>(a, t, k, want - before, mass, sums, &found);
     } else {  // nothing of p lies above q
         const void *row = row_of<F32>(a, t);
+        uint64_t all;
         tok = pick(
             a.V, [&](int i) { return units(kept_weight(et, st, value<F32>(row, i), i)); },
-            [&](uint64_t total) { return target(u, total); }, sums, &found, &total);
+            [&](uint64_t all) { return target(u, all); }, sums, &found, &all);
     }
     for (int i = tid; i < n; i += kRowThreads) {
         c.path[r0 + i] = i <= j ? i : -1;
@@ -970,33 +1020,29 @@ __global__ __launch_bounds__(kRowThreads) void chain_kernel(SampleArgs a, Accept
 // ---------------------------------------------------------------------------
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-// Tiles of a chunk: enough workgroups for the chip before longer chunks.
-int tiles_of(int T, int V) {
-    const int tiles = (V + kTile - 1) / kTile;
-    for (int e = 1; e < 4; e *= 2)
-        if ((long long)T * ((tiles + e - 1) / e) <= 2048) return e;
-    return 4;
-}
-
 struct Layout {
-    int E, C, rows;  // tiles of a chunk, chunks of a row, rows of a batch
+    int C, E, H, L, rows;  // as in Work; rows of a batch
     size_t states, drawn, kmax, count, sum, head, plan, list, hcnt, hmass, total;
 };
 
+// A histogram is written and read whole (12 KB), so it takes up to 4 chunks
+// where that leaves the chip enough workgroups.
 Layout layout(int T, int V) {
     Layout l{};
-    const int tiles = (V + kTile - 1) / kTile;
-    l.E = tiles_of(T, V);
-    l.C = (tiles + l.E - 1) / l.E;
-    l.rows = T < 4096 / l.C ? T : 4096 / l.C;
-    if (l.rows < 1) l.rows = 1;
+    l.C = (V + kChunk - 1) / kChunk;
+    const long long wgs = (long long)T * l.C;
+    l.E = wgs >= 2048 ? 4 : wgs >= 1024 ? 2 : 1;
+    l.H = (l.C + l.E - 1) / l.E;
+    l.L = V < kList ? (V + 63) & ~63 : kList;
+    l.rows = l.C > 8 ? 16384 / l.C : 2048;
+    if (l.rows > T) l.rows = T;
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
         off = align256(off + bytes);
         return at;
     };
-    const size_t rc = (size_t)l.rows * l.C;
+    const size_t rc = (size_t)l.rows * l.C, rh = (size_t)l.rows * l.H;
     l.states = take((size_t)T * sizeof(RowState));
     l.drawn = take((size_t)T * 4);
     l.kmax = take(rc * 4);
@@ -1004,9 +1050,9 @@ Layout layout(int T, int V) {
     l.sum = take(rc * 8);
     l.head = take((size_t)l.rows * sizeof(Header));
     l.plan = take((size_t)l.rows * sizeof(Plan));
-    l.list = take((size_t)l.rows * kList * 8);
-    l.hcnt = take(rc * kBins * 4);
-    l.hmass = take(rc * kBins * 8);
+    l.list = take((size_t)l.rows * l.L * 8);
+    l.hcnt = take(rh * kBins * 4);
+    l.hmass = take(rh * kBins * 8);
     l.total = off;
     return l;
 }
@@ -1026,86 +1072,61 @@ Work work_of(const SampleArgs &a, const Layout &l) {
     w.hmass = reinterpret_cast<uint64_t *>(p + l.hmass);
     w.row0 = 0;
     w.C = l.C;
+    w.E = l.E;
+    w.H = l.H;
+    w.L = l.L;
     return w;
 }
 
 // States, and draws with u, of all rows.
-template <int E, bool F32>
+template <bool F32>
 hipError_t rows(const SampleArgs &a, Work w, const Layout &l, const float *u, int32_t *token, float *prob, float *probs,
                 hipStream_t s) {
+    const dim3 block(kThreads);
     for (; w.row0 < a.T; w.row0 += l.rows) {
         const int n = a.T - w.row0 < l.rows ? a.T - w.row0 : l.rows;
-        const dim3 grid(l.C, n), block(kRowThreads);
+        const dim3 grid(l.C, n);
         if (!a.top_k && !a.top_p && !a.min_p) {
-            hipLaunchKernelGGL((part_kernel<E, F32>), grid, block, 0, s, a, w);
-            hipLaunchKernelGGL((join_kernel<E, F32>), dim3(n), block, 0, s, a, w, u, token, prob);
+            hipLaunchKernelGGL((part_kernel<F32>), grid, block, 0, s, a, w);
+            hipLaunchKernelGGL((join_kernel<F32>), dim3(n), block, 0, s, a, w, u, token, prob);
         } else {
-            hipLaunchKernelGGL((max_kernel<E, F32>), grid, block, 0, s, a, w);
-            if (a.top_k || a.top_p) hipLaunchKernelGGL((hist_kernel<E, F32>), grid, block, 0, s, a, w);
-            hipLaunchKernelGGL((draw_kernel<E, F32>), grid, block, 0, s, a, w, u, token, prob);
+            hipLaunchKernelGGL((max_kernel<F32>), grid, block, 0, s, a, w);
+            if (a.top_k || a.top_p) hipLaunchKernelGGL((hist_kernel<F32>), dim3(l.H, n), block, 0, s, a, w);
+            hipLaunchKernelGGL((gather_kernel<F32>), grid, block, 0, s, a, w);
+            hipLaunchKernelGGL((resolve_kernel<F32>), dim3(n), dim3(kRowThreads), 0, s, a, w, u, token, prob);
         }
-        if (probs) hipLaunchKernelGGL((probs_kernel<E, F32>), grid, block, 0, s, a, w, probs);
+        if (probs) hipLaunchKernelGGL((probs_kernel<F32>), grid, block, 0, s, a, w, probs);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
 }
 
-template <int E, bool F32>
+template <bool F32>
 hipError_t accept(const SampleArgs &a, const AcceptArgs &c, hipStream_t s) {
     const Layout l = layout(a.T, a.V);
     const Work w = work_of(a, l);
-    hipError_t e = rows<E, F32>(a, w, l, c.q ? nullptr : c.u, c.q ? nullptr : w.drawn, nullptr, nullptr, s);
+    hipError_t e = rows<F32>(a, w, l, c.q ? nullptr : c.u, c.q ? nullptr : w.drawn, nullptr, nullptr, s);
     if (e != hipSuccess) return e;
     if (c.q)
-        hipLaunchKernelGGL((chain_kernel<E, F32>), dim3(l.C, c.nseq), dim3(kRowThreads), 0, s, a, c, w);
+        hipLaunchKernelGGL((chain_kernel<F32>), dim3(l.C, c.nseq), dim3(kRowThreads), 0, s, a, c, w);
     else
         hipLaunchKernelGGL(match_kernel, dim3(1), dim3(64), 0, s, c, w.drawn);
     return hipGetLastError();
 }
-
-template <typename F>
-hipError_t by_type(const SampleArgs &a, F f) {
-    switch (layout(a.T, a.V).E) {
-        case 1: return a.f32 ? f.template operator()<1, true>() : f.template operator()<1, false>();
-        case 2: return a.f32 ? f.template operator()<2, true>() : f.template operator()<2, false>();
-        default: return a.f32 ? f.template operator()<4, true>() : f.template operator()<4, false>();
-    }
-}
-
-struct SampleCall {
-    const SampleArgs &a;
-    const float *u;
-    int32_t *token;
-    float *prob, *probs;
-    hipStream_t s;
-    template <int E, bool F32>
-    hipError_t operator()() const {
-        const Layout l = layout(a.T, a.V);
-        return rows<E, F32>(a, work_of(a, l), l, u, token, prob, probs, s);
-    }
-};
-
-struct AcceptCall {
-    const SampleArgs &a;
-    const AcceptArgs &c;
-    hipStream_t s;
-    template <int E, bool F32>
-    hipError_t operator()() const {
-        return accept<E, F32>(a, c, s);
-    }
-};
 
 }  // namespace
 
 size_t sample_ws_bytes(int T, int V) { return layout(T > 0 ? T : 1, V).total; }
 
 hipError_t launch_sample(const SampleArgs &a, const float *u, int32_t *token, float *prob, float *probs, hipStream_t s) {
-    return by_type(a, SampleCall{a, u, token, prob, probs, s});
+    const Layout l = layout(a.T, a.V);
+    const Work w = work_of(a, l);
+    return a.f32 ? rows<true>(a, w, l, u, token, prob, probs, s) : rows<false>(a, w, l, u, token, prob, probs, s);
 }
 
 hipError_t launch_accept(const SampleArgs &a, const AcceptArgs &c, hipStream_t s) {
-    return by_type(a, AcceptCall{a, c, s});
+    return a.f32 ? accept<true>(a, c, s) : accept<false>(a, c, s);
 }
 
 }  // namespace moe
