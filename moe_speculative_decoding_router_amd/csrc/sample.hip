@@ -12,7 +12,7 @@
 // sum relative to it, one pass over the logits) and join_kernel (a workgroup
 // a row: the chunk that holds the draw, then the token).  With filters:
 //   max_kernel      the row's largest value
-//   hist_kernel     a histogram of the distance from it (1 / 32 nat a bin): the
+//   hist_kernel     a histogram of the distance from it (1 / 64 nat a bin): the
 //                   bins above which every token is kept, and the few that
 //                   the thresholds lie in (top-k, top-p)
 //   gather_kernel   sums of the kept, a list of the tokens in those few bins
@@ -31,7 +31,11 @@ constexpr int kRowThreads = 512;         // of those with a workgroup a row
 constexpr int kChunk = 4096;             // tokens
 constexpr int kRowWaves = kRowThreads / 64;
 constexpr int kMaxChunks = 64;           // of a row of 2^18 tokens: a lane each
-constexpr int kBins = 1024;              // the last holds all that lies beyond
+constexpr int kHistThreads = 1024;       // of hist_kernel, which takes kHistChunks chunks
+constexpr int kHistChunks = 4;
+constexpr int kBins = 2048;              // the last holds all that lies beyond
+constexpr double kBinsPerNat = 64.0;
+constexpr int kGroups = kChunk / 256;
 constexpr int kList = 8192;              // tokens in the bins of the thresholds
 constexpr double kUnit = 35184372088832.0;         // 2^45
 constexpr double kUnitP = 2251799813685248.0;       // 2^51, of probabilities (their sum is 1)
@@ -107,6 +111,8 @@ __device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) {
     return v;
 }
 
+__device__ __forceinline__ int wave_scan_i32(int v) { return wave_incl_scan(v); }
+
 __device__ __forceinline__ uint64_t wave_scan_u64(uint64_t v) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
@@ -117,12 +123,12 @@ __device__ __forceinline__ uint64_t wave_scan_u64(uint64_t v) {
     return v;
 }
 
-// Block of kRowThreads: the lowest index whose running sum of f(i) exceeds
+// Block of NT threads: the lowest index whose running sum of f(i) exceeds
 // `want(total)`; -1 if the total is 0.  Each wave owns a contiguous part.
-template <typename F, typename W>
+template <int NT, typename F, typename W>
 __device__ int pick(int V, F f, W want, uint64_t *sums, int *found, uint64_t *total_out) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int per = (((V + kRowWaves - 1) / kRowWaves) + 63) & ~63;
+    const int per = (((V + (NT / 64) - 1) / (NT / 64)) + 63) & ~63;
     const int b = wave * per, e = min(V, b + per);
     uint64_t s = 0;
     for (int i = b + lane; i < e; i += 64) s += f(i);
@@ -132,7 +138,7 @@ __device__ int pick(int V, F f, W want, uint64_t *sums, int *found, uint64_t *to
     __syncthreads();
     uint64_t total = 0, before = 0;
 #pragma unroll
-    for (int w = 0; w < kRowWaves; ++w) {
+    for (int w = 0; w < (NT / 64); ++w) {
         if (w < wave) before += sums[w];
         total += sums[w];
     }
@@ -168,7 +174,7 @@ __device__ __forceinline__ uint64_t target(float u, uint64_t total) {
 struct Histogram {
     unsigned cnt[2048];
     unsigned long long mass[2048];
-    uint64_t wsum[kRowWaves], wcnt[kRowWaves];
+    uint64_t wsum[16], wcnt[16];  // a wave each
     // the found bin: what lies above it
     unsigned bin;
     uint64_t above_cnt, above_mass;
@@ -177,7 +183,7 @@ struct Histogram {
 // Radix descent over the keys from the top: the bin, key after key, in which
 // the running count (by_count) or the running weight of the ranking reaches
 // `want`.  Leaves the key, and the count and weight strictly above it.
-template <bool F32>
+template <int NT, bool F32>
 __device__ void descend(const ExpTable &et, const void *row, int V, float first, double invt, bool by_count, uint64_t want, Histogram &h,
                         unsigned &key, uint64_t &above_cnt, uint64_t &above_mass) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -186,9 +192,9 @@ __device__ void descend(const ExpTable &et, const void *row, int V, float first,
 #pragma unroll
     for (int level = 0; level < 3; ++level) {
         const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bits = level == 2 ? 10 : 11;
-        for (int i = tid; i < 2048; i += kRowThreads) h.cnt[i] = 0, h.mass[i] = 0;
+        for (int i = tid; i < 2048; i += NT) h.cnt[i] = 0, h.mass[i] = 0;
         __syncthreads();
-        for (int i = tid; i < V; i += kRowThreads) {
+        for (int i = tid; i < V; i += NT) {
             const float x = value<F32>(row, i);
             const unsigned k = key_of(x);
             if (k == 0 || (level && (k >> (shift + bits)) != prefix)) continue;
@@ -198,7 +204,7 @@ __device__ void descend(const ExpTable &et, const void *row, int V, float first,
         }
         __syncthreads();
         // thread t owns 4 bins, the first thread the highest
-        constexpr int kOwn = 2048 / kRowThreads;
+        constexpr int kOwn = 2048 / NT;
         const int b0 = 2047 - kOwn * tid;
         uint64_t cs = 0, ms = 0;
 #pragma unroll
@@ -251,9 +257,11 @@ struct Header {
     int hist_done, chain_done, listed, pad;
 };
 
-// hist_kernel's result: bins below `sure` are kept, those up to `end` listed.
+// hist_kernel's result: bins below `sure` are kept, tokens up to bin `end`
+// with a key of at least `cut` listed.
 struct Plan {
-    int sure, end, slow, pad;
+    int sure, end, slow;
+    unsigned cut;
     uint64_t above_mass, mass;  // of the sure bins, of all
 };
 
@@ -263,6 +271,7 @@ struct Work {
     int32_t *drawn;    // [T]
     unsigned *kmax;    // [rows][C] largest key
     int *count;        // [rows][C] tokens with a key
+    unsigned *group;   // [rows][C][kGroups] largest keys of 256 tokens each
     uint64_t *sum;     // [rows][C]
     Header *head;      // [rows]
     Plan *plan;        // [rows]
@@ -270,7 +279,7 @@ struct Work {
     unsigned *hcnt;    // [rows][H][kBins]
     uint64_t *hmass;   // [rows][H][kBins]
     int row0, C;
-    int E, H;          // chunks of a histogram, histograms of a row
+    int H;             // histograms of a row
     int L;             // entries of a list, min(kList, V) at least
 };
 
@@ -293,26 +302,29 @@ __device__ __forceinline__ bool last_of(int *done, int n, int *sh) {
     return *sh != 0;
 }
 
-// 4 consecutive values from token i of a row on; -inf past its end.  Rows
-// begin at any element, so the load is unaligned.
+// 16 bytes of consecutive tokens a load: 4 float32 or 8 bf16.  Rows begin at
+// any element, so the load is unaligned; -inf past the row's end.
+template <bool F32>
+constexpr int kVec = F32 ? 4 : 8;
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
-typedef u32x2 u32x2_any __attribute__((aligned(2)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
 
 template <bool F32>
-__device__ __forceinline__ void load4(const void *row, int i, int V, float (&x)[4]) {
-    if (i + 4 <= V) {
-        if (F32) {
+__device__ __forceinline__ void load_tokens(const void *row, int i, int V, float (&x)[kVec<F32>]) {
+    if (i + kVec<F32> <= V) {
+        if constexpr (F32) {
             const f32x4 v = *reinterpret_cast<const f32x4_any *>((const float *)row + i);
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[e] = v[e];
         } else {
-            const u32x2 v = *reinterpret_cast<const u32x2_any *>((const uint16_t *)row + i);
+            const u32x4 v = *reinterpret_cast<const u32x4_any *>((const uint16_t *)row + i);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(e & 1 ? v[e >> 1] & 0xffff0000u : v[e >> 1] << 16);
+            for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(e & 1 ? v[e >> 1] & 0xffff0000u : v[e >> 1] << 16);
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = i + e < V ? (F32 ? ((const float *)row)[i + e] : bf16_to_f32(((const uint16_t *)row)[i + e])) : -INFINITY;
+        for (int e = 0; e < kVec<F32>; ++e)
+            x[e] = i + e < V ? (F32 ? ((const float *)row)[i + e] : bf16_to_f32(((const uint16_t *)row)[i + e])) : -INFINITY;
     }
 }
 
@@ -321,21 +333,24 @@ __device__ __forceinline__ const void *row_of(const SampleArgs &a, int t) {
     return (const char *)a.logits + (size_t)t * a.stride * (F32 ? 4 : 2);
 }
 
-// A chunk by NT threads: thread tid holds tokens token_at(c, e) .. + 3.
-template <int NT>
-__device__ __forceinline__ int token_at(int c, int e) {
-    return c * kChunk + 4 * (e * NT + (int)threadIdx.x);
-}
-
+// N consecutive tokens by NT threads in rounds of kVec tokens a thread:
+// thread tid holds tokens token_at(first, e) .. of round e.
 template <int NT, bool F32>
-__device__ __forceinline__ void load_chunk(const SampleArgs &a, int t, int c, float (&x)[kChunk / 4 / NT][4]) {
+__device__ __forceinline__ int token_at(int first, int e) {
+    return first + kVec<F32> * (e * NT + (int)threadIdx.x);
+}
+template <int NT, bool F32, int N = kChunk>
+constexpr int kRounds = N / kVec<F32> / NT;
+
+template <int NT, bool F32, int E>
+__device__ __forceinline__ void load_block(const SampleArgs &a, int t, int first, float (&x)[E][kVec<F32>]) {
     const void *row = row_of<F32>(a, t);
 #pragma unroll
-    for (int e = 0; e < kChunk / 4 / NT; ++e) load4<F32>(row, token_at<NT>(c, e), a.V, x[e]);
+    for (int e = 0; e < E; ++e) load_tokens<F32>(row, token_at<NT, F32>(first, e), a.V, x[e]);
 #pragma unroll
-    for (int e = 0; e < kChunk / 4 / NT; ++e)
+    for (int e = 0; e < E; ++e)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[e][i] = clean(x[e][i]);
+        for (int i = 0; i < kVec<F32>; ++i) x[e][i] = clean(x[e][i]);
 }
 
 __device__ __forceinline__ unsigned wave_max_u32(unsigned v) {
@@ -383,18 +398,18 @@ __device__ __forceinline__ int lane_of_mass(uint64_t m, uint64_t want, uint64_t 
 // threads, all of which get it.
 template <int NT, bool F32, typename F>
 __device__ int find_in_chunk(const SampleArgs &a, int t, int c, uint64_t want, F f, uint64_t *sums, int *found) {
-    constexpr int E = kChunk / 4 / NT, W = NT / 64;
-    static_assert(E * W <= 64, "a part a lane");
+    constexpr int E = kRounds<NT, F32>, Q = kVec<F32>, W = NT / 64;
+    static_assert(E >= 1 && E * W <= 64, "a part a lane");
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    float x[E][4];
-    load_chunk<NT, F32>(a, t, c, x);
+    float x[E][Q];
+    load_block<NT, F32>(a, t, c * kChunk, x);
     int last = -1;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         uint64_t s = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int at = token_at<NT>(c, e) + i;
+        for (int i = 0; i < Q; ++i) {
+            const int at = token_at<NT, F32>(c * kChunk, e) + i;
             const uint64_t m = at < a.V ? f(x[e][i], at) : 0;
             if (m) last = at;
             s += m;
@@ -409,19 +424,24 @@ __device__ int find_in_chunk(const SampleArgs &a, int t, int c, uint64_t want, F
     if (part < 0) {
         atomicMax(found, last);
     } else if (part % W == wave) {
-        float y[4];
-        const int at = token_at<NT>(c, part / W);
-        load4<F32>(row_of<F32>(a, t), at, a.V, y);
-        uint64_t m[4], s = 0;
+        float y[Q];
+        const int at = token_at<NT, F32>(c * kChunk, part / W);
+        load_tokens<F32>(row_of<F32>(a, t), at, a.V, y);
+        uint64_t m[Q], s = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < Q; ++i) {
             m[i] = at + i < a.V ? f(clean(y[i]), at + i) : 0;
             s += m[i];
         }
-        const uint64_t b0 = run + wave_scan_u64(s) - s;
-        if (b0 <= want && want < b0 + s) {
-            const uint64_t b1 = b0 + m[0], b2 = b1 + m[1], b3 = b2 + m[2];
-            *found = at + (want < b1 ? 0 : want < b2 ? 1 : want < b3 ? 2 : 3);
+        uint64_t b = run + wave_scan_u64(s) - s;
+        if (b <= want && want < b + s) {
+            int to = -1;
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                b += m[i];
+                if (to < 0 && want < b) to = at + i;
+            }
+            *found = to;
         }
     }
     __syncthreads();
@@ -442,27 +462,27 @@ __device__ __forceinline__ void finish_row(const SampleArgs &a, const ExpTable &
 // ---------------------------------------------------------------------------
 template <bool F32>
 __global__ __launch_bounds__(kThreads) void part_kernel(SampleArgs a, Work w) {
-    constexpr int E = kChunk / 4 / kThreads;
+    constexpr int E = kRounds<kThreads, F32>, Q = kVec<F32>;
     __shared__ ExpTable et;
     __shared__ unsigned sk[kThreads / 64];
     __shared__ uint64_t ss[kThreads / 64];
     const int c = blockIdx.x, t = w.row0 + blockIdx.y;
-    float x[E][4];
-    load_chunk<kThreads, F32>(a, t, c, x);
+    float x[E][Q];
+    load_block<kThreads, F32>(a, t, c * kChunk, x);
     const Filter f = filter_of(a, t);
     et.fill();
     float v = -INFINITY;
 #pragma unroll
     for (int e = 0; e < E; ++e)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v = fmaxf(v, x[e][i]);
+        for (int i = 0; i < Q; ++i) v = fmaxf(v, x[e][i]);
     const unsigned k = block_max_u32<kThreads>(key_of(v), sk);
     const float top = of_key(k);
     uint64_t s = 0;
 #pragma unroll
     for (int e = 0; e < E; ++e)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < Q; ++i)
             if (x[e][i] != -INFINITY) s += f.one ? (uint64_t)(x[e][i] == top) : units(weight(et, x[e][i], top, f.invt));
     s = block_sum_u64<kThreads>(s, ss);
     if (threadIdx.x == 0) {
@@ -525,29 +545,53 @@ __global__ __launch_bounds__(kThreads) void join_kernel(SampleArgs a, Work w, co
 // ---------------------------------------------------------------------------
 // With filters
 // ---------------------------------------------------------------------------
+// Largest keys of the chunk and of its groups (16 lanes each), and for rows
+// with top_p alone the sum of its weights relative to its largest value.
 template <bool F32>
 __global__ __launch_bounds__(kThreads) void max_kernel(SampleArgs a, Work w) {
-    constexpr int E = kChunk / 4 / kThreads;
+    constexpr int E = kRounds<kThreads, F32>, Q = kVec<F32>;
+    static_assert(E * Q * 16 == 256, "a group of 256 tokens");
+    __shared__ ExpTable et;
     __shared__ unsigned sk[kThreads / 64];
     __shared__ uint64_t sn[kThreads / 64];
-    const int c = blockIdx.x, t = w.row0 + blockIdx.y;
-    float x[E][4];
-    load_chunk<kThreads, F32>(a, t, c, x);
+    const int c = blockIdx.x, t = w.row0 + blockIdx.y, tid = threadIdx.x;
+    float x[E][Q];
+    load_block<kThreads, F32>(a, t, c * kChunk, x);
+    const Filter f = filter_of(a, t);
+    const bool sums = f.topp < 1.f && !f.one;
+    if (sums) et.fill();
     float v = -INFINITY;
     int n = 0;
 #pragma unroll
     for (int e = 0; e < E; ++e)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < Q; ++i) {
             v = fmaxf(v, x[e][i]);
             n += x[e][i] != -INFINITY;
         }
+    v = fmaxf(v, dpp_ror<8>(v));
+    v = fmaxf(v, dpp_ror<4>(v));
+    v = fmaxf(v, dpp_ror<2>(v));
+    v = fmaxf(v, dpp_ror<1>(v));
+    const int at = blockIdx.y * w.C + c;
+    if ((tid & 15) == 0) w.group[at * kGroups + (tid >> 4)] = key_of(v);
     const unsigned k = block_max_u32<kThreads>(key_of(v), sk);
-    const uint64_t all = block_sum_u64<kThreads>((uint64_t)n, sn);
-    if (threadIdx.x == 0) {
-        w.kmax[blockIdx.y * w.C + c] = k;
-        w.count[blockIdx.y * w.C + c] = (int)all;
+    uint64_t all = block_sum_u64<kThreads>((uint64_t)n, sn);
+    if (tid == 0) {
+        w.kmax[at] = k;
+        w.count[at] = (int)all;
         if (c == 0) w.head[blockIdx.y] = Header{0, 0, 0, 0};
+    }
+    if (sums) {
+        const float top = of_key(k);
+        uint64_t s = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+            for (int i = 0; i < Q; ++i)
+                if (x[e][i] != -INFINITY) s += units(weight(et, x[e][i], top, f.invt));
+        s = block_sum_u64<kThreads>(s, sn);
+        if (tid == 0) w.sum[at] = s;
     }
 }
 
@@ -567,105 +611,186 @@ __device__ __forceinline__ Kind kind_of(const Filter &f, const Work &w, int row)
     return k;
 }
 
-__device__ __forceinline__ int bin_of(float x, float first, double invt) {
-    return min((int)(((double)first - (double)x) * invt * 32.0), kBins - 1);
+// Bin of a token's distance from the first, in float32: all that is asked of
+// it is that it never falls while the value does.
+__device__ __forceinline__ float bin_scale(double invt) { return (float)fmin(invt * kBinsPerNat, 1e30); }
+
+__device__ __forceinline__ int bin_of(float x, float first, float scale) {
+    return min((int)((first - x) * scale), kBins - 1);
 }
 
-// The weights of the last bin are below 2^-45 / 2 and have no units, so a
-// top-p threshold never lies in it.  A workgroup takes w.E chunks.
-template <bool F32>
-__global__ __launch_bounds__(kThreads) void hist_kernel(SampleArgs a, Work w) {
-    constexpr int E = kChunk / 4 / kThreads, B = kBins / kThreads;
-    __shared__ ExpTable et;
-    __shared__ unsigned cnt[kBins];
-    __shared__ unsigned long long mass[kBins];
-    __shared__ uint64_t wc[kThreads / 64], wm[kThreads / 64];
-    __shared__ int sh;
-    const int hc = blockIdx.x, row = blockIdx.y, t = w.row0 + row, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const Filter f = filter_of(a, t);
-    const Kind kind = kind_of(f, w, row);
-    if (!kind.by_k && !kind.by_p) return;  // the whole row's workgroups
-    et.fill();
+// Which tokens can be left out of the search for a threshold.
+//   top_p: tokens of weight below (1 - top_p) / V of the row's sum hold less
+//   than 1 - top_p of it together, so the threshold lies above them (half of
+//   that here, for the roundings).  Returns the distance in nats.
+__device__ __forceinline__ double cut_distance(const Filter &f, double mass, int V) {
+    return log(2.0 * V * kUnit / ((1.0 - (double)f.topp) * mass));
+}
+
+__device__ __forceinline__ unsigned cut_key(float first, double invt, double nats) {
+    const double x = (double)first - nats / invt * 1.000001;  // invt = 0: every token weighs the same
+    return invt > 0.0 && x > -3.4e38 ? key_of(clean((float)x)) : 1u;
+}
+
+//   top_k: the k-th largest of any set of tokens, one of each of some groups,
+//   is no larger than the k-th largest of all.  The largest key with at least
+//   k of the block's keys (one a thread, NT threads) at or above it, found bit
+//   by bit from the top; the low bits are left 0.
+template <int NT>
+__device__ unsigned key_of_rank(unsigned key, int k, int *sh) {
+    unsigned cut = 0;
+    for (int bit = 31; bit >= 14; --bit) {
+        const unsigned c = cut | (1u << bit);
+        const int n = __popcll(__ballot(key >= c));
+        if ((threadIdx.x & 63) == 0) sh[(bit & 1) * (NT / 64) + (threadIdx.x >> 6)] = n;
+        __syncthreads();
+        int all = 0;
 #pragma unroll
-    for (int y = 0; y < B; ++y) cnt[y * kThreads + tid] = 0, mass[y * kThreads + tid] = 0;
-    __syncthreads();
-    const float first = of_key(kind.km);
-    for (int c = hc * w.E; c < min(w.C, (hc + 1) * w.E); ++c) {
-        float x[E][4];
-        load_chunk<kThreads, F32>(a, t, c, x);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (x[e][i] == -INFINITY) continue;
-                const int b = bin_of(x[e][i], first, f.invt);
-                if (b == kBins - 1) continue;
-                atomicAdd(&cnt[b], 1u);
-                if (!kind.by_k) atomicAdd(&mass[b], (unsigned long long)units(weight(et, x[e][i], first, f.invt)));
-            }
+        for (int i = 0; i < NT / 64; ++i) all += sh[(bit & 1) * (NT / 64) + i];
+        if (all >= k) cut = c;
     }
     __syncthreads();
-    const size_t at = (size_t)row * w.H * kBins;
-#pragma unroll
-    for (int y = 0; y < B; ++y) {
-        const int b = y * kThreads + tid;
-        put(w.hcnt + at + hc * kBins + b, cnt[b]);
-        if (!kind.by_k) put(w.hmass + at + hc * kBins + b, (uint64_t)mass[b]);
-    }
-    if (!last_of(&w.head[row].hist_done, w.H, &sh)) return;
-    // the row's histogram: thread tid joins bins tid, tid + 256, ..., then owns B consecutive ones
-#pragma unroll
-    for (int y = 0; y < B; ++y) {
-        const int b = y * kThreads + tid;
-        unsigned n = 0;
-        uint64_t m = 0;
-#pragma unroll 4
-        for (int i = 0; i < w.H; ++i) {
-            n += get(w.hcnt + at + i * kBins + b);
-            if (!kind.by_k) m += get(w.hmass + at + i * kBins + b);
-        }
-        cnt[b] = n;
-        mass[b] = m;
-    }
+    return max(cut, 1u);
+}
+
+// The bins' shared memory; where a row's histogram is searched, 1024 threads
+// of a block own two bins each.
+struct Bins {
+    unsigned cnt[kBins];
+    unsigned long long mass[kBins];
+    uint64_t wc[16], wm[16];
+    Plan plan;
+};
+
+__device__ __forceinline__ void clear_bins(Bins &h, int nt) {
+    for (int b = threadIdx.x; b < kBins; b += nt) h.cnt[b] = 0, h.mass[b] = 0;
+}
+
+// Tokens below `cut` are left out, and so is the last bin; a threshold in them
+// is seen by its absence.  The weights of the last bin are below 2^-45 / 2 and
+// have no units, so a top-p threshold never lies there.
+__device__ __forceinline__ void count_token(Bins &h, const Kind &kind, float x, unsigned cut, float first, float scale,
+                                            double invt, const ExpTable &et) {
+    const int b = bin_of(x, first, scale);
+    if (b == kBins - 1 || key_of(x) < cut) return;
+    atomicAdd(&h.cnt[b], 1u);
+    if (!kind.by_k) atomicAdd(&h.mass[b], (unsigned long long)units(weight(et, x, first, invt)));
+}
+
+// The plan of a whole row's histogram, by 1024 threads; the block gets it in
+// h.plan.  `mass`: the row's sum, for top_p alone; `cut`: the least key counted.
+__device__ void plan_row(Bins &h, const Filter &f, const Kind &kind, uint64_t mass, unsigned cut) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const uint64_t n0 = h.cnt[2 * tid], n1 = h.cnt[2 * tid + 1];
+    const uint64_t m0 = kind.by_k ? 0 : h.mass[2 * tid], m1 = kind.by_k ? 0 : h.mass[2 * tid + 1];
+    uint64_t nb = (uint64_t)wave_scan_i32((int)(n0 + n1)) - n0 - n1;  // counts are below 2^18
+    uint64_t mb = kind.by_k ? 0 : wave_scan_u64(m0 + m1) - m0 - m1;
+    if (lane == 63) h.wc[wave] = nb + n0 + n1, h.wm[wave] = mb + m0 + m1;
+    if (tid == 0) h.plan = Plan{0, kBins - 1, 1, 1u, 0, mass};  // not among the counted
     __syncthreads();
-    uint64_t n = 0, m = 0;
 #pragma unroll
-    for (int y = 0; y < B; ++y) n += cnt[B * tid + y], m += mass[B * tid + y];
-    uint64_t nb = wave_scan_u64(n) - n, mb = kind.by_k ? 0 : wave_scan_u64(m) - m;
-    if (lane == 63) wc[wave] = nb + n, wm[wave] = mb + m;
-    __syncthreads();
-    uint64_t total = 0, counted = 0;
+    for (int i = 0; i < 16; ++i)
+        if (i < wave) nb += h.wc[i], mb += h.wm[i];
+    const uint64_t want = kind.by_k ? (uint64_t)f.topk : max((uint64_t)1, (uint64_t)ceil((double)f.topp * (double)mass));
 #pragma unroll
-    for (int i = 0; i < kThreads / 64; ++i) {
-        if (i < wave) nb += wc[i], mb += wm[i];
-        counted += wc[i];
-        total += wm[i];
-    }
-    const uint64_t want = kind.by_k ? (uint64_t)f.topk : max((uint64_t)1, (uint64_t)ceil((double)f.topp * (double)total));
-#pragma unroll
-    for (int y = 0; y < B; ++y) {
-        const uint64_t c = cnt[B * tid + y], v = mass[B * tid + y];
+    for (int y = 0; y < 2; ++y) {
+        const uint64_t c = y ? n1 : n0, v = y ? m1 : m0;
         const uint64_t lo = kind.by_k ? nb : mb, hi = lo + (kind.by_k ? c : v);
         if (lo < want && want <= hi) {
             Plan p;
-            p.sure = kind.by_k ? 0 : B * tid + y;  // by_k: the sum of the first top_k comes from the list
-            p.end = B * tid + y;
+            p.sure = kind.by_k ? 0 : 2 * tid + y;  // by_k: the sum of the first top_k comes from the list
+            p.end = 2 * tid + y;
             p.slow = (kind.by_k ? hi : c) > (uint64_t)kList;
-            p.pad = 0;
+            p.cut = cut;
             p.above_mass = mb;
-            p.mass = total;
-            w.plan[row] = p;
+            p.mass = mass;
+            h.plan = p;
         }
         nb += c;
         mb += v;
     }
-    // the threshold of top_k in the last bin
-    if (tid == 0 && kind.by_k && want > counted) w.plan[row] = Plan{0, kBins - 1, 1, 0, 0, 0};
+    __syncthreads();
+}
+
+// The row's sum from its chunks' (relative to their own largest values), in
+// units of the first's weight.
+__device__ __forceinline__ double row_mass(const ExpTable &et, const Work &w, int row, const Filter &f, unsigned km) {
+    const int lane = threadIdx.x & 63;
+    const unsigned kc = lane < w.C ? w.kmax[row * w.C + lane] : 0;
+    double v = kc ? (double)w.sum[row * w.C + lane] * weight(et, of_key(kc), of_key(km), f.invt) : 0.0;
+#pragma unroll
+    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+    return v;
 }
 
 template <bool F32>
+__global__ __launch_bounds__(kHistThreads) void hist_kernel(SampleArgs a, Work w) {
+    constexpr int E = kRounds<kHistThreads, F32, kHistChunks * kChunk>, Q = kVec<F32>;
+    __shared__ ExpTable et;
+    __shared__ Bins h;
+    __shared__ int sh, ranks[2 * kHistThreads / 64];
+    static_assert(kHistThreads == 1024 && kBins == 2048 && kMaxChunks * kGroups <= kHistThreads, "two bins, a group a thread");
+    const int hc = blockIdx.x, row = blockIdx.y, t = w.row0 + row, tid = threadIdx.x;
+    const Filter f = filter_of(a, t);
+    const Kind kind = kind_of(f, w, row);
+    if (!kind.by_k && !kind.by_p) return;  // the whole row's workgroups
+    // a small top_k against the groups: no histogram.  At 7 / 8 of the groups
+    // about 2 tokens a group lie above the cut.
+    if (kind.by_k && f.topk <= w.C * kGroups * 7 / 8 && f.topk <= kList / 4) {
+        if (hc) return;
+        const unsigned cut = key_of_rank<kHistThreads>(tid < w.C * kGroups ? w.group[row * w.C * kGroups + tid] : 0, f.topk, ranks);
+        if (tid == 0) w.plan[row] = Plan{0, kBins - 1, 0, cut, 0, 0};
+        return;
+    }
+    float x[E][Q];
+    load_block<kHistThreads, F32>(a, t, hc * kHistChunks * kChunk, x);
+    if (!kind.by_k) et.fill();
+    clear_bins(h, kHistThreads);
+    __syncthreads();
+    const float first = of_key(kind.km), scale = bin_scale(f.invt);
+    const uint64_t mass = kind.by_k ? 0 : (uint64_t)row_mass(et, w, row, f, kind.km);
+    const unsigned cut = kind.by_k ? 1u : cut_key(first, f.invt, cut_distance(f, (double)mass, a.V));
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+        for (int i = 0; i < Q; ++i)
+            if (x[e][i] != -INFINITY) count_token(h, kind, x[e][i], cut, first, scale, f.invt, et);
+    __syncthreads();
+    if (w.H > 1) {
+        const size_t at = (size_t)row * w.H * kBins;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const int b = y * kHistThreads + tid;
+            put(w.hcnt + at + hc * kBins + b, h.cnt[b]);
+            if (!kind.by_k) put(w.hmass + at + hc * kBins + b, (uint64_t)h.mass[b]);
+        }
+        if (!last_of(&w.head[row].hist_done, w.H, &sh)) return;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const int b = y * kHistThreads + tid;
+            unsigned n = 0;
+            uint64_t m = 0;
+#pragma unroll 4
+            for (int i = 0; i < w.H; ++i) {
+                n += get(w.hcnt + at + i * kBins + b);
+                if (!kind.by_k) m += get(w.hmass + at + i * kBins + b);
+            }
+            h.cnt[b] = n;
+            h.mass[b] = m;
+        }
+        __syncthreads();
+    }
+    plan_row(h, f, kind, mass, cut);
+    if (tid == 0) w.plan[row] = h.plan;
+}
+
+// List entries sort as the ranking does.
+__device__ __forceinline__ unsigned entry_key(uint64_t e) { return ~(unsigned)(e >> 32); }
+__device__ __forceinline__ uint64_t entry_of(float x, int i) { return ((uint64_t)~key_of(x) << 32) | (unsigned)i; }
+
+template <bool F32>
 __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a, Work w) {
-    constexpr int E = kChunk / 4 / kThreads;
+    constexpr int E = kRounds<kThreads, F32>, Q = kVec<F32>;
     __shared__ ExpTable et;
     __shared__ uint64_t sums[kThreads / 64];
     __shared__ int sh;
@@ -673,22 +798,22 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a, Work w) 
     const Filter f = filter_of(a, t);
     const Kind kind = kind_of(f, w, row);
     const bool planned = kind.by_k || kind.by_p;
-    Plan p{kBins, -1, 0, 0, 0, 0};
+    Plan p{kBins, -1, 0, 1u, 0, 0};
     if (planned) p = w.plan[row];
     if (p.slow) return;
-    float x[E][4];
-    load_chunk<kThreads, F32>(a, t, c, x);
+    float x[E][Q];
+    load_block<kThreads, F32>(a, t, c * kChunk, x);
     et.fill();
     if (tid == 0) sh = f.one ? INT_MAX : 0;
     __syncthreads();
-    const float first = of_key(kind.km);
+    const float first = of_key(kind.km), scale = bin_scale(f.invt);
     uint64_t sum = 0;
     if (f.one) {
 #pragma unroll
         for (int e = 0; e < E; ++e)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (kind.km && key_of(x[e][i]) == kind.km) atomicMin(&sh, token_at<kThreads>(c, e) + i);
+            for (int i = 0; i < Q; ++i)
+                if (kind.km && key_of(x[e][i]) == kind.km) atomicMin(&sh, token_at<kThreads, F32>(c * kChunk, e) + i);
         __syncthreads();
         sum = (uint64_t)sh;
     } else {
@@ -697,15 +822,15 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a, Work w) 
 #pragma unroll
         for (int e = 0; e < E; ++e)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < Q; ++i) {
                 if (x[e][i] == -INFINITY) continue;
-                const int b = planned ? bin_of(x[e][i], first, f.invt) : 0;
+                const int b = planned ? bin_of(x[e][i], first, scale) : 0;
                 if (b < p.sure) {
                     const double wt = weight(et, x[e][i], first, f.invt);
                     if (wt >= f.minp) sum += units(wt);
-                } else if (b <= p.end) {
+                } else if (b <= p.end && key_of(x[e][i]) >= p.cut) {
                     ++mine;
-                    in |= 1u << (4 * e + i);
+                    in |= 1u << (Q * e + i);
                 }
             }
         if (p.sure) sum = block_sum_u64<kThreads>(sum, sums);
@@ -720,10 +845,10 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a, Work w) 
 #pragma unroll
                 for (int e = 0; e < E; ++e)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if ((in >> (4 * e + i)) & 1 && at < w.L)
+                    for (int i = 0; i < Q; ++i)
+                        if ((in >> (Q * e + i)) & 1 && at < w.L)
                             w.list[(size_t)row * w.L + at++] =
-                                ((uint64_t)~key_of(x[e][i]) << 32) | (unsigned)(token_at<kThreads>(c, e) + i);
+                                entry_of(x[e][i], token_at<kThreads, F32>(c * kChunk, e) + i);
             }
         }
     }
@@ -731,16 +856,16 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a, Work w) 
 }
 
 // The row's filter by radix descent, by one workgroup.
-template <bool F32>
+template <int NT, bool F32>
 __device__ void descend_row(const ExpTable &et, const SampleArgs &a, const void *row, const Filter &f, const Kind &kind,
                             RowState &st, Histogram &h, uint64_t *sums, int *found) {
     uint64_t ca, ma, wk = 0, ties = 0;
     if (kind.by_k) {
-        descend<F32>(et, row, a.V, st.first, st.invt, true, (uint64_t)f.topk, h, st.key, ca, ma);
+        descend<NT, F32>(et, row, a.V, st.first, st.invt, true, (uint64_t)f.topk, h, st.key, ca, ma);
         ties = (uint64_t)f.topk - ca;
         wk = ma + ties * units(weight(et, of_key(st.key), st.first, st.invt));
     } else {
-        pick(
+        pick<NT>(
             a.V,
             [&](int i) {
                 const float x = value<F32>(row, i);
@@ -750,36 +875,152 @@ __device__ void descend_row(const ExpTable &et, const SampleArgs &a, const void 
     }
     if (kind.by_p) {
         const uint64_t want = min(max((uint64_t)1, (uint64_t)ceil((double)f.topp * (double)wk)), wk);
-        descend<F32>(et, row, a.V, st.first, st.invt, false, want, h, st.key, ca, ma);
+        descend<NT, F32>(et, row, a.V, st.first, st.invt, false, want, h, st.key, ca, ma);
         const uint64_t w = units(weight(et, of_key(st.key), st.first, st.invt));
         ties = (want - ma + w - 1) / w;
     }
     uint64_t total;
-    st.last = pick(
+    st.last = pick<NT>(
         a.V, [&](int i) { return (uint64_t)(key_of(value<F32>(row, i)) == st.key); },
         [&](uint64_t n) { return min(ties, n) - 1; }, sums, found, &total);
 }
 
-// Bitonic sort of `size` (a power of two >= 64) list entries, ascending:
-// key descending, index ascending.  Strides up to 64 stay inside the 128
-// entries of a wave and need no barrier of the block.
+// Bitonic sort of `size` (a power of two >= 64) list entries by NT threads,
+// ascending: key descending, index ascending.  Strides up to 64 stay inside
+// the 128 entries of a wave and need no barrier of the block.
+template <int NT>
 __device__ void sort_list(uint64_t *list, int size) {
     for (int k = 2; k <= size; k <<= 1)
         for (int j = k >> 1; j > 0; j >>= 1) {
             if (j > 64 || (j == 64 && k > 128)) __syncthreads();
-            for (int i = threadIdx.x; i < size / 2; i += kRowThreads) {
+            for (int i = threadIdx.x; i < size / 2; i += NT) {
                 const int lo = ((i & ~(j - 1)) << 1) | (i & (j - 1)), hi = lo | j;
                 const uint64_t x0 = list[lo], x1 = list[hi];
                 if ((x0 > x1) == ((lo & k) == 0)) list[lo] = x1, list[hi] = x0;
             }
-            __builtin_amdgcn_wave_barrier();
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
         }
     __syncthreads();
 }
 
-union DrawShared {
+struct ListShared {
     uint64_t list[kList];
+    unsigned long long sub[1024];
+    uint64_t ws[16];
+    unsigned klo[16], khi[16];
+    int n, kept;
+};
+
+// The threshold of a row from its list of n entries (in s.list, unsorted):
+// sets st.key and st.last and calls add(index, units) for every kept entry.
+// A list for top_p alone is first narrowed to those of 1024 equal parts of its
+// key range that the threshold lies in.
+template <int NT, typename Add>
+__device__ void resolve_list(ListShared &s, int n, const Filter &f, const Kind &kind, const Plan &p, const ExpTable &et,
+                             RowState &st, Add add) {
+    constexpr int W = NT / 64;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    auto weight_of = [&](uint64_t e) { return weight(et, of_key(entry_key(e)), st.first, f.invt); };
+    auto keep = [&](uint64_t e) {
+        const double w = weight_of(e);
+        if (w >= st.minp) add((int)(unsigned)e, units(w));
+    };
+    uint64_t above = p.above_mass;
+    const double share = (double)f.topp;
+    uint64_t want = max((uint64_t)1, (uint64_t)ceil(share * (double)p.mass));  // by_p alone
+    if (!kind.by_k && n > 256) {
+        unsigned lo = ~0u, hi = 0;
+        for (int i = tid; i < n; i += NT) {
+            const unsigned k = entry_key(s.list[i]);
+            lo = min(lo, k);
+            hi = max(hi, k);
+        }
+        for (int i = tid; i < 1024; i += NT) s.sub[i] = 0;
+        hi = wave_max_u32(hi);
+        lo = ~wave_max_u32(~lo);
+        if (lane == 0) s.klo[wave] = lo, s.khi[wave] = hi;
+        if (tid == 0) s.n = 0;
+        __syncthreads();
+        for (int i = 0; i < W; ++i) lo = min(lo, s.klo[i]), hi = max(hi, s.khi[i]);
+        // parts from the top; a key's part never falls while the key does
+        const float part = 1023.f / fmaxf((float)(hi - lo), 1.f);
+        auto part_of = [&](uint64_t e) { return min((int)((float)(hi - entry_key(e)) * part), 1023); };
+        for (int i = tid; i < n; i += NT) atomicAdd(&s.sub[part_of(s.list[i])], (unsigned long long)units(weight_of(s.list[i])));
+        __syncthreads();
+        constexpr int B = 1024 / NT;
+        uint64_t m = 0;
+#pragma unroll
+        for (int y = 0; y < B; ++y) m += s.sub[B * tid + y];
+        uint64_t run = above + wave_scan_u64(m) - m;
+        if (lane == 63) s.ws[wave] = run + m - above;
+        __syncthreads();
+        for (int i = 0; i < wave; ++i) run += s.ws[i];
+#pragma unroll
+        for (int y = 0; y < B; ++y) {
+            const uint64_t v = s.sub[B * tid + y];
+            if (run < want && want <= run + v) s.kept = B * tid + y, s.ws[W - 1] = run;  // the waves before are read
+            run += v;
+        }
+        __syncthreads();
+        const int at = s.kept;
+        above = s.ws[W - 1];
+        // entries above are kept, those of the part go on
+        uint64_t mine[kList / NT];
+#pragma unroll
+        for (int y = 0; y < kList / NT; ++y) mine[y] = y * NT + tid < n ? s.list[y * NT + tid] : ~0ull;
+        __syncthreads();
+#pragma unroll
+        for (int y = 0; y < kList / NT; ++y)
+            if (y * NT + tid < n) {
+                const int b = part_of(mine[y]);
+                if (b < at) keep(mine[y]);
+                if (b == at) s.list[atomicAdd(&s.n, 1)] = mine[y];
+            }
+        __syncthreads();
+        n = s.n;
+    }
+    int size = 64;
+    while (size < n) size <<= 1;
+    for (int i = n + tid; i < size; i += NT) s.list[i] = ~0ull;
+    __syncthreads();
+    sort_list<NT>(s.list, size);
+    // running weights of the list: thread tid holds `per` of them
+    const int per = (size + NT - 1) / NT, b = tid * per;
+    const int nk = kind.by_k ? min(f.topk, n) : n, e = min(b + per, nk);
+    if (tid == 0) s.kept = nk;
+    if (kind.by_p) {
+        uint64_t mine = 0;
+        for (int i = b; i < e; ++i) mine += units(weight_of(s.list[i]));
+        uint64_t incl = wave_scan_u64(mine), wk = 0;
+        if (lane == 63) s.ws[wave] = incl;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            if (i < wave) incl += s.ws[i];
+            wk += s.ws[i];
+        }
+        if (kind.by_k) want = max((uint64_t)1, (uint64_t)ceil(share * (double)wk));
+        uint64_t run = above + incl - mine;
+        if (run < want && want <= run + mine)
+            for (int i = b; i < e; ++i) {
+                run += units(weight_of(s.list[i]));
+                if (run >= want) {
+                    s.kept = i + 1;
+                    break;
+                }
+            }
+    }
+    __syncthreads();
+    const int kept = s.kept;
+    st.key = entry_key(s.list[kept - 1]);
+    st.last = (int)(unsigned)s.list[kept - 1];
+    for (int i = b; i < e && i < kept; ++i) keep(s.list[i]);
+    __syncthreads();
+}
+
+union DrawShared {
+    ListShared l;
     Histogram h;
 };
 
@@ -790,15 +1031,20 @@ __global__ __launch_bounds__(kRowThreads) void resolve_kernel(SampleArgs a, Work
     __shared__ uint64_t sums[kMaxChunks];
     __shared__ unsigned long long cs[kMaxChunks];
     __shared__ int found;
-    const int row = blockIdx.x, t = w.row0 + row, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int row = blockIdx.x, t = w.row0 + row, tid = threadIdx.x, lane = tid & 63;
+    // everything that does not wait for anything else first
+    const uint64_t mine = tid < w.C ? w.sum[row * w.C + tid] : 0;
+    const uint64_t head = w.list[(size_t)row * w.L + min(tid, w.L - 1)];  // most lists end in it; not read past their length
+    int n = w.head[row].listed;
+    Plan p = w.plan[row];
+    const float uu = u ? u[t] : 0.f;
     const Filter f = filter_of(a, t);
     const Kind kind = kind_of(f, w, row);
     const bool planned = kind.by_k || kind.by_p;
-    const float uu = u ? u[t] : 0.f;
-    Plan p{kBins, -1, 0, 0, 0, 0};
-    if (planned) p = w.plan[row];
+    if (!planned) p = Plan{kBins, -1, 0, 1u, 0, 0};
+    if (planned && n > kList) p.slow = 1;  // tied rows: the cut let too many through
     et.fill();
-    if (tid < kMaxChunks) cs[tid] = tid < w.C && !p.slow ? w.sum[row * w.C + tid] : 0;
+    if (tid < kMaxChunks) cs[tid] = p.slow ? 0 : mine;
     RowState st{f.invt, f.one ? 0.0 : f.minp, of_key(kind.km), 1u, a.V, -1, 0.0};
     float x = 0.f;
     const void *r = row_of<F32>(a, t);
@@ -813,59 +1059,20 @@ __global__ __launch_bounds__(kRowThreads) void resolve_kernel(SampleArgs a, Work
         st.last = st.token = lo;
         st.sum = kUnit;
     } else if (p.slow) {
-        descend_row<F32>(et, a, r, f, kind, st, s.h, sums, &found);
+        descend_row<kRowThreads, F32>(et, a, r, f, kind, st, s.h, sums, &found);
         uint64_t total;
-        st.token = pick(
+        st.token = pick<kRowThreads>(
             a.V, [&](int i) { return units(kept_weight(et, st, value<F32>(r, i), i)); },
             [&](uint64_t total) { return target(uu, total); }, sums, &found, &total);
         st.sum = (double)total;
     } else {
         if (planned) {
-            const int n = min(w.head[row].listed, w.L);
-            int size = 64;
-            while (size < n) size <<= 1;
-            for (int i = tid; i < size; i += kRowThreads) s.list[i] = i < n ? w.list[(size_t)row * w.L + i] : ~0ull;
+            n = min(n, w.L);  // V <= L where that is below kList
+            if (tid < n) s.l.list[tid] = head;
+            for (int i = kRowThreads + tid; i < n; i += kRowThreads) s.l.list[i] = w.list[(size_t)row * w.L + i];
             __syncthreads();
-            sort_list(s.list, size);
-            // running weights of the list: thread tid holds `per` of them
-            const int per = (size + kRowThreads - 1) / kRowThreads, b = tid * per;
-            auto weight_at = [&](int i) { return weight(et, of_key(~(unsigned)(s.list[i] >> 32)), st.first, f.invt); };
-            const int nk = kind.by_k ? min(f.topk, n) : n, e = min(b + per, nk);
-            uint64_t mine = 0;
-            if (kind.by_p)
-                for (int i = b; i < e; ++i) mine += units(weight_at(i));
-            if (tid == 0) found = nk;
-            if (kind.by_p) {
-                uint64_t incl = wave_scan_u64(mine), wk = 0;
-                if (lane == 63) sums[wave] = incl;
-                __syncthreads();
-#pragma unroll
-                for (int i = 0; i < kRowWaves; ++i) {
-                    if (i < wave) incl += sums[i];
-                    wk += sums[i];
-                }
-                // how many of the list are kept
-                const uint64_t whole = kind.by_k ? wk : p.mass;
-                const uint64_t want = max((uint64_t)1, (uint64_t)ceil((double)f.topp * (double)whole));
-                uint64_t run = p.above_mass + incl - mine;
-                if (run < want && want <= run + mine)
-                    for (int i = b; i < e; ++i) {
-                        run += units(weight_at(i));
-                        if (run >= want) {
-                            found = i + 1;
-                            break;
-                        }
-                    }
-            }
-            __syncthreads();
-            const int kept = found;
-            st.key = ~(unsigned)(s.list[kept - 1] >> 32);
-            st.last = (int)(unsigned)s.list[kept - 1];
-            for (int i = b; i < e && i < kept; ++i) {
-                const double wt = weight_at(i);
-                if (wt >= st.minp) atomicAdd(&cs[(unsigned)s.list[i] / kChunk], (unsigned long long)units(wt));
-            }
-            __syncthreads();
+            resolve_list<kRowThreads>(s.l, n, f, kind, p, et, st,
+                                      [&](int i, uint64_t m) { atomicAdd(&cs[i / kChunk], (unsigned long long)m); });
         }
         const uint64_t mc = cs[lane], total = wave_sum_u64(mc);
         const uint64_t want = target(uu, total);
@@ -880,15 +1087,186 @@ __global__ __launch_bounds__(kRowThreads) void resolve_kernel(SampleArgs a, Work
 }
 
 // ---------------------------------------------------------------------------
+// Rows of up to 32768 tokens: the row in the registers of one workgroup, all
+// of the above in one launch, where launches and passes over the caches cost
+// more than the arithmetic of one compute unit.
+// ---------------------------------------------------------------------------
+constexpr int kSmallThreads = 1024;
+constexpr int kSmall = 32 * kSmallThreads;
+
+union SmallShared {
+    Bins b;
+    ListShared l;
+    Histogram h;
+};
+
+// R: tokens a thread.
+template <int R, bool F32>
+__global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowState *states, Header *head, const float *u,
+                                                              int32_t *token, float *prob) {
+    constexpr int NT = kSmallThreads, W = NT / 64, Q = kVec<F32>, E = R / Q;
+    __shared__ ExpTable et;
+    __shared__ SmallShared s;
+    __shared__ uint64_t sums[E * W > W ? E * W : W];
+    __shared__ unsigned sk[W];
+    __shared__ int sn[W], ranks[2 * W], found;
+    const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const void *r = row_of<F32>(a, t);
+    float x[E][Q];
+    load_block<NT, F32>(a, t, 0, x);
+    const Filter f = filter_of(a, t);
+    const float uu = u ? u[t] : 0.f;
+    et.fill();
+    float v = -INFINITY;
+    int nv = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            v = fmaxf(v, x[e][i]);
+            nv += x[e][i] != -INFINITY;
+        }
+    nv = wave_sum_int(nv);
+    if (lane == 0) sn[wave] = nv;
+    Kind kind;
+    const unsigned mykey = key_of(v);
+    kind.km = block_max_u32<NT>(mykey, sk);
+    nv = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) nv += sn[i];
+    kind.by_k = !f.one && f.topk > 0 && f.topk < nv;
+    kind.by_p = !f.one && f.topp < 1.f && kind.km;
+    RowState st{f.invt, f.one ? 0.0 : f.minp, of_key(kind.km), 1u, a.V, -1, 0.0};
+    auto at = [&](int e, int i) { return token_at<NT, F32>(0, e) + i; };
+    if (kind.km && f.one) {
+        if (tid == 0) found = INT_MAX;
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+            for (int i = 0; i < Q; ++i)
+                if (key_of(x[e][i]) == kind.km) atomicMin(&found, at(e, i));
+        __syncthreads();
+        st.key = kind.km;
+        st.last = st.token = found;
+        st.sum = kUnit;
+    } else if (kind.km) {
+        if (kind.by_k || kind.by_p) {
+            Plan p{0, kBins - 1, 0, 1u, 0, 0};
+            const float scale = bin_scale(f.invt);
+            if (kind.by_k) {  // thread maxima are the groups
+                p.slow = f.topk > NT * 7 / 8;
+                if (!p.slow) p.cut = key_of_rank<NT>(mykey, f.topk, ranks);
+            } else {
+                uint64_t m = 0;
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+#pragma unroll
+                    for (int i = 0; i < Q; ++i) {
+                        if (x[e][i] != -INFINITY) m += units(weight(et, x[e][i], st.first, f.invt));
+                        if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // a few at a time: registers
+                    }
+                p.mass = block_sum_u64<NT>(m, sums);
+                p.cut = cut_key(st.first, f.invt, cut_distance(f, (double)p.mass, a.V));
+            }
+            int n = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+#pragma unroll
+                for (int i = 0; i < Q; ++i) n += key_of(x[e][i]) >= p.cut;
+            n = (int)block_sum_u64<NT>((uint64_t)n, sums);
+            if (p.slow || n > kList) {  // the histogram, and the few bins of the threshold
+                const unsigned cut = kind.by_k ? 1u : p.cut;
+                const uint64_t mass = p.mass;
+                clear_bins(s.b, NT);
+                __syncthreads();
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+#pragma unroll
+                    for (int i = 0; i < Q; ++i)
+                        if (x[e][i] != -INFINITY) count_token(s.b, kind, x[e][i], cut, st.first, scale, f.invt, et);
+                __syncthreads();
+                plan_row(s.b, f, kind, mass, cut);
+                p = s.b.plan;
+            }
+            if (tid == 0) found = 0;
+            __syncthreads();
+            if (p.slow) {
+                descend_row<NT, F32>(et, a, r, f, kind, st, s.h, sums, &found);
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+#pragma unroll
+                    for (int i = 0; i < Q; ++i) {
+                        if (key_of(x[e][i]) < p.cut) continue;
+                        const int b = bin_of(x[e][i], st.first, scale);
+                        if (b >= p.sure && b <= p.end) s.l.list[atomicAdd(&found, 1)] = entry_of(x[e][i], at(e, i));
+                    }
+                __syncthreads();
+                resolve_list<NT>(s.l, found, f, kind, p, et, st, [](int, uint64_t) {});
+            }
+        }
+        // the draw: masses of the kept in index order, a part a wave and round
+        auto mass = [&](int e, int i) { return units(kept_weight(et, st, x[e][i], at(e, i))); };
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            uint64_t m = 0;
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                m += mass(e, i);
+                if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+            }
+            if (__any(m != 0)) m = wave_sum_u64(m);
+            if (lane == 0) sums[e * W + wave] = m;
+        }
+        __syncthreads();
+        constexpr int P = (E * W + 63) / 64;  // parts a lane
+        uint64_t mp = 0;
+#pragma unroll
+        for (int y = 0; y < P; ++y) mp += lane * P + y < E * W ? sums[lane * P + y] : 0;
+        const uint64_t total = wave_sum_u64(mp), want = target(uu, total);
+        uint64_t run;
+        int part = lane_of_mass(mp, want, run) * P;
+#pragma unroll
+        for (int y = 1; y < P; ++y)
+            if (want >= run + sums[part]) run += sums[part++];
+        if (part % W == wave) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (part / W == e) {
+                    uint64_t m[Q], ms = 0;
+#pragma unroll
+                    for (int i = 0; i < Q; ++i) m[i] = mass(e, i), ms += m[i];
+                    uint64_t b = run + wave_scan_u64(ms) - ms;
+                    if (b <= want && want < b + ms) {
+                        int to = -1;
+#pragma unroll
+                        for (int i = 0; i < Q; ++i) {
+                            b += m[i];
+                            if (to < 0 && want < b) to = at(e, i);
+                        }
+                        found = to;
+                    }
+                }
+        }
+        __syncthreads();
+        st.token = found;
+        st.sum = (double)total;
+    }
+    if (tid == 0 && head) head[t] = Header{0, 0, 0, 0};
+    if (tid == 0) finish_row(a, et, st, states, t, st.token >= 0 ? value<F32>(r, st.token) : 0.f, token, prob);
+}
+
+// ---------------------------------------------------------------------------
 // The whole distribution of a row
 // ---------------------------------------------------------------------------
 template <bool F32>
 __global__ __launch_bounds__(kThreads) void probs_kernel(SampleArgs a, Work w, float *probs) {
-    constexpr int E = kChunk / 4 / kThreads;
+    constexpr int E = kRounds<kThreads, F32>, Q = kVec<F32>;
     __shared__ ExpTable et;
     const int c = blockIdx.x, t = w.row0 + blockIdx.y;
-    float x[E][4];
-    load_chunk<kThreads, F32>(a, t, c, x);
+    float x[E][Q];
+    load_block<kThreads, F32>(a, t, c * kChunk, x);
     const RowState st = w.states[t];
     et.fill();
     __syncthreads();
@@ -896,15 +1274,16 @@ __global__ __launch_bounds__(kThreads) void probs_kernel(SampleArgs a, Work w, f
     float *out = probs + (size_t)t * a.V;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        const int at = token_at<kThreads>(c, e);
-        f32x4 v;
+        const int at = token_at<kThreads, F32>(c * kChunk, e);
+        float v[Q];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = (float)(kept_weight(et, st, x[e][i], at + i) * k);
-        if (at + 4 <= a.V) {
-            *reinterpret_cast<f32x4_any *>(out + at) = v;
+        for (int i = 0; i < Q; ++i) v[i] = (float)(kept_weight(et, st, x[e][i], at + i) * k);
+        if (at + Q <= a.V) {
+#pragma unroll
+            for (int i = 0; i < Q; i += 4) *reinterpret_cast<f32x4_any *>(out + at + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < Q; ++i)
                 if (at + i < a.V) out[at + i] = v[i];
         }
     }
@@ -945,7 +1324,7 @@ __global__ __launch_bounds__(64) void match_kernel(AcceptArgs c, const int32_t *
 // chunk of max(p - q, 0) there, or of p, and the last one draws.
 template <bool F32>
 __global__ __launch_bounds__(kRowThreads) void chain_kernel(SampleArgs a, AcceptArgs c, Work w) {
-    constexpr int E = kChunk / 4 / kRowThreads;
+    constexpr int E = kRounds<kRowThreads, F32>, Q = kVec<F32>;
     __shared__ ExpTable et;
     __shared__ uint64_t sums[kMaxChunks];
     __shared__ int sh, found, row_sh;
@@ -980,14 +1359,14 @@ __global__ __launch_bounds__(kRowThreads) void chain_kernel(SampleArgs a, Accept
         const double v = fmax(p_of(st, scale, x, i) - (rest ? (double)q[i] : 0.0), 0.0);
         return (uint64_t)__double_as_longlong(fma(v, kUnitP, 4503599627370496.0)) & 0xFFFFFFFFFFFFFull;
     };
-    float x[E][4];
-    load_chunk<kRowThreads, F32>(a, t, ch, x);
+    float x[E][Q];
+    load_block<kRowThreads, F32>(a, t, ch * kChunk, x);
     uint64_t sum = 0;
 #pragma unroll
     for (int e = 0; e < E; ++e)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int at = token_at<kRowThreads>(ch, e) + i;
+        for (int i = 0; i < Q; ++i) {
+            const int at = token_at<kRowThreads, F32>(ch * kChunk, e) + i;
             if (at < a.V) sum += mass(x[e][i], at);
         }
     sum = block_sum_u64<kRowThreads>(sum, sums);
@@ -1004,7 +1383,7 @@ __global__ __launch_bounds__(kRowThreads) void chain_kernel(SampleArgs a, Accept
     } else {  // nothing of p lies above q
         const void *row = row_of<F32>(a, t);
         uint64_t all;
-        tok = pick(
+        tok = pick<kRowThreads>(
             a.V, [&](int i) { return units(kept_weight(et, st, value<F32>(row, i), i)); },
             [&](uint64_t all) { return target(u, all); }, sums, &found, &all);
     }
@@ -1021,18 +1400,14 @@ __global__ __launch_bounds__(kRowThreads) void chain_kernel(SampleArgs a, Accept
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 struct Layout {
-    int C, E, H, L, rows;  // as in Work; rows of a batch
-    size_t states, drawn, kmax, count, sum, head, plan, list, hcnt, hmass, total;
+    int C, H, L, rows;  // as in Work; rows of a batch
+    size_t states, drawn, kmax, count, group, sum, head, plan, list, hcnt, hmass, total;
 };
 
-// A histogram is written and read whole (12 KB), so it takes up to 4 chunks
-// where that leaves the chip enough workgroups.
 Layout layout(int T, int V) {
     Layout l{};
     l.C = (V + kChunk - 1) / kChunk;
-    const long long wgs = (long long)T * l.C;
-    l.E = wgs >= 2048 ? 4 : wgs >= 1024 ? 2 : 1;
-    l.H = (l.C + l.E - 1) / l.E;
+    l.H = (l.C + kHistChunks - 1) / kHistChunks;
     l.L = V < kList ? (V + 63) & ~63 : kList;
     l.rows = l.C > 8 ? 16384 / l.C : 2048;
     if (l.rows > T) l.rows = T;
@@ -1047,6 +1422,7 @@ Layout layout(int T, int V) {
     l.drawn = take((size_t)T * 4);
     l.kmax = take(rc * 4);
     l.count = take(rc * 4);
+    l.group = take(rc * kGroups * 4);
     l.sum = take(rc * 8);
     l.head = take((size_t)l.rows * sizeof(Header));
     l.plan = take((size_t)l.rows * sizeof(Plan));
@@ -1064,6 +1440,7 @@ Work work_of(const SampleArgs &a, const Layout &l) {
     w.drawn = reinterpret_cast<int32_t *>(p + l.drawn);
     w.kmax = reinterpret_cast<unsigned *>(p + l.kmax);
     w.count = reinterpret_cast<int *>(p + l.count);
+    w.group = reinterpret_cast<unsigned *>(p + l.group);
     w.sum = reinterpret_cast<uint64_t *>(p + l.sum);
     w.head = reinterpret_cast<Header *>(p + l.head);
     w.plan = reinterpret_cast<Plan *>(p + l.plan);
@@ -1072,7 +1449,6 @@ Work work_of(const SampleArgs &a, const Layout &l) {
     w.hmass = reinterpret_cast<uint64_t *>(p + l.hmass);
     w.row0 = 0;
     w.C = l.C;
-    w.E = l.E;
     w.H = l.H;
     w.L = l.L;
     return w;
@@ -1083,15 +1459,30 @@ template <bool F32>
 hipError_t rows(const SampleArgs &a, Work w, const Layout &l, const float *u, int32_t *token, float *prob, float *probs,
                 hipStream_t s) {
     const dim3 block(kThreads);
+    const bool small = a.V <= kSmall;
+    if (small) {
+        const dim3 wide(kSmallThreads);
+        Header *head = a.T <= l.rows ? w.head : nullptr;  // acceptance counts in it
+        if (a.V <= kSmall / 4)
+            hipLaunchKernelGGL((small_kernel<8, F32>), dim3(a.T), wide, 0, s, a, w.states, head, u, token, prob);
+        else if (a.V <= kSmall / 2)
+            hipLaunchKernelGGL((small_kernel<16, F32>), dim3(a.T), wide, 0, s, a, w.states, head, u, token, prob);
+        else
+            hipLaunchKernelGGL((small_kernel<32, F32>), dim3(a.T), wide, 0, s, a, w.states, head, u, token, prob);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     for (; w.row0 < a.T; w.row0 += l.rows) {
         const int n = a.T - w.row0 < l.rows ? a.T - w.row0 : l.rows;
         const dim3 grid(l.C, n);
-        if (!a.top_k && !a.top_p && !a.min_p) {
+        if (small) {
+            // drawn above
+        } else if (!a.top_k && !a.top_p && !a.min_p) {
             hipLaunchKernelGGL((part_kernel<F32>), grid, block, 0, s, a, w);
             hipLaunchKernelGGL((join_kernel<F32>), dim3(n), block, 0, s, a, w, u, token, prob);
         } else {
             hipLaunchKernelGGL((max_kernel<F32>), grid, block, 0, s, a, w);
-            if (a.top_k || a.top_p) hipLaunchKernelGGL((hist_kernel<F32>), dim3(l.H, n), block, 0, s, a, w);
+            if (a.top_k || a.top_p) hipLaunchKernelGGL((hist_kernel<F32>), dim3(l.H, n), dim3(kHistThreads), 0, s, a, w);
             hipLaunchKernelGGL((gather_kernel<F32>), grid, block, 0, s, a, w);
             hipLaunchKernelGGL((resolve_kernel<F32>), dim3(n), dim3(kRowThreads), 0, s, a, w, u, token, prob);
         }
