@@ -51,10 +51,7 @@ struct RowState {
 };
 
 // Value of a row's token; NaN becomes -inf, +inf the largest float, -0 +0.
-__device__ __forceinline__ float clean(float x) {
-    x = x != x ? -INFINITY : fminf(x, 3.402823466e38f);
-    return x == 0.f ? 0.f : x;
-}
+__device__ __forceinline__ float clean(float x) { return (x != x ? -INFINITY : fminf(x, 3.402823466e38f)) + 0.f; }
 
 template <bool F32>
 __device__ __forceinline__ float value(const void *row, int i) {
@@ -69,33 +66,45 @@ __device__ __forceinline__ unsigned key_of(float x) {
 
 __device__ __forceinline__ float of_key(unsigned k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
 
-// exp for arguments <= 0: 2^(j / 128) from a table in LDS and the exponent,
-// e^r of the rest |r| <= ln 2 / 256 by its series to r^4 (the next term is
-// 1e-15 of the result).  j comes out of the low bits of a sum with 1.5 2^52;
-// below -700 the result stays e^-700, which is 0 in every use.
+// a * b + c with c in scalar registers (the compiler copies such a constant
+// into the result's registers first, which costs as much as the product).
+__device__ __forceinline__ double fma_sc(double a, double b, double c) {
+    double d;
+    asm("v_fma_f64 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "s"(c));
+    return d;
+}
+
+// 2^(t / 128) for t <= 0: 2^(j / 128) from a table in LDS and the exponent, and
+// the series of 2^(f / 128), |f| <= 1 / 2, to f^4 (the next term is 1e-15 of
+// the result).  j comes out of the low bits of a sum with 1.5 2^52.  Far
+// arguments, -inf and NaN give e^-700, which is 0 in every use.
 struct ExpTable {
     double t[128];
     __device__ void fill() {  // a barrier follows
         if (threadIdx.x < 128) t[threadIdx.x] = exp2((double)threadIdx.x / 128.0);
     }
-    __device__ __forceinline__ double operator()(double d) const {
-        d = fmax(d, -700.0);
-        const double s = fma(d, 128.0 * 1.4426950408889634074, 6755399441055744.0);
+    __device__ __forceinline__ double operator()(double x) const {
+        constexpr double l = 0.69314718055994530942 / 128.0;
+        x = fmax(x, -129262.0);
+        const double s = x + 6755399441055744.0;
         const int i = (int)__double_as_longlong(s);
-        const double r = fma(s - 6755399441055744.0, -0.69314718055994530942 / 128.0, d);
-        const double e = fma(r, fma(r, fma(r, fma(r, 1.0 / 24.0, 1.0 / 6.0), 0.5), 1.0), 1.0) * t[i & 127];
-        return __longlong_as_double(__double_as_longlong(e) + ((long long)(i >> 7) << 52));
+        const double f = x - (s - 6755399441055744.0);
+        const double e = fma_sc(f, fma_sc(f, fma_sc(f, l * l * l * l / 24.0 * f + l * l * l / 6.0, l * l / 2.0), l), 1.0) * t[i & 127];
+        return __hiloint2double(__double2hiint(e) + ((i & ~127) << 13), __double2loint(e));
     }
 };
 
 __device__ __forceinline__ double weight(const ExpTable &et, float x, float first, double invt) {
-    return et(((double)x - (double)first) * invt);
+    return et(((double)x - (double)first) * (invt * (128.0 * 1.4426950408889634074)));
 }
 
-// w 2^45 rounded to an integer: the low bits of 2^52 + w 2^45.
-__device__ __forceinline__ uint64_t units(double w) {
-    return (uint64_t)__double_as_longlong(fma(w, kUnit, 4503599627370496.0)) & 0xFFFFFFFFFFFFFull;
+// w 2^45 rounded to an integer: the low bits of 2^52 + w 2^45.  Sums are taken
+// of the raw bits, and what n of them hold too much is taken off at the end.
+__device__ __forceinline__ uint64_t raw_units(double w) {
+    return (uint64_t)__double_as_longlong(fma_sc(w, kUnit, 4503599627370496.0));
 }
+__device__ __forceinline__ uint64_t off_units(int n) { return (uint64_t)n * 0x4330000000000000ull; }
+__device__ __forceinline__ uint64_t units(double w) { return raw_units(w) - off_units(1); }
 
 // A kept token's weight, 0 for the others.
 __device__ __forceinline__ double kept_weight(const ExpTable &et, const RowState &st, float x, int i) {
@@ -479,11 +488,18 @@ __global__ __launch_bounds__(kThreads) void part_kernel(SampleArgs a, Work w) {
     const unsigned k = block_max_u32<kThreads>(key_of(v), sk);
     const float top = of_key(k);
     uint64_t s = 0;
+    if (f.one) {
 #pragma unroll
-    for (int e = 0; e < E; ++e)
+        for (int e = 0; e < E; ++e)
 #pragma unroll
-        for (int i = 0; i < Q; ++i)
-            if (x[e][i] != -INFINITY) s += f.one ? (uint64_t)(x[e][i] == top) : units(weight(et, x[e][i], top, f.invt));
+            for (int i = 0; i < Q; ++i) s += x[e][i] == top;
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+            for (int i = 0; i < Q; ++i) s += raw_units(weight(et, x[e][i], top, f.invt));
+        s -= off_units(E * Q);
+    }
     s = block_sum_u64<kThreads>(s, ss);
     if (threadIdx.x == 0) {
         w.kmax[blockIdx.y * w.C + c] = k;
@@ -496,7 +512,7 @@ __global__ __launch_bounds__(kThreads) void part_kernel(SampleArgs a, Work w) {
 // float64 in chunk order; the draw is made inside its chunk in that chunk's
 // units.
 template <bool F32>
-__global__ __launch_bounds__(kThreads) void join_kernel(SampleArgs a, Work w, const float *u, int32_t *token, float *prob) {
+__global__ __launch_bounds__(kRowThreads) void join_kernel(SampleArgs a, Work w, const float *u, int32_t *token, float *prob) {
     __shared__ ExpTable et;
     __shared__ uint64_t sums[kMaxChunks];
     __shared__ int found;
@@ -529,10 +545,11 @@ __global__ __launch_bounds__(kThreads) void join_kernel(SampleArgs a, Work w, co
         const int c = hit ? __ffsll((unsigned long long)hit) - 1 : 63 - __clzll((long long)some);
         const double inside = fmin((want - __shfl(incl - part, c)) / __shfl(scale, c), 9.0e18);
         const float topc = __shfl(top, c);
-        st.token = find_in_chunk<kThreads, F32>(
+        st.token = find_in_chunk<kRowThreads, F32>(
             a, t, c, inside > 0.0 ? (uint64_t)inside : 0,
             [&](float v, int) {
-                return v == -INFINITY ? (uint64_t)0 : f.one ? (uint64_t)(v == topc) : units(weight(et, v, topc, f.invt));
+                const uint64_t m = units(weight(et, v, topc, f.invt));
+                return f.one ? (uint64_t)(v == topc) : m;
             },
             sums, &found);
         st.sum = f.one ? kUnit : total;
@@ -558,7 +575,7 @@ __global__ __launch_bounds__(kThreads) void max_kernel(SampleArgs a, Work w) {
     float x[E][Q];
     load_block<kThreads, F32>(a, t, c * kChunk, x);
     const Filter f = filter_of(a, t);
-    const bool sums = f.topp < 1.f && !f.one;
+    const bool sums = f.topp < 1.f && !f.one && !(f.topk > 0 && f.topk < a.V);
     if (sums) et.fill();
     float v = -INFINITY;
     int n = 0;
@@ -588,27 +605,35 @@ __global__ __launch_bounds__(kThreads) void max_kernel(SampleArgs a, Work w) {
 #pragma unroll
         for (int e = 0; e < E; ++e)
 #pragma unroll
-            for (int i = 0; i < Q; ++i)
-                if (x[e][i] != -INFINITY) s += units(weight(et, x[e][i], top, f.invt));
+            for (int i = 0; i < Q; ++i) s += raw_units(weight(et, x[e][i], top, f.invt));
+        s -= off_units(E * Q);
         s = block_sum_u64<kThreads>(s, sn);
         if (tid == 0) w.sum[at] = s;
     }
 }
 
-// Which thresholds a row has.
+// Which thresholds a row has: the first k of the ranking, or a share of the
+// sum (of those k, or of the row).
 struct Kind {
     unsigned km;
+    int k;
     bool by_k, by_p;
 };
 
-__device__ __forceinline__ Kind kind_of(const Filter &f, const Work &w, int row) {
-    const int lane = threadIdx.x & 63;
+__device__ __forceinline__ Kind kind_from(const Filter &f, unsigned km, int n, int V) {
     Kind k;
-    k.km = wave_max_u32(lane < w.C ? w.kmax[row * w.C + lane] : 0u);
-    const int n = wave_sum_int(lane < w.C ? w.count[row * w.C + lane] : 0);
-    k.by_k = !f.one && f.topk > 0 && f.topk < n;
-    k.by_p = !f.one && f.topp < 1.f && k.km;
+    k.km = km;
+    k.k = min(f.topk, n);
+    k.by_k = !f.one && f.topk > 0 && f.topk < V && km;
+    k.by_p = !f.one && f.topp < 1.f && km;
     return k;
+}
+
+__device__ __forceinline__ Kind kind_of(const Filter &f, const Work &w, int row, int V) {
+    const int lane = threadIdx.x & 63;
+    const unsigned km = lane < w.C ? w.kmax[row * w.C + lane] : 0u;
+    const int n = lane < w.C ? w.count[row * w.C + lane] : 0;
+    return kind_from(f, wave_max_u32(km), wave_sum_int(n), V);
 }
 
 // Bin of a token's distance from the first, in float32: all that is asked of
@@ -678,8 +703,9 @@ __device__ __forceinline__ void count_token(Bins &h, const Kind &kind, float x, 
 }
 
 // The plan of a whole row's histogram, by 1024 threads; the block gets it in
-// h.plan.  `mass`: the row's sum, for top_p alone; `cut`: the least key counted.
-__device__ void plan_row(Bins &h, const Filter &f, const Kind &kind, uint64_t mass, unsigned cut) {
+// h.plan.  `mass`: the row's sum, for top_p alone; `cut`: the least key
+// counted; `cap`: of the list.
+__device__ void plan_row(Bins &h, const Filter &f, const Kind &kind, uint64_t mass, unsigned cut, int cap) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const uint64_t n0 = h.cnt[2 * tid], n1 = h.cnt[2 * tid + 1];
     const uint64_t m0 = kind.by_k ? 0 : h.mass[2 * tid], m1 = kind.by_k ? 0 : h.mass[2 * tid + 1];
@@ -691,7 +717,7 @@ __device__ void plan_row(Bins &h, const Filter &f, const Kind &kind, uint64_t ma
 #pragma unroll
     for (int i = 0; i < 16; ++i)
         if (i < wave) nb += h.wc[i], mb += h.wm[i];
-    const uint64_t want = kind.by_k ? (uint64_t)f.topk : max((uint64_t)1, (uint64_t)ceil((double)f.topp * (double)mass));
+    const uint64_t want = kind.by_k ? (uint64_t)kind.k : max((uint64_t)1, (uint64_t)ceil((double)f.topp * (double)mass));
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
         const uint64_t c = y ? n1 : n0, v = y ? m1 : m0;
@@ -700,7 +726,7 @@ __device__ void plan_row(Bins &h, const Filter &f, const Kind &kind, uint64_t ma
             Plan p;
             p.sure = kind.by_k ? 0 : 2 * tid + y;  // by_k: the sum of the first top_k comes from the list
             p.end = 2 * tid + y;
-            p.slow = (kind.by_k ? hi : c) > (uint64_t)kList;
+            p.slow = (kind.by_k ? hi : c) > (uint64_t)cap;
             p.cut = cut;
             p.above_mass = mb;
             p.mass = mass;
@@ -732,13 +758,13 @@ __global__ __launch_bounds__(kHistThreads) void hist_kernel(SampleArgs a, Work w
     static_assert(kHistThreads == 1024 && kBins == 2048 && kMaxChunks * kGroups <= kHistThreads, "two bins, a group a thread");
     const int hc = blockIdx.x, row = blockIdx.y, t = w.row0 + row, tid = threadIdx.x;
     const Filter f = filter_of(a, t);
-    const Kind kind = kind_of(f, w, row);
+    const Kind kind = kind_of(f, w, row, a.V);
     if (!kind.by_k && !kind.by_p) return;  // the whole row's workgroups
     // a small top_k against the groups: no histogram.  At 7 / 8 of the groups
     // about 2 tokens a group lie above the cut.
-    if (kind.by_k && f.topk <= w.C * kGroups * 7 / 8 && f.topk <= kList / 4) {
+    if (kind.by_k && kind.k <= w.C * kGroups * 7 / 8 && kind.k <= kList / 4) {
         if (hc) return;
-        const unsigned cut = key_of_rank<kHistThreads>(tid < w.C * kGroups ? w.group[row * w.C * kGroups + tid] : 0, f.topk, ranks);
+        const unsigned cut = key_of_rank<kHistThreads>(tid < w.C * kGroups ? w.group[row * w.C * kGroups + tid] : 0, kind.k, ranks);
         if (tid == 0) w.plan[row] = Plan{0, kBins - 1, 0, cut, 0, 0};
         return;
     }
@@ -780,7 +806,7 @@ __global__ __launch_bounds__(kHistThreads) void hist_kernel(SampleArgs a, Work w
         }
         __syncthreads();
     }
-    plan_row(h, f, kind, mass, cut);
+    plan_row(h, f, kind, mass, cut, kList);
     if (tid == 0) w.plan[row] = h.plan;
 }
 
@@ -796,7 +822,7 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a, Work w) 
     __shared__ int sh;
     const int c = blockIdx.x, row = blockIdx.y, t = w.row0 + row, tid = threadIdx.x;
     const Filter f = filter_of(a, t);
-    const Kind kind = kind_of(f, w, row);
+    const Kind kind = kind_of(f, w, row, a.V);
     const bool planned = kind.by_k || kind.by_p;
     Plan p{kBins, -1, 0, 1u, 0, 0};
     if (planned) p = w.plan[row];
@@ -817,22 +843,31 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a, Work w) 
         __syncthreads();
         sum = (uint64_t)sh;
     } else {
-        int mine = 0;
-        unsigned in = 0;  // which of the thread's tokens go to the list
+        // tokens below the cut are neither kept nor listed
+        const float low = planned && p.cut > 1u ? of_key(p.cut) : -3.402823466e38f;
+        float v = -INFINITY;
 #pragma unroll
         for (int e = 0; e < E; ++e)
 #pragma unroll
-            for (int i = 0; i < Q; ++i) {
-                if (x[e][i] == -INFINITY) continue;
-                const int b = planned ? bin_of(x[e][i], first, scale) : 0;
-                if (b < p.sure) {
-                    const double wt = weight(et, x[e][i], first, f.invt);
-                    if (wt >= f.minp) sum += units(wt);
-                } else if (b <= p.end && key_of(x[e][i]) >= p.cut) {
-                    ++mine;
-                    in |= 1u << (Q * e + i);
+            for (int i = 0; i < Q; ++i) v = fmaxf(v, x[e][i]);
+        int mine = 0;
+        unsigned in = 0;  // which of the thread's tokens go to the list
+        if (v >= low) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+#pragma unroll
+                for (int i = 0; i < Q; ++i) {
+                    if (!(x[e][i] >= low)) continue;
+                    const int b = planned ? bin_of(x[e][i], first, scale) : 0;
+                    if (b < p.sure) {
+                        const double wt = weight(et, x[e][i], first, f.invt);
+                        if (wt >= f.minp) sum += units(wt);
+                    } else if (b <= p.end) {
+                        ++mine;
+                        in |= 1u << (Q * e + i);
+                    }
                 }
-            }
+        }
         if (p.sure) sum = block_sum_u64<kThreads>(sum, sums);
         if (planned) {
             int at = 0;
@@ -861,8 +896,8 @@ __device__ void descend_row(const ExpTable &et, const SampleArgs &a, const void 
                             RowState &st, Histogram &h, uint64_t *sums, int *found) {
     uint64_t ca, ma, wk = 0, ties = 0;
     if (kind.by_k) {
-        descend<NT, F32>(et, row, a.V, st.first, st.invt, true, (uint64_t)f.topk, h, st.key, ca, ma);
-        ties = (uint64_t)f.topk - ca;
+        descend<NT, F32>(et, row, a.V, st.first, st.invt, true, (uint64_t)kind.k, h, st.key, ca, ma);
+        ties = (uint64_t)kind.k - ca;
         wk = ma + ties * units(weight(et, of_key(st.key), st.first, st.invt));
     } else {
         pick<NT>(
@@ -885,11 +920,33 @@ __device__ void descend_row(const ExpTable &et, const SampleArgs &a, const void 
         [&](uint64_t n) { return min(ties, n) - 1; }, sums, found, &total);
 }
 
+typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
+
 // Bitonic sort of `size` (a power of two >= 64) list entries by NT threads,
 // ascending: key descending, index ascending.  Strides up to 64 stay inside
 // the 128 entries of a wave and need no barrier of the block.
+// Up to 256 entries are put in the place that the number of smaller ones
+// gives, without any exchange.
 template <int NT>
 __device__ void sort_list(uint64_t *list, int size) {
+    if (size <= 256) {
+        const int i = threadIdx.x;
+        uint64_t mine = 0;
+        int rank = 0;
+        if (i < size) {
+            mine = list[i];
+#pragma unroll 4
+            for (int j = 0; j < size; j += 2) {
+                const u64x2 v = *reinterpret_cast<const u64x2 *>(list + j);
+                // equal entries only past the list's length
+                rank += (v[0] < mine || (v[0] == mine && j < i)) + (v[1] < mine || (v[1] == mine && j + 1 < i));
+            }
+        }
+        __syncthreads();
+        if (i < size) list[rank] = mine;
+        __syncthreads();
+        return;
+    }
     for (int k = 2; k <= size; k <<= 1)
         for (int j = k >> 1; j > 0; j >>= 1) {
             if (j > 64 || (j == 64 && k > 128)) __syncthreads();
@@ -904,8 +961,9 @@ __device__ void sort_list(uint64_t *list, int size) {
     __syncthreads();
 }
 
+template <int CAP>
 struct ListShared {
-    uint64_t list[kList];
+    uint64_t list[CAP];
     unsigned long long sub[1024];
     uint64_t ws[16];
     unsigned klo[16], khi[16];
@@ -916,8 +974,8 @@ struct ListShared {
 // sets st.key and st.last and calls add(index, units) for every kept entry.
 // A list for top_p alone is first narrowed to those of 1024 equal parts of its
 // key range that the threshold lies in.
-template <int NT, typename Add>
-__device__ void resolve_list(ListShared &s, int n, const Filter &f, const Kind &kind, const Plan &p, const ExpTable &et,
+template <int NT, int CAP, typename Add>
+__device__ void resolve_list(ListShared<CAP> &s, int n, const Filter &f, const Kind &kind, const Plan &p, const ExpTable &et,
                              RowState &st, Add add) {
     constexpr int W = NT / 64;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -966,12 +1024,12 @@ __device__ void resolve_list(ListShared &s, int n, const Filter &f, const Kind &
         const int at = s.kept;
         above = s.ws[W - 1];
         // entries above are kept, those of the part go on
-        uint64_t mine[kList / NT];
+        uint64_t mine[CAP / NT];
 #pragma unroll
-        for (int y = 0; y < kList / NT; ++y) mine[y] = y * NT + tid < n ? s.list[y * NT + tid] : ~0ull;
+        for (int y = 0; y < CAP / NT; ++y) mine[y] = y * NT + tid < n ? s.list[y * NT + tid] : ~0ull;
         __syncthreads();
 #pragma unroll
-        for (int y = 0; y < kList / NT; ++y)
+        for (int y = 0; y < CAP / NT; ++y)
             if (y * NT + tid < n) {
                 const int b = part_of(mine[y]);
                 if (b < at) keep(mine[y]);
@@ -987,7 +1045,7 @@ __device__ void resolve_list(ListShared &s, int n, const Filter &f, const Kind &
     sort_list<NT>(s.list, size);
     // running weights of the list: thread tid holds `per` of them
     const int per = (size + NT - 1) / NT, b = tid * per;
-    const int nk = kind.by_k ? min(f.topk, n) : n, e = min(b + per, nk);
+    const int nk = kind.by_k ? min(kind.k, n) : n, e = min(b + per, nk);
     if (tid == 0) s.kept = nk;
     if (kind.by_p) {
         uint64_t mine = 0;
@@ -1020,7 +1078,7 @@ __device__ void resolve_list(ListShared &s, int n, const Filter &f, const Kind &
 }
 
 union DrawShared {
-    ListShared l;
+    ListShared<kList> l;
     Histogram h;
 };
 
@@ -1039,7 +1097,7 @@ __global__ __launch_bounds__(kRowThreads) void resolve_kernel(SampleArgs a, Work
     Plan p = w.plan[row];
     const float uu = u ? u[t] : 0.f;
     const Filter f = filter_of(a, t);
-    const Kind kind = kind_of(f, w, row);
+    const Kind kind = kind_of(f, w, row, a.V);
     const bool planned = kind.by_k || kind.by_p;
     if (!planned) p = Plan{kBins, -1, 0, 1u, 0, 0};
     if (planned && n > kList) p.slow = 1;  // tied rows: the cut let too many through
@@ -1087,106 +1145,132 @@ __global__ __launch_bounds__(kRowThreads) void resolve_kernel(SampleArgs a, Work
 }
 
 // ---------------------------------------------------------------------------
-// Rows of up to 32768 tokens: the row in the registers of one workgroup, all
-// of the above in one launch, where launches and passes over the caches cost
-// more than the arithmetic of one compute unit.
+// Rows of up to 32768 tokens: the row in the shared memory of one workgroup,
+// all of the above in one launch.  There a launch and a pass over the caches
+// cost more than the arithmetic of one compute unit; the loops stay rolled,
+// since a code that runs once comes from memory as the data does.
 // ---------------------------------------------------------------------------
 constexpr int kSmallThreads = 1024;
-constexpr int kSmall = 32 * kSmallThreads;
+constexpr int kSmallRound = 4 * kSmallThreads;  // tokens
+constexpr int kSmall = 8 * kSmallRound;
+constexpr int kSmallList = 2048;
 
 union SmallShared {
     Bins b;
-    ListShared l;
+    ListShared<kSmallList> l;
     Histogram h;
 };
 
-// R: tokens a thread.
-template <int R, bool F32>
+template <bool F32>
 __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowState *states, Header *head, const float *u,
                                                               int32_t *token, float *prob) {
-    constexpr int NT = kSmallThreads, W = NT / 64, Q = kVec<F32>, E = R / Q;
+    constexpr int NT = kSmallThreads, W = NT / 64;
+    extern __shared__ __attribute__((aligned(16))) float tokens[];  // whole rounds, -inf past the end
     __shared__ ExpTable et;
     __shared__ SmallShared s;
-    __shared__ uint64_t sums[E * W > W ? E * W : W];
+    __shared__ uint64_t sums[8 * W];
     __shared__ unsigned sk[W];
     __shared__ int sn[W], ranks[2 * W], found;
     const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const void *r = row_of<F32>(a, t);
-    float x[E][Q];
-    load_block<NT, F32>(a, t, 0, x);
+    const int E = (a.V + kSmallRound - 1) / kSmallRound;  // rounds of 4 tokens a thread
+    f32x4 *own = reinterpret_cast<f32x4 *>(tokens) + tid;  // round e at own[e * NT]
+    {
+        constexpr int Q = kVec<F32>, B = kSmall / Q / NT;
+        float x[B][Q];
+#pragma unroll
+        for (int y = 0; y < B; ++y) {
+            const int i = Q * (y * NT + tid);
+            if (i < a.V) {
+                load_tokens<F32>(r, i, a.V, x[y]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < Q; ++e) x[y][e] = -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int y = 0; y < B; ++y) {
+            const int i = Q * (y * NT + tid);
+            if (i < E * kSmallRound)
+#pragma unroll
+                for (int e = 0; e < Q; e += 4)
+                    *reinterpret_cast<f32x4 *>(tokens + i + e) =
+                        f32x4{clean(x[y][e]), clean(x[y][e + 1]), clean(x[y][e + 2]), clean(x[y][e + 3])};
+        }
+    }
     const Filter f = filter_of(a, t);
     const float uu = u ? u[t] : 0.f;
     et.fill();
+    __syncthreads();
     float v = -INFINITY;
     int nv = 0;
+#pragma unroll 1
+    for (int e = 0; e < E; ++e) {
+        const f32x4 x = own[e * NT];
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-#pragma unroll
-        for (int i = 0; i < Q; ++i) {
-            v = fmaxf(v, x[e][i]);
-            nv += x[e][i] != -INFINITY;
+        for (int i = 0; i < 4; ++i) {
+            v = fmaxf(v, x[i]);
+            nv += x[i] != -INFINITY;
         }
+    }
     nv = wave_sum_int(nv);
     if (lane == 0) sn[wave] = nv;
-    Kind kind;
-    const unsigned mykey = key_of(v);
-    kind.km = block_max_u32<NT>(mykey, sk);
+    const unsigned mykey = key_of(v), km = block_max_u32<NT>(mykey, sk);
     nv = 0;
 #pragma unroll
     for (int i = 0; i < W; ++i) nv += sn[i];
-    kind.by_k = !f.one && f.topk > 0 && f.topk < nv;
-    kind.by_p = !f.one && f.topp < 1.f && kind.km;
-    RowState st{f.invt, f.one ? 0.0 : f.minp, of_key(kind.km), 1u, a.V, -1, 0.0};
-    auto at = [&](int e, int i) { return token_at<NT, F32>(0, e) + i; };
-    if (kind.km && f.one) {
+    const Kind kind = kind_from(f, km, nv, a.V);
+    RowState st{f.invt, f.one ? 0.0 : f.minp, of_key(km), 1u, a.V, -1, 0.0};
+    if (km && f.one) {
         if (tid == 0) found = INT_MAX;
         __syncthreads();
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-#pragma unroll
-            for (int i = 0; i < Q; ++i)
-                if (key_of(x[e][i]) == kind.km) atomicMin(&found, at(e, i));
+        if (mykey == km)
+            for (int e = E - 1; e >= 0; --e)
+                for (int i = 3; i >= 0; --i)
+                    if (own[e * NT][i] == st.first) atomicMin(&found, 4 * (e * NT + tid) + i);
         __syncthreads();
-        st.key = kind.km;
+        st.key = km;
         st.last = st.token = found;
         st.sum = kUnit;
-    } else if (kind.km) {
+    } else if (km) {
         if (kind.by_k || kind.by_p) {
             Plan p{0, kBins - 1, 0, 1u, 0, 0};
             const float scale = bin_scale(f.invt);
-            if (kind.by_k) {  // thread maxima are the groups
-                p.slow = f.topk > NT * 7 / 8;
-                if (!p.slow) p.cut = key_of_rank<NT>(mykey, f.topk, ranks);
+            if (kind.by_k) {  // a thread's tokens are a group
+                p.slow = kind.k > NT * 7 / 8;
+                if (!p.slow) p.cut = key_of_rank<NT>(mykey, kind.k, ranks);
             } else {
                 uint64_t m = 0;
+#pragma unroll 1
+                for (int e = 0; e < E; ++e) {
+                    const f32x4 x = own[e * NT];
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-#pragma unroll
-                    for (int i = 0; i < Q; ++i) {
-                        if (x[e][i] != -INFINITY) m += units(weight(et, x[e][i], st.first, f.invt));
-                        if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // a few at a time: registers
-                    }
-                p.mass = block_sum_u64<NT>(m, sums);
+                    for (int i = 0; i < 4; ++i) m += raw_units(weight(et, x[i], st.first, f.invt));
+                }
+                p.mass = block_sum_u64<NT>(m - off_units(4 * E), sums);
                 p.cut = cut_key(st.first, f.invt, cut_distance(f, (double)p.mass, a.V));
             }
+            const float low = p.cut > 1u ? of_key(p.cut) : -3.402823466e38f;
             int n = 0;
+#pragma unroll 1
+            for (int e = 0; e < E; ++e) {
+                const f32x4 x = own[e * NT];
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-#pragma unroll
-                for (int i = 0; i < Q; ++i) n += key_of(x[e][i]) >= p.cut;
+                for (int i = 0; i < 4; ++i) n += x[i] >= low;
+            }
             n = (int)block_sum_u64<NT>((uint64_t)n, sums);
-            if (p.slow || n > kList) {  // the histogram, and the few bins of the threshold
+            if (p.slow || n > kSmallList) {  // the histogram, and the few bins of the threshold
                 const unsigned cut = kind.by_k ? 1u : p.cut;
                 const uint64_t mass = p.mass;
                 clear_bins(s.b, NT);
                 __syncthreads();
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-#pragma unroll
-                    for (int i = 0; i < Q; ++i)
-                        if (x[e][i] != -INFINITY) count_token(s.b, kind, x[e][i], cut, st.first, scale, f.invt, et);
+#pragma unroll 1
+                for (int e = 0; e < 4 * E; ++e) {
+                    const float x = tokens[4 * ((e >> 2) * NT + tid) + (e & 3)];
+                    if (x != -INFINITY) count_token(s.b, kind, x, cut, st.first, scale, f.invt, et);
+                }
                 __syncthreads();
-                plan_row(s.b, f, kind, mass, cut);
+                plan_row(s.b, f, kind, mass, cut, kSmallList);
                 p = s.b.plan;
             }
             if (tid == 0) found = 0;
@@ -1194,67 +1278,61 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
             if (p.slow) {
                 descend_row<NT, F32>(et, a, r, f, kind, st, s.h, sums, &found);
             } else {
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-#pragma unroll
-                    for (int i = 0; i < Q; ++i) {
-                        if (key_of(x[e][i]) < p.cut) continue;
-                        const int b = bin_of(x[e][i], st.first, scale);
-                        if (b >= p.sure && b <= p.end) s.l.list[atomicAdd(&found, 1)] = entry_of(x[e][i], at(e, i));
+                const float from = p.cut > 1u ? of_key(p.cut) : -3.402823466e38f;
+                if (v >= from)
+#pragma unroll 1
+                    for (int e = 0; e < 4 * E; ++e) {
+                        const int at = 4 * ((e >> 2) * NT + tid) + (e & 3);
+                        const float x = tokens[at];
+                        if (!(x >= from)) continue;
+                        const int b = bin_of(x, st.first, scale);
+                        if (b >= p.sure && b <= p.end) s.l.list[atomicAdd(&found, 1)] = entry_of(x, at);
                     }
                 __syncthreads();
                 resolve_list<NT>(s.l, found, f, kind, p, et, st, [](int, uint64_t) {});
             }
         }
         // the draw: masses of the kept in index order, a part a wave and round
-        auto mass = [&](int e, int i) { return units(kept_weight(et, st, x[e][i], at(e, i))); };
-#pragma unroll
+        const float keep = st.key > 1u ? of_key(st.key) : -3.402823466e38f;
+        const bool some = v >= keep;
+#pragma unroll 1
         for (int e = 0; e < E; ++e) {
             uint64_t m = 0;
+            if (some) {
+                const f32x4 x = own[e * NT];
+                if (fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= keep)
 #pragma unroll
-            for (int i = 0; i < Q; ++i) {
-                m += mass(e, i);
-                if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+                    for (int i = 0; i < 4; ++i) m += units(kept_weight(et, st, x[i], 4 * (e * NT + tid) + i));
             }
             if (__any(m != 0)) m = wave_sum_u64(m);
             if (lane == 0) sums[e * W + wave] = m;
         }
         __syncthreads();
-        constexpr int P = (E * W + 63) / 64;  // parts a lane
-        uint64_t mp = 0;
-#pragma unroll
-        for (int y = 0; y < P; ++y) mp += lane * P + y < E * W ? sums[lane * P + y] : 0;
-        const uint64_t total = wave_sum_u64(mp), want = target(uu, total);
+        const uint64_t p0 = 2 * lane < E * W ? sums[2 * lane] : 0, p1 = 2 * lane < E * W ? sums[2 * lane + 1] : 0;
+        const uint64_t total = wave_sum_u64(p0 + p1), want = target(uu, total);
         uint64_t run;
-        int part = lane_of_mass(mp, want, run) * P;
-#pragma unroll
-        for (int y = 1; y < P; ++y)
-            if (want >= run + sums[part]) run += sums[part++];
+        int part = 2 * lane_of_mass(p0 + p1, want, run);
+        if (want >= run + sums[part]) run += sums[part++];
         if (part % W == wave) {
+            const int e = part / W, at = 4 * (e * NT + tid);
+            const f32x4 x = own[e * NT];
+            uint64_t m[4];
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (part / W == e) {
-                    uint64_t m[Q], ms = 0;
-#pragma unroll
-                    for (int i = 0; i < Q; ++i) m[i] = mass(e, i), ms += m[i];
-                    uint64_t b = run + wave_scan_u64(ms) - ms;
-                    if (b <= want && want < b + ms) {
-                        int to = -1;
-#pragma unroll
-                        for (int i = 0; i < Q; ++i) {
-                            b += m[i];
-                            if (to < 0 && want < b) to = at(e, i);
-                        }
-                        found = to;
-                    }
-                }
+            for (int i = 0; i < 4; ++i) m[i] = units(kept_weight(et, st, x[i], at + i));
+            const uint64_t ms = m[0] + m[1] + m[2] + m[3], b0 = run + wave_scan_u64(ms) - ms;
+            if (b0 <= want && want < b0 + ms) {
+                const uint64_t b1 = b0 + m[0], b2 = b1 + m[1], b3 = b2 + m[2];
+                found = at + (want < b1 ? 0 : want < b2 ? 1 : want < b3 ? 2 : 3);
+            }
         }
         __syncthreads();
         st.token = found;
         st.sum = (double)total;
     }
-    if (tid == 0 && head) head[t] = Header{0, 0, 0, 0};
-    if (tid == 0) finish_row(a, et, st, states, t, st.token >= 0 ? value<F32>(r, st.token) : 0.f, token, prob);
+    if (tid == 0) {
+        if (head) head[t] = Header{0, 0, 0, 0};
+        finish_row(a, et, st, states, t, st.token >= 0 ? tokens[st.token] : 0.f, token, prob);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -1461,16 +1539,13 @@ hipError_t rows(const SampleArgs &a, Work w, const Layout &l, const float *u, in
     const dim3 block(kThreads);
     const bool small = a.V <= kSmall;
     if (small) {
-        const dim3 wide(kSmallThreads);
+        const int lds = (a.V + kSmallRound - 1) / kSmallRound * kSmallRound * 4;
         Header *head = a.T <= l.rows ? w.head : nullptr;  // acceptance counts in it
-        if (a.V <= kSmall / 4)
-            hipLaunchKernelGGL((small_kernel<8, F32>), dim3(a.T), wide, 0, s, a, w.states, head, u, token, prob);
-        else if (a.V <= kSmall / 2)
-            hipLaunchKernelGGL((small_kernel<16, F32>), dim3(a.T), wide, 0, s, a, w.states, head, u, token, prob);
-        else
-            hipLaunchKernelGGL((small_kernel<32, F32>), dim3(a.T), wide, 0, s, a, w.states, head, u, token, prob);
-        const hipError_t e = hipGetLastError();
+        hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(small_kernel<F32>),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, kSmall * 4);
         if (e != hipSuccess) return e;
+        hipLaunchKernelGGL((small_kernel<F32>), dim3(a.T), dim3(kSmallThreads), lds, s, a, w.states, head, u, token, prob);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     for (; w.row0 < a.T; w.row0 += l.rows) {
         const int n = a.T - w.row0 < l.rows ? a.T - w.row0 : l.rows;
@@ -1479,7 +1554,7 @@ hipError_t rows(const SampleArgs &a, Work w, const Layout &l, const float *u, in
             // drawn above
         } else if (!a.top_k && !a.top_p && !a.min_p) {
             hipLaunchKernelGGL((part_kernel<F32>), grid, block, 0, s, a, w);
-            hipLaunchKernelGGL((join_kernel<F32>), dim3(n), block, 0, s, a, w, u, token, prob);
+            hipLaunchKernelGGL((join_kernel<F32>), dim3(n), dim3(kRowThreads), 0, s, a, w, u, token, prob);
         } else {
             hipLaunchKernelGGL((max_kernel<F32>), grid, block, 0, s, a, w);
             if (a.top_k || a.top_p) hipLaunchKernelGGL((hist_kernel<F32>), dim3(l.H, n), dim3(kHistThreads), 0, s, a, w);
