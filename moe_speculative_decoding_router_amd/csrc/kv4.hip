@@ -140,17 +140,20 @@ __global__ __launch_bounds__(kThreads) void append_kernel(KvAppendArgs a) {
 // its waves take the steps of a unit in turn.  A unit that more than one
 // workgroup worked on is joined by combine_kernel.
 //
-// A step is two tiles of 16 cache rows.  S^T = K Q^T leaves lane (g, c) = (l / 16, l % 16)
-// with the scores of rows 4 g .. 4 g + 3 of both tiles for query c, which is
-// just the operand that O^T += V^T P^T needs, so the probabilities never leave
-// the lane; the running maximum and sum belong to column c in both products.
-// Codes become bf16 by v_cvt_scalef32_pk_bf16_fp4, exactly (2 significant
-// bits and a power of two).  The maximum is moved only when a score passes it
-// by 2^8, so most steps need no exchange between lanes.
+// A step is two tiles of 16 cache rows, which each wave loads straight into a
+// ring of its own in LDS, two steps ahead.  S^T = K Q^T leaves lane (g, c) =
+// (l / 16, l % 16) with the scores of rows 4 g .. 4 g + 3 of both tiles for
+// query c, which is just the operand that O^T += V^T P^T needs, so the
+// probabilities never leave the lane; the running maximum and sum belong to
+// column c in both products.  Codes become bf16 by
+// v_cvt_scalef32_pk_bf16_fp4, exactly (2 significant bits and a power of two).
+// The maximum is moved only when a score passes it by 2^8, so most steps need
+// no exchange between lanes.
 // ---------------------------------------------------------------------------
 constexpr float kNone = -3.402823466e38f;  // running maximum before the first score
 constexpr float kSlack = 8.f;              // a score may pass the maximum by this (log2) before it moves
 constexpr int kMinShare = 8;               // steps of a workgroup at least
+constexpr int kStages = 3;                 // steps of a wave's ring
 
 __device__ __forceinline__ bf16x8 dequant8(unsigned w, float s) {
     union {
@@ -192,47 +195,124 @@ __device__ __forceinline__ Units units_of(const KvRows &r, int G, int block_rows
     return u;
 }
 
+// Quotient of non-negative numbers, short where both are.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
+    return a / b;
+}
+
 __device__ __forceinline__ long long share_of(long long all, int nwg) {
-    const long long s = (all + nwg - 1) / nwg;
+    const long long s = quotient(all + nwg - 1, nwg);
     return s > kMinShare ? s : kMinShare;
 }
 
-// Values of one step as loaded.
+// Values of one step in a lane's registers.
 template <int D>
 struct Frag {
     static constexpr int W = D / 32;  // words of a lane: D / 4 K elements, or 4 rows of D / 16 V elements
     unsigned k[2][W], v[2][W], vs[2];
     unsigned ks[2];  // one byte, or two for D = 256
-    bool ok[2];      // the tile's page is in the pool
 };
 
-template <int N>
-__device__ __forceinline__ void load_words(unsigned (&w)[N], const uint8_t *p) {
-    if (N == 2) {
-        const u32x2 a = *reinterpret_cast<const u32x2 *>(p);
-        w[0] = a[0], w[1] = a[1];
+// From the step's two tiles in LDS at byte `at` into registers.  The loads
+// that fill LDS are counted by hand, so the reads are written out: the
+// compiler would wait for every one of them that is under way.
+template <int D>
+__device__ __forceinline__ void read_frag(Frag<D> &f, unsigned at) {
+    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+    const unsigned ka = at + c * (D / 2) + g * (D / 8), va = at + lane * (D / 8);
+    const unsigned ksa = at + c + 16 * (g * (D / 4) / 32), vsa = at + 16 * (c * (D / 16) / 32) + 4 * g;
+    typedef Tile<D> T;
+    if constexpr (D == 64) {
+        u32x2 k0, k1, v0, v1;
+        asm volatile(
+            "ds_read_b64 %0, %8 offset:%12\n\tds_read_b64 %1, %8 offset:%13\n\t"
+            "ds_read_u8 %4, %10 offset:%14\n\tds_read_u8 %5, %10 offset:%15\n\t"
+            "ds_read_b64 %2, %9 offset:%16\n\tds_read_b64 %3, %9 offset:%17\n\t"
+            "ds_read_b32 %6, %11 offset:%18\n\tds_read_b32 %7, %11 offset:%19\n\ts_waitcnt lgkmcnt(0)"
+            : "=&v"(k0), "=&v"(k1), "=&v"(v0), "=&v"(v1), "=&v"(f.ks[0]), "=&v"(f.ks[1]), "=&v"(f.vs[0]), "=&v"(f.vs[1])
+            : "v"(ka), "v"(va), "v"(ksa), "v"(vsa), "i"(T::kK), "i"(T::kBytes + T::kK), "i"(T::kKs), "i"(T::kBytes + T::kKs),
+              "i"(T::kV), "i"(T::kBytes + T::kV), "i"(T::kVs), "i"(T::kBytes + T::kVs)
+            : "memory");
+#pragma unroll
+        for (int i = 0; i < 2; ++i) f.k[0][i] = k0[i], f.k[1][i] = k1[i], f.v[0][i] = v0[i], f.v[1][i] = v1[i];
+    } else if constexpr (D == 128) {
+        u32x4 k0, k1, v0, v1;
+        asm volatile(
+            "ds_read_b128 %0, %8 offset:%12\n\tds_read_b128 %1, %8 offset:%13\n\t"
+            "ds_read_u8 %4, %10 offset:%14\n\tds_read_u8 %5, %10 offset:%15\n\t"
+            "ds_read_b128 %2, %9 offset:%16\n\tds_read_b128 %3, %9 offset:%17\n\t"
+            "ds_read_b32 %6, %11 offset:%18\n\tds_read_b32 %7, %11 offset:%19\n\ts_waitcnt lgkmcnt(0)"
+            : "=&v"(k0), "=&v"(k1), "=&v"(v0), "=&v"(v1), "=&v"(f.ks[0]), "=&v"(f.ks[1]), "=&v"(f.vs[0]), "=&v"(f.vs[1])
+            : "v"(ka), "v"(va), "v"(ksa), "v"(vsa), "i"(T::kK), "i"(T::kBytes + T::kK), "i"(T::kKs), "i"(T::kBytes + T::kKs),
+              "i"(T::kV), "i"(T::kBytes + T::kV), "i"(T::kVs), "i"(T::kBytes + T::kVs)
+            : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f.k[0][i] = k0[i], f.k[1][i] = k1[i], f.v[0][i] = v0[i], f.v[1][i] = v1[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < N / 4; ++i) {
-            const u32x4 a = reinterpret_cast<const u32x4 *>(p)[i];
+        for (int t = 0; t < 2; ++t) {
+            u32x4 k0, k1, v0, v1;
+            unsigned s0, s1;
+            asm volatile(
+                "ds_read_b128 %0, %7 offset:%11\n\tds_read_b128 %1, %7 offset:%12\n\t"
+                "ds_read_u8 %4, %9 offset:%13\n\tds_read_u8 %5, %9 offset:%14\n\t"
+                "ds_read_b128 %2, %8 offset:%15\n\tds_read_b128 %3, %8 offset:%16\n\t"
+                "ds_read_b32 %6, %10 offset:%17\n\ts_waitcnt lgkmcnt(0)"
+                : "=&v"(k0), "=&v"(k1), "=&v"(v0), "=&v"(v1), "=&v"(s0), "=&v"(s1), "=&v"(f.vs[t])
+                : "v"(ka + t * T::kBytes), "v"(va + t * T::kBytes), "v"(ksa + t * T::kBytes), "v"(vsa + t * T::kBytes), "i"(T::kK),
+                  "i"(T::kK + 16), "i"(T::kKs), "i"(T::kKs + 16), "i"(T::kV), "i"(T::kV + 16), "i"(T::kVs)
+                : "memory");
+            f.ks[t] = s0 | (s1 << 8);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[4 * i + j] = a[j];
+            for (int i = 0; i < 4; ++i)
+                f.k[t][i] = k0[i], f.k[t][4 + i] = k1[i], f.v[t][i] = v0[i], f.v[t][4 + i] = v1[i];
         }
     }
 }
 
+// Loads of a tile: 1 KB a wave each, the last one partial.
+template <int D>
+constexpr int kTileLoads = (Tile<D>::kBytes + 1023) / 1024;
+
+// Waits until at most N loads of this wave are under way.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"i"(N) : "memory");
+}
+
+// Bits of the rows j .. j + 3 of the call in `see`; rows before the call
+// (j < 0) are seen.
+__device__ __forceinline__ unsigned four_seen(uint64_t see, int j) {
+    const int n = min(max(-j, 0), 4);
+    const unsigned before = (unsigned)(see << n) | ((1u << n) - 1u), from = (unsigned)(see >> min(max(j, 0), 63));
+    return (j < 0 ? before : from) & 15u;
+}
+
+// Waits here for a loaded value: where it is used, the wait would be for the
+// loads into LDS that came after it as well.
+template <typename T>
+__device__ __forceinline__ void settle(T &v) {
+    asm volatile("" : "+v"(v));
+}
+
+template <int MT, int D, bool F32>
+constexpr int ring_offset() {  // the queries' operand terms lie before the rings
+    return MT * 16 * D * 2 * (F32 ? 3 : 1);
+}
+
 template <int MT, int D, bool F32>
 constexpr int attend_lds_bytes() {
-    const int q = MT * 16 * D * 2 * (F32 ? 3 : 1), m = 2 * MT * 16 * D * 4;
+    const int q = ring_offset<MT, D, F32>() + kWaves * kStages * 2 * Tile<D>::kBytes, m = 2 * MT * 16 * D * 4;
     return q > m ? q : m;
 }
 
 // 16-row tiles of a row block: its MT * D / 4 accumulators a lane, with the
 // float32 type's three-term operands beside them, have to fit the registers.
-constexpr int max_mt(int D, bool f32) { return D == 64 ? 4 : D == 128 ? (f32 ? 2 : 3) : 1; }
+constexpr int max_mt(int D, bool f32) { return D == 64 ? 4 : D == 128 ? (f32 ? 2 : 4) : 1; }
 
 template <int MT, int D, bool F32>
-__global__ __launch_bounds__(kThreads, MT == 1 && D < 256 ? 2 : 1) void attend_kernel(KvAttendArgs a) {
+__global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void attend_kernel(KvAttendArgs a) {
     constexpr int NS = F32 ? 3 : 1;  // bf16 terms of q and of the probabilities
     constexpr int KS = D / 32;       // k steps of the first product
     constexpr int C = D / 16;        // row tiles of the second
@@ -244,13 +324,17 @@ __global__ __launch_bounds__(kThreads, MT == 1 && D < 256 ? 2 : 1) void attend_k
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, c = lane & 15;
     const KvRows &r = a.r;
+    uint8_t *ring = lds + ring_offset<MT, D, F32>() + wave * (kStages * 2 * Tile<D>::kBytes);
+    const unsigned ring_at = (unsigned)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)ring;
 
     long long all;
     const Units un = units_of(r, a.G, BR, all);
     const long long share = share_of(all, a.nwg);
     const long long x0 = (long long)blockIdx.x * share;
     long long x = x0, xe = x0 + share < all ? x0 + share : all;
-    const float sl = a.scale * 1.44269504088896341f;
+    // the sign is the queries'; above 0, so that hidden rows' -inf stays what it is
+    const float sl = fmaxf(fabsf(a.scale) * 1.44269504088896341f, 1e-30f);
+    const unsigned flip = a.scale < 0.f ? 0x8000u : 0u;
 
     while (x < xe) {
         const int s = __ffsll((unsigned long long)__ballot(un.incl > x)) - 1;
@@ -259,13 +343,57 @@ __global__ __launch_bounds__(kThreads, MT == 1 && D < 256 ? 2 : 1) void attend_k
         const int mbs = __builtin_amdgcn_readlane(un.mb, s);
         const long long end_s = __shfl(un.incl, s);
         const long long rel = x - (end_s - (long long)steps * mbs * r.Hkv);
-        const int unit = (int)(rel / steps), st0 = (int)(rel - (long long)unit * steps);
+        const int unit = __builtin_amdgcn_readfirstlane((int)quotient(rel, steps));
+        const int st0 = __builtin_amdgcn_readfirstlane((int)(rel - (long long)unit * steps));
         const int h = unit / mbs, mb = unit - h * mbs;
-        const int n = (int)(xe - x < steps - st0 ? xe - x : steps - st0);
-        const int row0 = mb * BR, t0 = r.off[s], ntok = rows / a.G;
+        const int n = __builtin_amdgcn_readfirstlane((int)(xe - x < steps - st0 ? xe - x : steps - st0));
+        const int row0 = mb * BR, t0 = r.off[s], se = st0 + n;
+
+        // ---- loads of a step into stage `at` of the ring; whether its tiles are in the pool (2 bits) ----
+        int slot0 = -64, pids = -1;  // page ids of 64 table entries from slot0 on, one a lane
+        auto issue = [&](int st, int at) {
+            unsigned ok = 0;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int tile = 2 * st + t, slot = tile >> (r.page_shift - 4);
+                if (slot >= slot0 + 64 || slot < slot0) {
+                    slot0 = slot;
+                    pids = slot + lane < r.max_pages ? r.table[(size_t)s * r.max_pages + slot + lane] : -1;
+                    settle(pids);
+                }
+                const int pid = __builtin_amdgcn_readlane(pids, slot - slot0);
+                const bool in_pool = pid >= 0 && pid < r.num_pages;
+                ok |= (unsigned)in_pool << t;
+                const int in = tile & ((1 << (r.page_shift - 4)) - 1);
+                const uint8_t *b = r.data + ((((size_t)(in_pool ? pid : 0) * r.Hkv + h) << (r.page_shift - 4)) + in) *
+                                                Tile<D>::kBytes + lane * 16;
+                uint8_t *d = ring + (at * 2 + t) * Tile<D>::kBytes;
+#pragma unroll
+                for (int i = 0; i < kTileLoads<D>; ++i)
+                    if ((i + 1) * 1024 <= Tile<D>::kBytes || lane * 16 < Tile<D>::kBytes - i * 1024) load_lds16(b + i * 1024, d + i * 1024);
+            }
+            return ok;
+        };
+
+        uint64_t see[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int row = row0 + mt * 16 + c;
+            see[mt] = row < rows ? a.anc[t0 + row / a.G] : 0;
+            settle(see[mt]);
+        }
+        __syncthreads();  // the last unit's exchange is over
+        unsigned pool = 0;  // 2 bits a step, the newest lowest
+        int next = st0 + wave, put = 0;
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) {
+            pool <<= 2;
+            if (next < se) pool |= issue(next, put);
+            next += kWaves;
+            ++put;
+        }
 
         // ---- the block's queries into LDS as bf16 operand terms ----
-        __syncthreads();
         for (int i = threadIdx.x; i < BR * (D / 8); i += kThreads) {
             const int mt = i / (16 * (D / 8)), ks = (i / 64) % KS, ln = i & 63;
             const int row = row0 + mt * 16 + (ln & 15), d = (ln >> 4) * (D / 4) + ks * 8;
@@ -276,66 +404,54 @@ __global__ __launch_bounds__(kThreads, MT == 1 && D < 256 ? 2 : 1) void attend_k
             if (row < rows) {
                 const size_t at = (size_t)(t0 + row / a.G) * a.qs + (size_t)(h * a.G + row % a.G) * D + d;
                 if (F32) {
-                    const float *p = (const float *)a.q + at;
+                    const f32x4 *p = reinterpret_cast<const f32x4 *>((const float *)a.q + at);
+                    const f32x4 p0 = p[0], p1 = p[1];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        float v = p[e];
+                        float v = e < 4 ? p0[e & 3] : p1[e & 3];
 #pragma unroll
                         for (int y = 0; y < NS; ++y) {
                             const unsigned b = f32_to_bf16_rne(v);
                             v -= bf16_to_f32((uint16_t)b);
-                            z[y][e >> 1] |= b << (16 * (e & 1));
+                            z[y][e >> 1] |= (b ^ flip) << (16 * (e & 1));
                         }
                     }
                 } else {
                     z[0] = *reinterpret_cast<const u32x4 *>((const uint16_t *)a.q + at);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[0][e] ^= flip | (flip << 16);
                 }
             }
 #pragma unroll
             for (int p = 0; p < NS; ++p) *reinterpret_cast<u32x4 *>(dst + (size_t)p * KS * 64 * 8) = z[p];
         }
-        __syncthreads();
 
         float m[MT], l[MT];
         f32x4 o[MT][C];
-        uint64_t see[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             m[mt] = kNone;
             l[mt] = 0.f;
-            const int row = row0 + mt * 16 + c;
-            see[mt] = row < rows ? a.anc[t0 + row / a.G] : 0;
 #pragma unroll
             for (int i = 0; i < C; ++i) o[mt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
+        lds_barrier();  // the queries are there; the loads go on
 
-        // page ids of 64 table entries from slot0 on, one a lane
-        int slot0 = -64, pids = -1;
-        auto load = [&](int st, Frag<D> &f) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int tile = 2 * st + t, slot = tile >> (r.page_shift - 4);
-                if (slot >= slot0 + 64 || slot < slot0) {
-                    slot0 = slot;
-                    pids = slot + lane < r.max_pages ? r.table[(size_t)s * r.max_pages + slot + lane] : -1;
-                }
-                const int pid = __builtin_amdgcn_readlane(pids, slot - slot0);
-                f.ok[t] = pid >= 0 && pid < r.num_pages;
-                const int in = tile & ((1 << (r.page_shift - 4)) - 1);
-                const uint8_t *b = r.data + ((((size_t)(f.ok[t] ? pid : 0) * r.Hkv + h) << (r.page_shift - 4)) + in) *
-                                                Tile<D>::kBytes;
-                load_words(f.k[t], b + Tile<D>::kK + c * (D / 2) + g * (D / 8));
-                const uint8_t *ks = b + Tile<D>::kKs + c;
-                if (D == 256)
-                    f.ks[t] = ks[32 * g] | (ks[32 * g + 16] << 8);
-                else
-                    f.ks[t] = ks[16 * (g * (D / 4) / 32)];
-                load_words(f.v[t], b + Tile<D>::kV + lane * (D / 8));
-                f.vs[t] = *reinterpret_cast<const unsigned *>(b + Tile<D>::kVs + 16 * (c * (D / 16) / 32) + 4 * g);
+        int get = 0;
+        for (int st = st0 + wave; st < se; st += kWaves) {
+            pool <<= 2;
+            if (next < se) {
+                pool |= issue(next, put);
+                wait_loads<(kStages - 1) * 2 * kTileLoads<D>>();
+            } else {
+                wait_loads<0>();
             }
-        };
+            next += kWaves;
+            put = put + 1 == kStages ? 0 : put + 1;
+            Frag<D> f;
+            read_frag<D>(f, ring_at + get * 2 * Tile<D>::kBytes);
+            get = get + 1 == kStages ? 0 : get + 1;
 
-        auto compute = [&](int st, Frag<D> &f) {
             f32x4 sc[MT][2];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) sc[mt][0] = sc[mt][1] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -354,30 +470,36 @@ __global__ __launch_bounds__(kThreads, MT == 1 && D < 256 ? 2 : 1) void attend_k
                         sc[mt][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[1], q, sc[mt][1], 0, 0, 0);
                     }
             }
-            const bool part = st * 32 + 32 > len || !f.ok[0] || !f.ok[1];  // some rows are hidden or absent
-            unsigned there = 0xff;                                         // rows that exist, bit 4 t + i
+            const unsigned ok = (pool >> (2 * (kStages - 1))) & 3u;
+            const bool part = st * 32 + 32 > len || ok != 3u;  // some rows are hidden or absent
             bool move = false;
             float mx[MT];
             if (part) {
-                there = 0;
+                // bit 4 t + i: row 4 g + i of tile t exists
+                const int left0 = total - st * 32 - 4 * g, left1 = left0 - 16;
+                const unsigned there = ((ok & 1u) ? (1u << min(max(left0, 0), 4)) - 1u : 0u) |
+                                       ((ok & 2u) ? ((1u << min(max(left1, 0), 4)) - 1u) << 4 : 0u);
+                const int j0 = st * 32 + 4 * g - len, j1 = j0 + 16;  // rows of the call, if >= 0
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (f.ok[e >> 2] && st * 32 + (e >> 2) * 16 + 4 * g + (e & 3) < total) there |= 1u << e;
+                for (int mt = 0; mt < MT; ++mt) {
+                    const unsigned vis = there & (four_seen(see[mt], j0) | (four_seen(see[mt], j1) << 4));
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sc[mt][e >> 2][e & 3] = (vis >> e) & 1u ? sc[mt][e >> 2][e & 3] : -INFINITY;
+                }
+                // whatever lies in absent rows becomes finite: scale bytes of 127
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    unsigned keep = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) keep |= (there >> (4 * t + i)) & 1u ? 255u << (8 * i) : 0u;
+                    f.vs[t] = (f.vs[t] & keep) | (0x7f7f7f7fu & ~keep);
+                }
             }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sc[mt][e >> 2][e & 3] *= sl;
-                if (part) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int j = st * 32 + (e >> 2) * 16 + 4 * g + (e & 3) - len;  // row of the call, if >= 0
-                        const bool vis = ((there >> e) & 1) && (j < 0 || ((see[mt] >> (j & 63)) & 1));
-                        sc[mt][e >> 2][e & 3] = vis ? sc[mt][e >> 2][e & 3] : -INFINITY;
-                    }
-                }
-                mx[mt] = fmaxf(fmaxf(fmaxf(sc[mt][0][0], sc[mt][0][1]), fmaxf(sc[mt][0][2], sc[mt][0][3])),
-                               fmaxf(fmaxf(sc[mt][1][0], sc[mt][1][1]), fmaxf(sc[mt][1][2], sc[mt][1][3])));
+                const float v = fmaxf(fmaxf(fmaxf(sc[mt][0][0], sc[mt][0][1]), fmaxf(sc[mt][0][2], sc[mt][0][3])),
+                                      fmaxf(fmaxf(sc[mt][1][0], sc[mt][1][1]), fmaxf(sc[mt][1][2], sc[mt][1][3])));
+                mx[mt] = v == -INFINITY ? kNone : v * sl;
                 move |= mx[mt] > m[mt] + kSlack;
             }
             if (__any(move)) {
@@ -399,7 +521,7 @@ __global__ __launch_bounds__(kThreads, MT == 1 && D < 256 ? 2 : 1) void attend_k
                 float p[8], sum = 0.f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    p[e] = __builtin_amdgcn_exp2f(sc[mt][e >> 2][e & 3] - m[mt]);
+                    p[e] = __builtin_amdgcn_exp2f(fmaf(sc[mt][e >> 2][e & 3], sl, -m[mt]));
                     sum += p[e];
                 }
                 l[mt] += sum;
@@ -415,11 +537,7 @@ __global__ __launch_bounds__(kThreads, MT == 1 && D < 256 ? 2 : 1) void attend_k
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    unsigned e = (f.vs[t] >> (8 * b)) & 255u;
-                    if (part) e = (there >> (4 * t + b)) & 1 ? e : 127u;  // whatever lies there is finite
-                    vsc[t][b] = scale_of(e);
-                }
+                for (int b = 0; b < 4; ++b) vsc[t][b] = scale_of((f.vs[t] >> (8 * b)) & 255u);
 #pragma unroll
             for (int p = 0; p < C / 2; ++p) {
                 union {
@@ -457,20 +575,6 @@ __global__ __launch_bounds__(kThreads, MT == 1 && D < 256 ? 2 : 1) void attend_k
                             __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi2.v, pb[mt][y], o[mt][2 * p + 1], 0, 0, 0);
                     }
             }
-        };
-
-        const int se = st0 + n;
-        Frag<D> f0, f1;
-        int st = st0 + wave;
-        if (st < se) load(st, f0);
-        while (st < se) {
-            if (st + kWaves < se) load(st + kWaves, f1);
-            compute(st, f0);
-            st += kWaves;
-            if (st >= se) break;
-            if (st + kWaves < se) load(st + kWaves, f0);
-            compute(st, f1);
-            st += kWaves;
         }
 
         // ---- the waves' results to one ----
@@ -511,7 +615,7 @@ __global__ __launch_bounds__(kThreads, MT == 1 && D < 256 ? 2 : 1) void attend_k
 #pragma unroll
                     for (int i = 0; i < C; ++i) o[mt][i] += reinterpret_cast<const f32x4 *>(d)[(mt * C + i) * 64 + lane];
             }
-            __syncthreads();
+            if (half > 1) __syncthreads();
         }
         if (wave == 0) {
             const bool whole = n == steps;
@@ -556,81 +660,81 @@ __global__ __launch_bounds__(kThreads, MT == 1 && D < 256 ? 2 : 1) void attend_k
     }
 }
 
-// Joins the parts of a unit: one workgroup per unit and 16-row tile, 16
-// threads a row.  A workgroup's part of a unit that began before it is its
-// slot 0, of one that begins in it slot 1.
+// Joins the parts of a unit, one workgroup a query row of it: lane i of every
+// wave takes the statistics of part i, the waves take the parts in turn.  A
+// workgroup's part of a unit that began before it is its slot 0, of one that
+// begins in it slot 1.
 template <int D, bool F32>
 __global__ __launch_bounds__(kThreads) void combine_kernel(KvAttendArgs a) {
+    constexpr int E = D / 64;  // elements of a lane
+    __shared__ float sum[kWaves][D];
     const KvRows &r = a.r;
-    const int BR = 16 * a.mt;
+    const int BR = 16 * a.mt, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     long long all;
     const Units un = units_of(r, a.G, BR, all);
     const long long share = share_of(all, a.nwg);
-    // the block's unit: units are counted over sequences in the same order
-    const int lane = threadIdx.x & 63;
-    int cnt = un.mb * r.Hkv, incl = cnt;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int v = __shfl_up(incl, d);
-        if (lane >= d) incl += v;
-    }
-    const int unit_all = blockIdx.x / a.mt, mt = blockIdx.x % a.mt;
-    const uint64_t in = __ballot(incl > unit_all);
+    // the block's row: rows are counted over sequences and heads
+    const int cnt = un.rows * r.Hkv, incl = wave_incl_scan(cnt);
+    const uint64_t in = __ballot(incl > (int)blockIdx.x);
     if (in == 0) return;
     const int s = __ffsll((unsigned long long)in) - 1;
     const int steps = __shfl(un.steps, s), rows = __shfl(un.rows, s), mbs = __shfl(un.mb, s);
-    const int unit = unit_all - (__shfl(incl, s) - __shfl(cnt, s));
+    const int rel = (int)blockIdx.x - (__shfl(incl, s) - __shfl(cnt, s));
+    const int h = rel / rows, row = rel - h * rows, unit = h * mbs + row / BR, rb = row % BR;
     const long long u0 = __shfl(un.incl, s) - (long long)steps * mbs * r.Hkv + (long long)unit * steps, u1 = u0 + steps;
-    const int w0 = (int)(u0 / share), w1 = (int)((u1 - 1) / share);
+    const int w0 = __builtin_amdgcn_readfirstlane((int)quotient(u0, share)), w1 = __builtin_amdgcn_readfirstlane((int)quotient(u1 - 1, share));
     if (w0 == w1) return;
-    const int h = unit / mbs, rb = mt * 16 + (threadIdx.x >> 4), row = (unit - h * mbs) * BR + rb;
-    if (row >= rows) return;
     const float *ml = a.part;
-    const float *po = a.part + (size_t)a.nwg * 2 * BR * 2;
-    auto slot = [&](int w) { return (size_t)w * 2 + (u0 < (long long)w * share ? 0 : 1); };
+    const float *po = a.part + (size_t)a.nwg * 2 * BR * 2 + lane * E;
+    auto at = [&](int w) { return ((size_t)w * 2 + (w == w0 ? 1 : 0)) * BR + rb; };
     float m = kNone;
-    for (int w = w0; w <= w1; ++w) m = fmaxf(m, ml[(slot(w) * BR + rb) * 2]);
-    constexpr int E = D / 16;
-    const int d = (threadIdx.x & 15) * E;
+    for (int w = w0 + lane; w <= w1; w += 64) m = fmaxf(m, ml[at(w) * 2]);
+    m = wave_max(m);
     float l = 0.f, o[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) o[i] = 0.f;
-    for (int w = w0; w <= w1; ++w) {
-        const size_t at = slot(w) * BR + rb;
-        const float k = __builtin_amdgcn_exp2f(ml[at * 2] - m);
-        l += k * ml[at * 2 + 1];
+    for (int b = w0; b <= w1; b += 64) {
+        const int w = b + lane;
+        const float k = w <= w1 ? __builtin_amdgcn_exp2f(ml[at(w) * 2] - m) : 0.f;
+        if (w <= w1) l += k * ml[at(w) * 2 + 1];
+        const int n = min(64, w1 - b + 1);
+        for (int i = wave; i < n; i += kWaves) {
+            const float ki = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(k), i));
+            const float *p = po + at(b + i) * D;
 #pragma unroll
-        for (int i = 0; i < E; i += 4) {
-            const f32x4 v = *reinterpret_cast<const f32x4 *>(po + at * D + d + i);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) o[i + y] += k * v[y];
+            for (int e = 0; e < E; ++e) o[e] += ki * p[e];
         }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const size_t at = ((size_t)(r.off[s] + row / a.G) * a.Hq + h * a.G + row % a.G) * D + d;
+    l = wave_sum(l);
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
+    for (int e = 0; e < E; ++e) sum[wave][lane * E + e] = o[e];
+    __syncthreads();
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const size_t to = ((size_t)(r.off[s] + row / a.G) * a.Hq + h * a.G + row % a.G) * D;
+    for (int d = threadIdx.x; d < D; d += kThreads) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) v += sum[w][d];
         if (F32)
-            ((float *)a.out)[at + i] = o[i] * inv;
+            ((float *)a.out)[to + d] = v * inv;
         else
-            ((uint16_t *)a.out)[at + i] = f32_to_bf16_rne(o[i] * inv);
+            ((uint16_t *)a.out)[to + d] = f32_to_bf16_rne(v * inv);
     }
 }
 
 template <int MT, int D, bool F32>
 hipError_t attend_launch(const KvAttendArgs &a, hipStream_t s) {
     constexpr int lds = attend_lds_bytes<MT, D, F32>();
-    if (lds > 65536) {
+    static_assert(lds <= 160 * 1024 - 2 * kWaves * MT * 16 * 4, "one compute unit's LDS");
+    if (lds > 32768) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(attend_kernel<MT, D, F32>),
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
     }
     hipLaunchKernelGGL((attend_kernel<MT, D, F32>), dim3(a.nwg), dim3(kThreads), lds, s, a);
-    hipError_t e = hipGetLastError();
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    int units = 0;
-    for (int q = 0; q < a.r.nseq; ++q) units += a.r.Hkv * (((a.r.off[q + 1] - a.r.off[q]) * a.G + 16 * MT - 1) / (16 * MT));
-    hipLaunchKernelGGL((combine_kernel<D, F32>), dim3(units * MT), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((combine_kernel<D, F32>), dim3(a.T * a.Hq), dim3(kThreads), 0, s, a);
     return hipGetLastError();
 }
 
@@ -670,7 +774,7 @@ size_t kv4_attend_plan(KvAttendArgs &a, int n_cu) {
     const int tiles = (most + 15) / 16, cap = max_mt(a.r.D, a.f32);
     const int blocks = (tiles + cap - 1) / cap;
     a.mt = (tiles + blocks - 1) / blocks;
-    a.nwg = n_cu * 2;
+    a.nwg = n_cu * (a.r.D < 256 ? 2 : 1);  // what runs at once
     return (size_t)a.nwg * 2 * 16 * a.mt * (a.r.D + 2) * 4;
 }
 
