@@ -153,7 +153,6 @@ __global__ __launch_bounds__(kThreads) void append_kernel(KvAppendArgs a) {
 constexpr float kNone = -3.402823466e38f;  // running maximum before the first score
 constexpr float kSlack = 8.f;              // a score may pass the maximum by this (log2) before it moves
 constexpr int kMinShare = 8;               // steps of a workgroup at least
-constexpr int kStages = 3;                 // steps of a wave's ring
 
 __device__ __forceinline__ bf16x8 dequant8(unsigned w, float s) {
     union {
@@ -296,6 +295,11 @@ __device__ __forceinline__ void settle(T &v) {
     asm volatile("" : "+v"(v));
 }
 
+// Workgroups of a compute unit, by the registers and the LDS they take, and
+// the steps of a wave's ring that this leaves room for.
+constexpr int groups(int MT, int D) { return D == 256 ? 1 : MT > 1 ? 2 : D == 128 ? 3 : 4; }
+constexpr int stages(int MT, int D) { return D == 128 && MT == 1 ? 2 : 3; }
+
 template <int MT, int D, bool F32>
 constexpr int ring_offset() {  // the queries' operand terms lie before the rings
     return MT * 16 * D * 2 * (F32 ? 3 : 1);
@@ -303,7 +307,7 @@ constexpr int ring_offset() {  // the queries' operand terms lie before the ring
 
 template <int MT, int D, bool F32>
 constexpr int attend_lds_bytes() {
-    const int q = ring_offset<MT, D, F32>() + kWaves * kStages * 2 * Tile<D>::kBytes, m = 2 * MT * 16 * D * 4;
+    const int q = ring_offset<MT, D, F32>() + kWaves * stages(MT, D) * 2 * Tile<D>::kBytes, m = 2 * MT * 16 * D * 4;
     return q > m ? q : m;
 }
 
@@ -312,11 +316,12 @@ constexpr int attend_lds_bytes() {
 constexpr int max_mt(int D, bool f32) { return D == 64 ? 4 : D == 128 ? (f32 ? 2 : 4) : 1; }
 
 template <int MT, int D, bool F32>
-__global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void attend_kernel(KvAttendArgs a) {
+__global__ __launch_bounds__(kThreads, groups(MT, D)) void attend_kernel(KvAttendArgs a) {
     constexpr int NS = F32 ? 3 : 1;  // bf16 terms of q and of the probabilities
     constexpr int KS = D / 32;       // k steps of the first product
     constexpr int C = D / 16;        // row tiles of the second
     constexpr int BR = 16 * MT;
+    constexpr int kStages = stages(MT, D);
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     __shared__ float wm[kWaves][BR], wl[kWaves][BR];
     uint16_t *lq = reinterpret_cast<uint16_t *>(lds);  // [MT][NS][KS][64][8]
@@ -774,7 +779,7 @@ size_t kv4_attend_plan(KvAttendArgs &a, int n_cu) {
     const int tiles = (most + 15) / 16, cap = max_mt(a.r.D, a.f32);
     const int blocks = (tiles + cap - 1) / cap;
     a.mt = (tiles + blocks - 1) / blocks;
-    a.nwg = n_cu * (a.r.D < 256 ? 2 : 1);  // what runs at once
+    a.nwg = n_cu * groups(a.mt, a.r.D);  // what runs at once
     return (size_t)a.nwg * 2 * 16 * a.mt * (a.r.D + 2) * 4;
 }
 
