@@ -114,22 +114,35 @@ __device__ __forceinline__ double kept_weight(const ExpTable &et, const RowState
     return w >= st.minp ? w : 0.0;
 }
 
-__device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v += (uint64_t)__shfl_xor((unsigned long long)v, d);
-    return v;
+template <int CTRL>
+__device__ __forceinline__ uint64_t dpp_u64(uint64_t v) {  // 0 where the source lane is outside the row
+    const int lo = __builtin_amdgcn_update_dpp(0, (int)(unsigned)v, CTRL, 0xF, 0xF, false);
+    const int hi = __builtin_amdgcn_update_dpp(0, (int)(v >> 32), CTRL, 0xF, 0xF, false);
+    return ((uint64_t)(unsigned)hi << 32) | (unsigned)lo;
 }
 
-__device__ __forceinline__ int wave_scan_i32(int v) { return wave_incl_scan(v); }
+__device__ __forceinline__ uint64_t lane_u64(uint64_t v, int lane) {
+    return ((uint64_t)(unsigned)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32) |
+           (unsigned)__builtin_amdgcn_readlane((int)(unsigned)v, lane);
+}
+
+// As wave_sum and wave_incl_scan of common.h, for 64 bits.
+__device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) {
+    v += dpp_u64<0x128>(v);  // row_ror:8, 4, 2, 1
+    v += dpp_u64<0x124>(v);
+    v += dpp_u64<0x122>(v);
+    v += dpp_u64<0x121>(v);
+    return lane_u64(v, 0) + lane_u64(v, 16) + lane_u64(v, 32) + lane_u64(v, 48);
+}
 
 __device__ __forceinline__ uint64_t wave_scan_u64(uint64_t v) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint64_t o = (uint64_t)__shfl_up((unsigned long long)v, d);
-        if (lane >= d) v += o;
-    }
-    return v;
+    v += dpp_u64<0x111>(v);  // row_shr:1, 2, 4, 8
+    v += dpp_u64<0x112>(v);
+    v += dpp_u64<0x114>(v);
+    v += dpp_u64<0x118>(v);
+    const uint64_t r0 = lane_u64(v, 15), r1 = lane_u64(v, 31), r2 = lane_u64(v, 47);
+    const int row = (threadIdx.x & 63) >> 4;
+    return v + (row > 0 ? r0 : 0) + (row > 1 ? r1 : 0) + (row > 2 ? r2 : 0);
 }
 
 // Block of NT threads: the lowest index whose running sum of f(i) exceeds
@@ -363,9 +376,31 @@ __device__ __forceinline__ void load_block(const SampleArgs &a, int t, int first
 }
 
 __device__ __forceinline__ unsigned wave_max_u32(unsigned v) {
+    v = max(v, (unsigned)dpp_ror<8>((int)v));
+    v = max(v, (unsigned)dpp_ror<4>((int)v));
+    v = max(v, (unsigned)dpp_ror<2>((int)v));
+    v = max(v, (unsigned)dpp_ror<1>((int)v));
+    const unsigned a = (unsigned)__builtin_amdgcn_readlane((int)v, 0), b = (unsigned)__builtin_amdgcn_readlane((int)v, 16);
+    const unsigned c = (unsigned)__builtin_amdgcn_readlane((int)v, 32), d = (unsigned)__builtin_amdgcn_readlane((int)v, 48);
+    return max(max(a, b), max(c, d));
+}
+
+// Exclusive running sum over a block of NT threads; `total` gets the sum.
+// `sh` [NT / 64] is free afterwards.
+template <int NT>
+__device__ __forceinline__ int block_before(int v, int *sh, int &total) {
+    const int incl = wave_incl_scan(v), wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 63) sh[wave] = incl;
+    __syncthreads();
+    int before = incl - v;
+    total = 0;
 #pragma unroll
-    for (int d = 32; d; d >>= 1) v = max(v, (unsigned)__shfl_xor((int)v, d));
-    return v;
+    for (int w = 0; w < NT / 64; ++w) {
+        if (w < wave) before += sh[w];
+        total += sh[w];
+    }
+    __syncthreads();
+    return before;
 }
 
 // Over a block of NT threads; every thread gets the result, `sh` [NT / 64] is
@@ -709,7 +744,7 @@ __device__ void plan_row(Bins &h, const Filter &f, const Kind &kind, uint64_t ma
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const uint64_t n0 = h.cnt[2 * tid], n1 = h.cnt[2 * tid + 1];
     const uint64_t m0 = kind.by_k ? 0 : h.mass[2 * tid], m1 = kind.by_k ? 0 : h.mass[2 * tid + 1];
-    uint64_t nb = (uint64_t)wave_scan_i32((int)(n0 + n1)) - n0 - n1;  // counts are below 2^18
+    uint64_t nb = (uint64_t)wave_incl_scan((int)(n0 + n1)) - n0 - n1;  // counts are below 2^18
     uint64_t mb = kind.by_k ? 0 : wave_scan_u64(m0 + m1) - m0 - m1;
     if (lane == 63) h.wc[wave] = nb + n0 + n1, h.wm[wave] = mb + m0 + m1;
     if (tid == 0) h.plan = Plan{0, kBins - 1, 1, 1u, 0, mass};  // not among the counted
@@ -925,25 +960,26 @@ typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
 // Bitonic sort of `size` (a power of two >= 64) list entries by NT threads,
 // ascending: key descending, index ascending.  Strides up to 64 stay inside
 // the 128 entries of a wave and need no barrier of the block.
-// Up to 256 entries are put in the place that the number of smaller ones
-// gives, without any exchange.
+// Up to NT / 4 entries (all different) are put in the place that the number of
+// smaller ones gives, four threads counting for each; the rest keep ~0.
 template <int NT>
-__device__ void sort_list(uint64_t *list, int size) {
-    if (size <= 256) {
-        const int i = threadIdx.x;
+__device__ void sort_list(uint64_t *list, int n, int size) {
+    if (n <= NT / 4) {
+        const int i = threadIdx.x >> 2, part = threadIdx.x & 3, each = ((n + 7) >> 3) * 2;  // 4 of them: up to 8 n / 8, inside the list
         uint64_t mine = 0;
         int rank = 0;
-        if (i < size) {
+        if (i < n) {
             mine = list[i];
-#pragma unroll 4
-            for (int j = 0; j < size; j += 2) {
+#pragma unroll 2
+            for (int j = part * each; j < (part + 1) * each; j += 2) {
                 const u64x2 v = *reinterpret_cast<const u64x2 *>(list + j);
-                // equal entries only past the list's length
-                rank += (v[0] < mine || (v[0] == mine && j < i)) + (v[1] < mine || (v[1] == mine && j + 1 < i));
+                rank += (v[0] < mine) + (v[1] < mine);
             }
         }
+        rank += __builtin_amdgcn_update_dpp(0, rank, 0xB1, 0xF, 0xF, false);  // quad_perm 1, 0, 3, 2
+        rank += __builtin_amdgcn_update_dpp(0, rank, 0x4E, 0xF, 0xF, false);  // quad_perm 2, 3, 0, 1
         __syncthreads();
-        if (i < size) list[rank] = mine;
+        if (i < n && part == 0) list[rank] = mine;
         __syncthreads();
         return;
     }
@@ -973,9 +1009,10 @@ struct ListShared {
 // The threshold of a row from its list of n entries (in s.list, unsorted):
 // sets st.key and st.last and calls add(index, units) for every kept entry.
 // A list for top_p alone is first narrowed to those of 1024 equal parts of its
-// key range that the threshold lies in.
+// key range that the threshold lies in.  False if the threshold is not in the
+// list (the sums above it and in it say so).
 template <int NT, int CAP, typename Add>
-__device__ void resolve_list(ListShared<CAP> &s, int n, const Filter &f, const Kind &kind, const Plan &p, const ExpTable &et,
+__device__ bool resolve_list(ListShared<CAP> &s, int n, const Filter &f, const Kind &kind, const Plan &p, const ExpTable &et,
                              RowState &st, Add add) {
     constexpr int W = NT / 64;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -995,6 +1032,7 @@ __device__ void resolve_list(ListShared<CAP> &s, int n, const Filter &f, const K
             hi = max(hi, k);
         }
         for (int i = tid; i < 1024; i += NT) s.sub[i] = 0;
+        if (tid == 0) s.kept = -1;
         hi = wave_max_u32(hi);
         lo = ~wave_max_u32(~lo);
         if (lane == 0) s.klo[wave] = lo, s.khi[wave] = hi;
@@ -1022,6 +1060,7 @@ __device__ void resolve_list(ListShared<CAP> &s, int n, const Filter &f, const K
         }
         __syncthreads();
         const int at = s.kept;
+        if (at < 0) return false;
         above = s.ws[W - 1];
         // entries above are kept, those of the part go on
         uint64_t mine[CAP / NT];
@@ -1042,11 +1081,11 @@ __device__ void resolve_list(ListShared<CAP> &s, int n, const Filter &f, const K
     while (size < n) size <<= 1;
     for (int i = n + tid; i < size; i += NT) s.list[i] = ~0ull;
     __syncthreads();
-    sort_list<NT>(s.list, size);
+    sort_list<NT>(s.list, n, size);
     // running weights of the list: thread tid holds `per` of them
     const int per = (size + NT - 1) / NT, b = tid * per;
     const int nk = kind.by_k ? min(kind.k, n) : n, e = min(b + per, nk);
-    if (tid == 0) s.kept = nk;
+    if (tid == 0) s.kept = kind.by_p ? 0 : nk;
     if (kind.by_p) {
         uint64_t mine = 0;
         for (int i = b; i < e; ++i) mine += units(weight_of(s.list[i]));
@@ -1071,10 +1110,12 @@ __device__ void resolve_list(ListShared<CAP> &s, int n, const Filter &f, const K
     }
     __syncthreads();
     const int kept = s.kept;
+    if (kept == 0) return false;
     st.key = entry_key(s.list[kept - 1]);
     st.last = (int)(unsigned)s.list[kept - 1];
     for (int i = b; i < e && i < kept; ++i) keep(s.list[i]);
     __syncthreads();
+    return true;
 }
 
 union DrawShared {
@@ -1116,28 +1157,31 @@ __global__ __launch_bounds__(kRowThreads) void resolve_kernel(SampleArgs a, Work
         st.key = kind.km;
         st.last = st.token = lo;
         st.sum = kUnit;
-    } else if (p.slow) {
-        descend_row<kRowThreads, F32>(et, a, r, f, kind, st, s.h, sums, &found);
-        uint64_t total;
-        st.token = pick<kRowThreads>(
-            a.V, [&](int i) { return units(kept_weight(et, st, value<F32>(r, i), i)); },
-            [&](uint64_t total) { return target(uu, total); }, sums, &found, &total);
-        st.sum = (double)total;
     } else {
-        if (planned) {
+        bool slow = p.slow;
+        if (planned && !slow) {
             n = min(n, w.L);  // V <= L where that is below kList
             if (tid < n) s.l.list[tid] = head;
             for (int i = kRowThreads + tid; i < n; i += kRowThreads) s.l.list[i] = w.list[(size_t)row * w.L + i];
             __syncthreads();
-            resolve_list<kRowThreads>(s.l, n, f, kind, p, et, st,
-                                      [&](int i, uint64_t m) { atomicAdd(&cs[i / kChunk], (unsigned long long)m); });
+            slow = !resolve_list<kRowThreads>(s.l, n, f, kind, p, et, st,
+                                              [&](int i, uint64_t m) { atomicAdd(&cs[i / kChunk], (unsigned long long)m); });
         }
-        const uint64_t mc = cs[lane], total = wave_sum_u64(mc);
-        const uint64_t want = target(uu, total);
-        uint64_t before;
-        const int c = lane_of_mass(mc, want, before);
-        st.token = find_in_chunk<kRowThreads, F32>(
-            a, t, c, want - before, [&](float v, int i) { return units(kept_weight(et, st, v, i)); }, sums, &found);
+        uint64_t total;
+        if (slow) {
+            descend_row<kRowThreads, F32>(et, a, r, f, kind, st, s.h, sums, &found);
+            st.token = pick<kRowThreads>(
+                a.V, [&](int i) { return units(kept_weight(et, st, value<F32>(r, i), i)); },
+                [&](uint64_t total) { return target(uu, total); }, sums, &found, &total);
+        } else {
+            const uint64_t mc = cs[lane];
+            total = wave_sum_u64(mc);
+            const uint64_t want = target(uu, total);
+            uint64_t before;
+            const int c = lane_of_mass(mc, want, before);
+            st.token = find_in_chunk<kRowThreads, F32>(
+                a, t, c, want - before, [&](float v, int i) { return units(kept_weight(et, st, v, i)); }, sums, &found);
+        }
         st.sum = (double)total;
     }
     if (st.token >= 0) x = value<F32>(r, st.token);
@@ -1156,7 +1200,7 @@ constexpr int kSmall = 8 * kSmallRound;
 constexpr int kSmallList = 2048;
 
 union SmallShared {
-    Bins b;
+    unsigned b[2048];
     ListShared<kSmallList> l;
     Histogram h;
 };
@@ -1168,13 +1212,15 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
     extern __shared__ __attribute__((aligned(16))) float tokens[];  // whole rounds, -inf past the end
     __shared__ ExpTable et;
     __shared__ SmallShared s;
-    __shared__ uint64_t sums[8 * W];
+    __shared__ uint64_t sums[8 * W], masses[W];
     __shared__ unsigned sk[W];
     __shared__ int sn[W], ranks[2 * W], found;
     const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const void *r = row_of<F32>(a, t);
     const int E = (a.V + kSmallRound - 1) / kSmallRound;  // rounds of 4 tokens a thread
     f32x4 *own = reinterpret_cast<f32x4 *>(tokens) + tid;  // round e at own[e * NT]
+    float v = -INFINITY;  // this thread's largest
+    int nv = 0;
     {
         constexpr int Q = kVec<F32>, B = kSmall / Q / NT;
         float x[B][Q];
@@ -1191,19 +1237,18 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
 #pragma unroll
         for (int y = 0; y < B; ++y) {
             const int i = Q * (y * NT + tid);
-            if (i < E * kSmallRound)
+            if (i < E * kSmallRound) {
 #pragma unroll
                 for (int e = 0; e < Q; e += 4)
                     *reinterpret_cast<f32x4 *>(tokens + i + e) =
                         f32x4{clean(x[y][e]), clean(x[y][e + 1]), clean(x[y][e + 2]), clean(x[y][e + 3])};
+            }
         }
     }
     const Filter f = filter_of(a, t);
     const float uu = u ? u[t] : 0.f;
     et.fill();
     __syncthreads();
-    float v = -INFINITY;
-    int nv = 0;
 #pragma unroll 1
     for (int e = 0; e < E; ++e) {
         const f32x4 x = own[e * NT];
@@ -1233,12 +1278,20 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
         st.last = st.token = found;
         st.sum = kUnit;
     } else if (km) {
+        bool summed = false;
         if (kind.by_k || kind.by_p) {
+            // tokens of at least `top` are kept, those of at least `low` and less than `top` listed
             Plan p{0, kBins - 1, 0, 1u, 0, 0};
-            const float scale = bin_scale(f.invt);
+            float low = -3.402823466e38f, top = INFINITY;
+            bool narrow = true;
+            double want = (double)kind.k;
             if (kind.by_k) {  // a thread's tokens are a group
-                p.slow = kind.k > NT * 7 / 8;
-                if (!p.slow) p.cut = key_of_rank<NT>(mykey, kind.k, ranks);
+                if (kind.k <= NT * 7 / 8) {
+                    low = of_key(key_of_rank<NT>(mykey, kind.k, ranks));
+                    narrow = false;
+                } else {  // the least of the groups' largest, which must have the first k above it
+                    low = of_key(~block_max_u32<NT>(~mykey, sk));
+                }
             } else {
                 uint64_t m = 0;
 #pragma unroll 1
@@ -1247,72 +1300,133 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
 #pragma unroll
                     for (int i = 0; i < 4; ++i) m += raw_units(weight(et, x[i], st.first, f.invt));
                 }
-                p.mass = block_sum_u64<NT>(m - off_units(4 * E), sums);
-                p.cut = cut_key(st.first, f.invt, cut_distance(f, (double)p.mass, a.V));
+                p.mass = block_sum_u64<NT>(m - off_units(4 * E), masses);
+                want = (double)f.topp * (double)p.mass;
+                const unsigned cut = cut_key(st.first, f.invt, cut_distance(f, (double)p.mass, a.V));
+                if (cut > 1u) low = of_key(cut);
             }
-            const float low = p.cut > 1u ? of_key(p.cut) : -3.402823466e38f;
-            int n = 0;
+            // Narrowing, where too many are left: a histogram of 2048 equal parts of
+            // [low, first], by the count or by float32 weights in 2^-17 of the first's
+            // (whole rows fit 32 bits).  Those sums are good to 2^-12 or so; the part
+            // is widened by that, and the sum above the list taken again in units.
+            int n, before = 0;
+            auto count = [&]() {  // of the list: this thread's place in it, and its length
+                int mine = 0;
+                if (v >= low)
+#pragma unroll 2
+                    for (int e = 0; e < E; ++e) {
+                        const f32x4 x = own[e * NT];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mine += x[i] >= low && x[i] < top;
+                    }
+                before = block_before<NT>(mine, sn, n);
+            };
+            count();
+            if (narrow && n > kSmallList && low > -1e30f && st.first > low) {
+                const float part = 2047.9f / (st.first - low);
+                const float scale = (float)fmin(f.invt * 1.4426950408889634, 1e30);
+                for (int i = tid; i < 2048; i += NT) s.b[i] = 0;
+                __syncthreads();
+                if (v >= low)
+#pragma unroll 1
+                    for (int e = 0; e < E; ++e) {
+                        const f32x4 x = own[e * NT];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (x[i] >= low)
+                                atomicAdd(&s.b[(int)((st.first - x[i]) * part)],
+                                          kind.by_k ? 1u : (unsigned)(131072.f * __builtin_amdgcn_exp2f((x[i] - st.first) * scale) + 0.5f));
+                    }
+                __syncthreads();
+                // parts from the first down, two a thread
+                const unsigned b0 = s.b[2 * tid], b1 = s.b[2 * tid + 1];
+                int incl = wave_incl_scan((int)(b0 + b1));
+                if (lane == 63) sn[wave] = incl;
+                if (tid == 0) ranks[0] = 2047, ranks[1] = -1;
+                __syncthreads();
+                for (int i = 0; i < wave; ++i) incl += sn[i];
+                const unsigned after = (unsigned)incl, mid = after - b1;
+                const float goal = kind.by_k ? (float)kind.k : (float)(want * (131072.0 / kUnit)), slack = kind.by_k ? 0.f : goal * 1e-3f + 64.f;
+                // the list begins after the last part that surely lies above, and ends with the first that surely holds it
+                if ((float)mid < goal - slack) atomicMax(&ranks[1], 2 * tid);
+                if ((float)after < goal - slack) atomicMax(&ranks[1], 2 * tid + 1);
+                if ((float)mid >= goal + slack) atomicMin(&ranks[0], 2 * tid);
+                if ((float)after >= goal + slack) atomicMin(&ranks[0], 2 * tid + 1);
+                __syncthreads();
+                const float width = (st.first - low) / 2047.9f;
+                const int end = ranks[0], begin = ranks[1];
+                // a little beyond the parts' edges, which are rounded differently
+                if (end < 2047) low = fmaxf(low, st.first - width * ((float)end + 1.01f));
+                if (!kind.by_k && begin >= 0) top = st.first - width * ((float)begin + 0.99f);
+                __syncthreads();
+                count();
+            }
+            // what is kept above the list: by parts, for the draw, and in whole
+            for (int i = tid; i < E * W; i += NT) sums[i] = 0;
+            __syncthreads();
+            if (top < INFINITY) {
+                uint64_t all = 0;
+#pragma unroll 1
+                for (int e = 0; e < E; ++e) {
+                    const f32x4 x = own[e * NT];
+                    const bool some = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= top;
+                    if (!__any(some)) continue;
+                    uint64_t m = 0, kept = 0;
+                    if (some)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const double w = weight(et, x[i], st.first, f.invt);
+                            const uint64_t q = x[i] >= top ? units(w) : 0;
+                            m += q;
+                            kept += w >= st.minp ? q : 0;
+                        }
+                    all += m;
+                    kept = wave_sum_u64(kept);
+                    if (lane == 0) sums[e * W + wave] = kept;
+                }
+                p.above_mass = block_sum_u64<NT>(all, masses);
+            }
+            if (v >= low && n <= kSmallList)
+#pragma unroll 2
+                for (int e = 0; e < E; ++e) {
+                    const f32x4 x = own[e * NT];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (x[i] >= low && x[i] < top) s.l.list[before++] = entry_of(x[i], 4 * (e * NT + tid) + i);
+                }
+            __syncthreads();
+            // Ties, or a first k beyond the list; and a narrowing that the exact sums
+            // do not bear out.
+            const uint64_t least = max((uint64_t)1, (uint64_t)ceil((double)f.topp * (double)p.mass));
+            bool slow = n > kSmallList || (kind.by_k ? n < kind.k : p.above_mass >= least);
+            if (!slow)
+                slow = !resolve_list<NT>(s.l, n, f, kind, p, et, st,
+                                         [&](int i, uint64_t m) { atomicAdd((unsigned long long *)&sums[i / 256], (unsigned long long)m); });
+            if (slow) descend_row<NT, F32>(et, a, r, f, kind, st, s.h, masses, &found);
+            summed = !slow;
+        }
+        // the draw: masses of the kept in index order, a part of 256 tokens a wave and round
+        const float keep = st.key > 1u ? of_key(st.key) : -3.402823466e38f;
+        if (!summed)
 #pragma unroll 1
             for (int e = 0; e < E; ++e) {
                 const f32x4 x = own[e * NT];
+                uint64_t m = 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) n += x[i] >= low;
-            }
-            n = (int)block_sum_u64<NT>((uint64_t)n, sums);
-            if (p.slow || n > kSmallList) {  // the histogram, and the few bins of the threshold
-                const unsigned cut = kind.by_k ? 1u : p.cut;
-                const uint64_t mass = p.mass;
-                clear_bins(s.b, NT);
-                __syncthreads();
-#pragma unroll 1
-                for (int e = 0; e < 4 * E; ++e) {
-                    const float x = tokens[4 * ((e >> 2) * NT + tid) + (e & 3)];
-                    if (x != -INFINITY) count_token(s.b, kind, x, cut, st.first, scale, f.invt, et);
+                for (int i = 0; i < 4; ++i) {
+                    const double w = weight(et, x[i], st.first, st.invt);
+                    const bool kept = w >= st.minp && (x[i] > keep || (x[i] == keep && 4 * (e * NT + tid) + i <= st.last));
+                    m += kept ? units(w) : 0;
                 }
-                __syncthreads();
-                plan_row(s.b, f, kind, mass, cut, kSmallList);
-                p = s.b.plan;
+                m = wave_sum_u64(m);
+                if (lane == 0) sums[e * W + wave] = m;
             }
-            if (tid == 0) found = 0;
-            __syncthreads();
-            if (p.slow) {
-                descend_row<NT, F32>(et, a, r, f, kind, st, s.h, sums, &found);
-            } else {
-                const float from = p.cut > 1u ? of_key(p.cut) : -3.402823466e38f;
-                if (v >= from)
-#pragma unroll 1
-                    for (int e = 0; e < 4 * E; ++e) {
-                        const int at = 4 * ((e >> 2) * NT + tid) + (e & 3);
-                        const float x = tokens[at];
-                        if (!(x >= from)) continue;
-                        const int b = bin_of(x, st.first, scale);
-                        if (b >= p.sure && b <= p.end) s.l.list[atomicAdd(&found, 1)] = entry_of(x, at);
-                    }
-                __syncthreads();
-                resolve_list<NT>(s.l, found, f, kind, p, et, st, [](int, uint64_t) {});
-            }
-        }
-        // the draw: masses of the kept in index order, a part a wave and round
-        const float keep = st.key > 1u ? of_key(st.key) : -3.402823466e38f;
-        const bool some = v >= keep;
-#pragma unroll 1
-        for (int e = 0; e < E; ++e) {
-            uint64_t m = 0;
-            if (some) {
-                const f32x4 x = own[e * NT];
-                if (fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= keep)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) m += units(kept_weight(et, st, x[i], 4 * (e * NT + tid) + i));
-            }
-            if (__any(m != 0)) m = wave_sum_u64(m);
-            if (lane == 0) sums[e * W + wave] = m;
-        }
         __syncthreads();
         const uint64_t p0 = 2 * lane < E * W ? sums[2 * lane] : 0, p1 = 2 * lane < E * W ? sums[2 * lane + 1] : 0;
-        const uint64_t total = wave_sum_u64(p0 + p1), want = target(uu, total);
+        const uint64_t total = wave_sum_u64(p0 + p1), pick_at = target(uu, total);
         uint64_t run;
-        int part = 2 * lane_of_mass(p0 + p1, want, run);
-        if (want >= run + sums[part]) run += sums[part++];
+        int part = 2 * lane_of_mass(p0 + p1, pick_at, run);
+        if (pick_at >= run + sums[part]) run += sums[part++];
         if (part % W == wave) {
             const int e = part / W, at = 4 * (e * NT + tid);
             const f32x4 x = own[e * NT];
@@ -1320,9 +1434,9 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
 #pragma unroll
             for (int i = 0; i < 4; ++i) m[i] = units(kept_weight(et, st, x[i], at + i));
             const uint64_t ms = m[0] + m[1] + m[2] + m[3], b0 = run + wave_scan_u64(ms) - ms;
-            if (b0 <= want && want < b0 + ms) {
+            if (b0 <= pick_at && pick_at < b0 + ms) {
                 const uint64_t b1 = b0 + m[0], b2 = b1 + m[1], b3 = b2 + m[2];
-                found = at + (want < b1 ? 0 : want < b2 ? 1 : want < b3 ? 2 : 3);
+                found = at + (pick_at < b1 ? 0 : pick_at < b2 ? 1 : pick_at < b3 ? 2 : 3);
             }
         }
         __syncthreads();
