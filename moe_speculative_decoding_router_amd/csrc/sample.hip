@@ -694,20 +694,27 @@ __device__ __forceinline__ unsigned cut_key(float first, double invt, double nat
 
 //   top_k: the k-th largest of any set of tokens, one of each of some groups,
 //   is no larger than the k-th largest of all.  The largest key with at least
-//   k of the block's keys (one a thread, NT threads) at or above it, found bit
-//   by bit from the top; the low bits are left 0.
+//   k of the block's keys (one a thread, NT threads) at or above it, found two
+//   bits at a time from the top; the low bits are left 0.  `sh` [2 NT / 64].
 template <int NT>
-__device__ unsigned key_of_rank(unsigned key, int k, int *sh) {
+__device__ unsigned key_of_rank(unsigned key, int k, uint64_t *sh) {
+    constexpr int W = NT / 64;
     unsigned cut = 0;
-    for (int bit = 31; bit >= 14; --bit) {
-        const unsigned c = cut | (1u << bit);
-        const int n = __popcll(__ballot(key >= c));
-        if ((threadIdx.x & 63) == 0) sh[(bit & 1) * (NT / 64) + (threadIdx.x >> 6)] = n;
-        __syncthreads();
-        int all = 0;
+#pragma unroll 1
+    for (int bit = 30; bit >= 14; bit -= 2) {
+        uint64_t n = 0;  // three counts of up to 2^11
 #pragma unroll
-        for (int i = 0; i < NT / 64; ++i) all += sh[(bit & 1) * (NT / 64) + i];
-        if (all >= k) cut = c;
+        for (int y = 3; y >= 1; --y) n = (n << 20) | (unsigned)__popcll(__ballot(key >= (cut | ((unsigned)y << bit))));
+        uint64_t *to = sh + ((bit >> 1) & 1) * W;
+        if ((threadIdx.x & 63) == 0) to[threadIdx.x >> 6] = n;
+        __syncthreads();
+        n = 0;
+#pragma unroll
+        for (int i = 0; i < W; ++i) n += to[i];
+        unsigned y = 0;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) y += (int)((n >> (20 * i)) & 0xFFFFF) >= k;
+        cut |= y << bit;
     }
     __syncthreads();
     return max(cut, 1u);
@@ -789,9 +796,11 @@ __global__ __launch_bounds__(kHistThreads) void hist_kernel(SampleArgs a, Work w
     constexpr int E = kRounds<kHistThreads, F32, kHistChunks * kChunk>, Q = kVec<F32>;
     __shared__ ExpTable et;
     __shared__ Bins h;
-    __shared__ int sh, ranks[2 * kHistThreads / 64];
+    __shared__ int sh;
+    __shared__ uint64_t ranks[2 * kHistThreads / 64];
     static_assert(kHistThreads == 1024 && kBins == 2048 && kMaxChunks * kGroups <= kHistThreads, "two bins, a group a thread");
     const int hc = blockIdx.x, row = blockIdx.y, t = w.row0 + row, tid = threadIdx.x;
+    const unsigned group = hc == 0 && tid < w.C * kGroups ? w.group[row * w.C * kGroups + tid] : 0;
     const Filter f = filter_of(a, t);
     const Kind kind = kind_of(f, w, row, a.V);
     if (!kind.by_k && !kind.by_p) return;  // the whole row's workgroups
@@ -799,7 +808,7 @@ __global__ __launch_bounds__(kHistThreads) void hist_kernel(SampleArgs a, Work w
     // about 2 tokens a group lie above the cut.
     if (kind.by_k && kind.k <= w.C * kGroups * 7 / 8 && kind.k <= kList / 4) {
         if (hc) return;
-        const unsigned cut = key_of_rank<kHistThreads>(tid < w.C * kGroups ? w.group[row * w.C * kGroups + tid] : 0, kind.k, ranks);
+        const unsigned cut = key_of_rank<kHistThreads>(group, kind.k, ranks);
         if (tid == 0) w.plan[row] = Plan{0, kBins - 1, 0, cut, 0, 0};
         return;
     }
@@ -960,12 +969,13 @@ typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
 // Bitonic sort of `size` (a power of two >= 64) list entries by NT threads,
 // ascending: key descending, index ascending.  Strides up to 64 stay inside
 // the 128 entries of a wave and need no barrier of the block.
-// Up to NT / 4 entries (all different) are put in the place that the number of
-// smaller ones gives, four threads counting for each; the rest keep ~0.
+// Up to NT / 2 entries (all different) are put in the place that the number of
+// smaller ones gives, two or four threads counting for each; the rest keep ~0.
 template <int NT>
 __device__ void sort_list(uint64_t *list, int n, int size) {
-    if (n <= NT / 4) {
-        const int i = threadIdx.x >> 2, part = threadIdx.x & 3, each = ((n + 7) >> 3) * 2;  // 4 of them: up to 8 n / 8, inside the list
+    if (n <= NT / 2) {
+        const int log = n <= NT / 4 ? 2 : 1;
+        const int i = threadIdx.x >> log, part = threadIdx.x & ((1 << log) - 1), each = ((n + 7) >> 3) << (3 - log);  // 8 | size
         uint64_t mine = 0;
         int rank = 0;
         if (i < n) {
@@ -977,7 +987,7 @@ __device__ void sort_list(uint64_t *list, int n, int size) {
             }
         }
         rank += __builtin_amdgcn_update_dpp(0, rank, 0xB1, 0xF, 0xF, false);  // quad_perm 1, 0, 3, 2
-        rank += __builtin_amdgcn_update_dpp(0, rank, 0x4E, 0xF, 0xF, false);  // quad_perm 2, 3, 0, 1
+        if (log == 2) rank += __builtin_amdgcn_update_dpp(0, rank, 0x4E, 0xF, 0xF, false);  // quad_perm 2, 3, 0, 1
         __syncthreads();
         if (i < n && part == 0) list[rank] = mine;
         __syncthreads();
@@ -1214,7 +1224,7 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
     __shared__ SmallShared s;
     __shared__ uint64_t sums[8 * W], masses[W];
     __shared__ unsigned sk[W];
-    __shared__ int sn[W], ranks[2 * W], found;
+    __shared__ int sn[W], ranks[2], found;
     const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const void *r = row_of<F32>(a, t);
     const int E = (a.V + kSmallRound - 1) / kSmallRound;  // rounds of 4 tokens a thread
@@ -1287,7 +1297,7 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
             double want = (double)kind.k;
             if (kind.by_k) {  // a thread's tokens are a group
                 if (kind.k <= NT * 7 / 8) {
-                    low = of_key(key_of_rank<NT>(mykey, kind.k, ranks));
+                    low = of_key(key_of_rank<NT>(mykey, kind.k, sums));
                     narrow = false;
                 } else {  // the least of the groups' largest, which must have the first k above it
                     low = of_key(~block_max_u32<NT>(~mykey, sk));
@@ -1486,9 +1496,10 @@ __global__ __launch_bounds__(kThreads) void probs_kernel(SampleArgs a, Work w, f
 // ---------------------------------------------------------------------------
 // Drafts matched against the target's own draws: one thread a sequence.
 __global__ __launch_bounds__(64) void match_kernel(AcceptArgs c, const int32_t *drawn) {
-    __shared__ int32_t tok[kMaxTokens], drew[kMaxTokens];
-    const int s = threadIdx.x, T = c.off[c.nseq];
-    if (s < T) tok[s] = c.tokens[s], drew[s] = drawn[s];
+    __shared__ int32_t tok[kMaxTokens], drew[kMaxTokens], parent[kMaxTokens];
+    const int s = threadIdx.x;
+    static_assert(kMaxTokens == 64 && kMaxSegments <= 64, "a thread each");
+    if (s < c.off[c.nseq]) tok[s] = c.tokens[s], drew[s] = drawn[s], parent[s] = c.parent[s];
     __syncthreads();
     if (s >= c.nseq) return;
     const int r0 = c.off[s], n = c.off[s + 1] - r0;
@@ -1502,7 +1513,7 @@ __global__ __launch_bounds__(64) void match_kernel(AcceptArgs c, const int32_t *
             int next = -1;
             if (y >= 0)
                 for (int j = cur + 1; j < n && next < 0; ++j)
-                    if (c.parent[r0 + j] == cur && tok[r0 + j] == y) next = j;
+                    if (parent[r0 + j] == cur && tok[r0 + j] == y) next = j;
             if (next < 0) break;
             cur = next;
         }
