@@ -293,9 +293,9 @@ def _launch_stream(stream, device, owned=()) -> int:
     may still have pending uses there), and the tensors are marked as used
     by the launch stream."""
     import torch
-    cur = torch.cuda.current_stream(device)
     if stream is None:
-        return cur.cuda_stream
+        return torch._C._cuda_getCurrentRawStream(device.index if device.index is not None else torch.cuda.current_device())
+    cur = torch.cuda.current_stream(device)
     sobj = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
     owned = [t for t in owned if t is not None]
     if owned and sobj.cuda_stream != cur.cuda_stream:
@@ -659,18 +659,18 @@ def gate_depths(c, Epred, t_base: float, t_exp: float, stream=None):
 # ---------------------------------------------------------------------------
 def _int_array(values, n: Optional[int] = None, name: str = "offsets"):
     """Host int32 array of a sequence of ints (read by the C side during the call)."""
-    if hasattr(values, "tolist"):
+    if not isinstance(values, (list, tuple)):
         if hasattr(values, "device") and values.device.type != "cpu":
             raise ValueError(f"{name} is read on the host: give a list, an array or a CPU tensor")
-        values = values.tolist()
+        values = values.tolist() if hasattr(values, "tolist") else list(values)
     if n is not None and len(values) != n:
         raise ValueError(f"{name} must have {n} entries, got {len(values)}")
-    return (ctypes.c_int32 * len(values))(*values)
+    return (_i32 * len(values))(*values)
 
 
 def _dense(t, name: str, dtype, shape, device) -> None:
     """_check_tensor for one torch dtype, without building names on the way."""
-    if getattr(t, "dtype", None) != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+    if getattr(t, "dtype", None) is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         _check_tensor(t, name, (str(dtype).replace("torch.", ""),), shape=shape, device=device)
 
 
@@ -678,42 +678,51 @@ def _rows_dtype(t, name: str, dims: int):
     """MOE_F32 / MOE_BF16 of a device tensor [T, ...] whose rows are dense,
     and the elements between rows (size-1 dimensions have no stride)."""
     import torch
-    if getattr(t, "dtype", None) not in (torch.float32, torch.bfloat16):
+    dt = getattr(t, "dtype", None)
+    if dt is not torch.float32 and dt is not torch.bfloat16:
         raise ValueError(f"{name} must be a float32 or bfloat16 tensor")
-    if t.dim() != dims:
+    shape = t.shape
+    if len(shape) != dims:
         raise ValueError(f"{name} must have {dims} dimensions")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor, got {t.device}")
+    code = MOE_F32 if dt is torch.float32 else MOE_BF16
     row = 1
+    for n in shape[1:]:
+        row *= n
+    if t.is_contiguous():
+        return code, row
+    strides, dense = t.stride(), 1
     for d in range(dims - 1, 0, -1):
-        if t.shape[d] != 1 and t.stride(d) != row:
+        if shape[d] != 1 and strides[d] != dense:
             raise ValueError(f"{name} must have dense rows; only the distance between rows is free")
-        row *= t.shape[d]
-    stride = t.stride(0) if t.shape[0] > 1 else row
+        dense *= shape[d]
+    stride = strides[0] if shape[0] > 1 else row
     if stride < row:
         raise ValueError(f"{name} has overlapping rows")
-    return MOE_F32 if t.dtype == torch.float32 else MOE_BF16, stride
+    return code, stride
 
 
-class _on_device:
-    """Makes `device` current during a launch, as torch's own operators do."""
-
-    def __init__(self, device):
-        import torch
-        self.guard = torch.cuda.device(device) if torch.cuda.current_device() != device.index else None
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *a):
-        if self.guard is not None:
-            self.guard.__exit__(*a)
-
-
-def _aligned_ws(nbytes: int, device):
+def _call(fn, device, stream, owned, *args) -> None:
+    """fn(*args, stream) with `device` current, as torch's own operators run."""
     import torch
-    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args, _launch_stream(stream, device, owned)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _launch_stream(stream, device, owned)))
+
+
+def _workspace(need: int, what: str, device, workspace, owned):
+    import torch
+    if need == 0:
+        raise MoeError(-1, lib().moe_last_error().decode())
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        owned.append(workspace)
+    else:
+        _check_tensor(workspace, what, ("uint8",), numel=need, device=device, at_least=True)
+    return workspace
 
 
 @dataclass
@@ -738,13 +747,14 @@ class KV4Cache:
     def _c(self, device) -> _KvCache:
         import torch
         d = self.data
-        if getattr(d, "dtype", None) != torch.uint8 or not d.is_contiguous() or d.device != device:
+        if getattr(d, "dtype", None) is not torch.uint8 or d.device != device or not d.is_contiguous():
             raise ValueError(f"cache.data must be a contiguous uint8 tensor on {device}")
         if self.page < 16 or self.Hkv < 1 or self.D < 32:
             raise ValueError(f"cache sizes page={self.page}, Hkv={self.Hkv}, D={self.D} are not a cache's")
-        if d.numel() == 0 or d.numel() % self.page_bytes:
-            raise ValueError(f"cache.data has {d.numel()} bytes, pages have {self.page_bytes}")
-        return _KvCache(d.data_ptr(), self.num_pages, self.page, self.Hkv, self.D)
+        n, size = d.numel(), self.page_bytes
+        if n == 0 or n % size:
+            raise ValueError(f"cache.data has {n} bytes, pages have {size}")
+        return _KvCache(d.data_ptr(), n // size, self.page, self.Hkv, self.D)
 
 
 def kv4_cache(num_pages: int, page: int, Hkv: int, D: int, device=None) -> KV4Cache:
@@ -759,12 +769,13 @@ def kv4_cache(num_pages: int, page: int, Hkv: int, D: int, device=None) -> KV4Ca
 
 def _kv_rows(table, lengths, offsets, device):
     import torch
-    if getattr(table, "dtype", None) != torch.int32 or table.dim() != 2 or not table.is_contiguous() or table.device != device:
+    if (getattr(table, "dtype", None) is not torch.int32 or table.device != device or len(table.shape) != 2
+            or not table.is_contiguous()):
         raise ValueError(f"table must be a contiguous int32 [nseq, max_pages] tensor on {device}")
-    n = int(table.shape[0])
+    n, pages = table.shape
     off = _int_array(offsets, n + 1)
     _dense(lengths, "lengths", torch.int32, (n,), device)
-    r = _KvRows(table.data_ptr(), int(table.shape[1]), lengths.data_ptr(), n, ctypes.addressof(off))
+    r = _KvRows(table.data_ptr(), pages, lengths.data_ptr(), n, ctypes.addressof(off))
     r._keep = off
     return r, n
 
@@ -784,9 +795,10 @@ def kv4_append(cache: KV4Cache, k, v, table, lengths, offsets, *, path=None, cou
     import torch
     dtype, ks = _rows_dtype(k, "k", 3)
     vt, vs = _rows_dtype(v, "v", 3)
-    dev, T = k.device, int(k.shape[0])
+    dev, shape = k.device, k.shape
+    T = shape[0]
     c = cache._c(dev)
-    if tuple(k.shape[1:]) != (cache.Hkv, cache.D) or v.shape != k.shape or vt != dtype or v.device != dev:
+    if shape[1] != cache.Hkv or shape[2] != cache.D or v.shape != shape or vt != dtype or v.device != dev:
         raise ValueError(f"k and v must be [T, {cache.Hkv}, {cache.D}] tensors of one type and device")
     r, n = _kv_rows(table, lengths, offsets, dev)
     if (path is None) != (count is None):
@@ -796,11 +808,9 @@ def kv4_append(cache: KV4Cache, k, v, table, lengths, offsets, *, path=None, cou
         _dense(count, "count", torch.int32, (n,), dev)
         if return_stored:
             raise ValueError("return_stored is for whole calls, without path")
-    out = [torch.empty((T, cache.Hkv, cache.D), dtype=k.dtype, device=dev) for _ in range(2)] if return_stored else [None, None]
-    with _on_device(dev):
-        s = _launch_stream(stream, dev, out)
-        _check(lib().kv4_append(ctypes.byref(c), ctypes.byref(r), k.data_ptr(), v.data_ptr(), ks, vs, T, dtype, _ptr(path),
-                                _ptr(count), _ptr(out[0]), _ptr(out[1]), s))
+    out = [torch.empty(shape, dtype=k.dtype, device=dev) for _ in range(2)] if return_stored else [None, None]
+    _call(lib().kv4_append, dev, stream, out, ctypes.byref(c), ctypes.byref(r), k.data_ptr(), v.data_ptr(), ks, vs, T, dtype,
+          _ptr(path), _ptr(count), _ptr(out[0]), _ptr(out[1]))
     return tuple(out) if return_stored else None
 
 
@@ -815,55 +825,38 @@ def kv4_attend(cache: KV4Cache, q, table, lengths, offsets, *, parent=None, scal
     kv4_attend_workspace_bytes, one per stream; None allocates."""
     import torch
     dtype, qs = _rows_dtype(q, "q", 3)
-    dev, T, Hq = q.device, int(q.shape[0]), int(q.shape[1])
-    if q.shape[2] != cache.D:
+    dev, shape = q.device, q.shape
+    T, Hq = shape[0], shape[1]
+    if shape[2] != cache.D:
         raise ValueError(f"q must be [T, Hq, {cache.D}]")
     c = cache._c(dev)
     r, _ = _kv_rows(table, lengths, offsets, dev)
     par = None if parent is None else _int_array(parent, T, "parent")
-    L = lib()
-    with _on_device(dev):
-        need = L.kv4_attend_workspace_bytes(ctypes.byref(c), ctypes.byref(r), T, Hq, dtype)
-        if need == 0:
-            raise MoeError(-1, L.moe_last_error().decode())
-        owned = []
-        if workspace is None:
-            workspace = _aligned_ws(need, dev)
-            owned.append(workspace)
-        else:
-            _check_tensor(workspace, "workspace", ("uint8",), numel=need, device=dev, at_least=True)
-        if out is None:
-            out = torch.empty((T, Hq, cache.D), dtype=q.dtype, device=dev)
-            owned.append(out)
-        else:
-            _dense(out, "out", q.dtype, tuple(q.shape), dev)
-        s = _launch_stream(stream, dev, owned)
-        _check(L.kv4_attend(ctypes.byref(c), ctypes.byref(r), q.data_ptr(), qs, T, Hq, dtype,
-                            cache.D ** -0.5 if scale is None else scale,
-                            None if par is None else ctypes.addressof(par), out.data_ptr(), workspace.data_ptr(),
-                            workspace.numel(), s))
+    owned = []
+    need = lib().kv4_attend_workspace_bytes(ctypes.byref(c), ctypes.byref(r), T, Hq, dtype)
+    workspace = _workspace(need, "workspace", dev, workspace, owned)
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=dev)
+        owned.append(out)
+    else:
+        _dense(out, "out", q.dtype, shape, dev)
+    _call(lib().kv4_attend, dev, stream, owned, ctypes.byref(c), ctypes.byref(r), q.data_ptr(), qs, T, Hq, dtype,
+          cache.D ** -0.5 if scale is None else scale, None if par is None else ctypes.addressof(par), out.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
     return out
 
 
 def _filters(T: int, dev, temperature, top_k, top_p, min_p) -> _Sampling:
     import torch
-    for name, t, d in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
-                       ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
-        if t is not None:
-            _dense(t, name, d, (T,), dev)
+    if temperature is not None:
+        _dense(temperature, "temperature", torch.float32, (T,), dev)
+    if top_k is not None:
+        _dense(top_k, "top_k", torch.int32, (T,), dev)
+    if top_p is not None:
+        _dense(top_p, "top_p", torch.float32, (T,), dev)
+    if min_p is not None:
+        _dense(min_p, "min_p", torch.float32, (T,), dev)
     return _Sampling(_ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p))
-
-
-def _sampling_ws(T: int, V: int, dev, workspace, owned):
-    need = lib().sample_workspace_bytes(T, V)
-    if need == 0:
-        raise MoeError(-1, lib().moe_last_error().decode())
-    if workspace is None:
-        workspace = _aligned_ws(need, dev)
-        owned.append(workspace)
-    else:
-        _check_tensor(workspace, "workspace", ("uint8",), numel=need, device=dev, at_least=True)
-    return workspace
 
 
 def sample_tokens(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None, return_probs: bool = False,
@@ -876,18 +869,17 @@ def sample_tokens(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=
     its probability, and with return_probs the whole filtered distribution."""
     import torch
     dtype, stride = _rows_dtype(logits, "logits", 2)
-    dev, T, V = logits.device, int(logits.shape[0]), int(logits.shape[1])
+    dev = logits.device
+    T, V = logits.shape
     _dense(u, "u", torch.float32, (T,), dev)
     f = _filters(T, dev, temperature, top_k, top_p, min_p)
     token = torch.empty(T, dtype=torch.int32, device=dev)
     prob = torch.empty(T, dtype=torch.float32, device=dev)
     probs = torch.empty((T, V), dtype=torch.float32, device=dev) if return_probs else None
     owned = [token, prob, probs]
-    ws = _sampling_ws(T, V, dev, workspace, owned)
-    with _on_device(dev):
-        s = _launch_stream(stream, dev, owned)
-        _check(lib().sample_tokens(logits.data_ptr(), stride, T, V, dtype, ctypes.byref(f), u.data_ptr(), token.data_ptr(),
-                                   prob.data_ptr(), _ptr(probs), ws.data_ptr(), ws.numel(), s))
+    ws = _workspace(lib().sample_workspace_bytes(T, V), "workspace", dev, workspace, owned)
+    _call(lib().sample_tokens, dev, stream, owned, logits.data_ptr(), stride, T, V, dtype, ctypes.byref(f), u.data_ptr(),
+          token.data_ptr(), prob.data_ptr(), _ptr(probs), ws.data_ptr(), ws.numel())
     return token, prob, probs
 
 
@@ -904,7 +896,8 @@ def accept_drafts(logits, tokens, offsets, u, *, parent=None, draft_probs=None, 
     int32: the rows to keep, count [nseq] int32: how many)."""
     import torch
     dtype, stride = _rows_dtype(logits, "logits", 2)
-    dev, T, V = logits.device, int(logits.shape[0]), int(logits.shape[1])
+    dev = logits.device
+    T, V = logits.shape
     _dense(tokens, "tokens", torch.int32, (T,), dev)
     _dense(u, "u", torch.float32, (T,), dev)
     off = _int_array(offsets)
@@ -922,11 +915,8 @@ def accept_drafts(logits, tokens, offsets, u, *, parent=None, draft_probs=None, 
     path = torch.empty(T, dtype=torch.int32, device=dev)
     count = torch.empty(n, dtype=torch.int32, device=dev)
     owned = [out, path, count]
-    ws = _sampling_ws(T, V, dev, workspace, owned)
-    with _on_device(dev):
-        s = _launch_stream(stream, dev, owned)
-        _check(lib().accept_drafts(logits.data_ptr(), stride, T, V, dtype, ctypes.byref(f), tokens.data_ptr(), n,
-                                   ctypes.addressof(off), None if par is None else ctypes.addressof(par), _ptr(draft_probs),
-                                   u.data_ptr(), _ptr(u_final), out.data_ptr(), path.data_ptr(), count.data_ptr(),
-                                   ws.data_ptr(), ws.numel(), s))
+    ws = _workspace(lib().sample_workspace_bytes(T, V), "workspace", dev, workspace, owned)
+    _call(lib().accept_drafts, dev, stream, owned, logits.data_ptr(), stride, T, V, dtype, ctypes.byref(f), tokens.data_ptr(), n,
+          ctypes.addressof(off), None if par is None else ctypes.addressof(par), _ptr(draft_probs), u.data_ptr(), _ptr(u_final),
+          out.data_ptr(), path.data_ptr(), count.data_ptr(), ws.data_ptr(), ws.numel())
     return out, path, count

@@ -172,6 +172,11 @@ struct Units {
     long long incl;                   // running sum of steps over heads and row blocks
 };
 
+__device__ __forceinline__ long long lane_of(long long v, int lane) {
+    return (long long)(((uint64_t)(unsigned)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32) |
+                       (unsigned)__builtin_amdgcn_readlane((int)v, lane));
+}
+
 __device__ __forceinline__ Units units_of(const KvRows &r, int G, int block_rows, long long &all) {
     const int lane = threadIdx.x & 63;
     Units u{0, 0, 0, 0, 0, 0};
@@ -184,15 +189,18 @@ __device__ __forceinline__ Units units_of(const KvRows &r, int G, int block_rows
         u.mb = (u.rows + block_rows - 1) / block_rows;
         u.steps = (u.total + 31) >> 5;
     }
-    u.incl = (long long)u.steps * u.mb * r.Hkv;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const long long v = __shfl_up(u.incl, d);
-        if (lane >= d) u.incl += v;
-    }
-    all = __shfl(u.incl, 63);
+    // below 2^26 steps for each of 2^17 row blocks: sums of 24 low bits and of the rest fit an int
+    const long long mine = (long long)u.steps * u.mb * r.Hkv;
+    const int lo = wave_incl_scan((int)(mine & 0xFFFFFF)), hi = wave_incl_scan((int)(mine >> 24));
+    u.incl = ((long long)hi << 24) + lo;
+    all = lane_of(u.incl, 63);
     return u;
 }
+
+// row / G for a row of a sequence (row / G < 64, G <= 8192): the quotient of the
+// half next to it lies 2^-14 at least from a whole number, and its error is
+// below 2^-16.
+__device__ __forceinline__ int token_of(int row, float inv_g) { return (int)(((float)row + 0.5f) * inv_g); }
 
 // Quotient of non-negative numbers, short where both are.
 __device__ __forceinline__ long long quotient(long long a, long long b) {
@@ -340,13 +348,14 @@ __global__ __launch_bounds__(kThreads, groups(MT, D)) void attend_kernel(KvAtten
     // the sign is the queries'; above 0, so that hidden rows' -inf stays what it is
     const float sl = fmaxf(fabsf(a.scale) * 1.44269504088896341f, 1e-30f);
     const unsigned flip = a.scale < 0.f ? 0x8000u : 0u;
+    const float inv_g = 1.f / (float)a.G;
 
     while (x < xe) {
         const int s = __ffsll((unsigned long long)__ballot(un.incl > x)) - 1;
         const int len = __builtin_amdgcn_readlane(un.len, s), total = __builtin_amdgcn_readlane(un.total, s);
         const int steps = __builtin_amdgcn_readlane(un.steps, s), rows = __builtin_amdgcn_readlane(un.rows, s);
         const int mbs = __builtin_amdgcn_readlane(un.mb, s);
-        const long long end_s = __shfl(un.incl, s);
+        const long long end_s = lane_of(un.incl, s);
         const long long rel = x - (end_s - (long long)steps * mbs * r.Hkv);
         const int unit = __builtin_amdgcn_readfirstlane((int)quotient(rel, steps));
         const int st0 = __builtin_amdgcn_readfirstlane((int)(rel - (long long)unit * steps));
@@ -384,7 +393,7 @@ __global__ __launch_bounds__(kThreads, groups(MT, D)) void attend_kernel(KvAtten
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const int row = row0 + mt * 16 + c;
-            see[mt] = row < rows ? a.anc[t0 + row / a.G] : 0;
+            see[mt] = row < rows ? a.anc[t0 + token_of(row, inv_g)] : 0;
             settle(see[mt]);
         }
         __syncthreads();  // the last unit's exchange is over
@@ -407,7 +416,8 @@ __global__ __launch_bounds__(kThreads, groups(MT, D)) void attend_kernel(KvAtten
 #pragma unroll
             for (int p = 0; p < NS; ++p) z[p] = u32x4{0, 0, 0, 0};
             if (row < rows) {
-                const size_t at = (size_t)(t0 + row / a.G) * a.qs + (size_t)(h * a.G + row % a.G) * D + d;
+                const int tok = token_of(row, inv_g);
+                const size_t at = (size_t)(t0 + tok) * a.qs + (size_t)(h * a.G + row - tok * a.G) * D + d;
                 if (F32) {
                     const f32x4 *p = reinterpret_cast<const f32x4 *>((const float *)a.q + at);
                     const f32x4 p0 = p[0], p1 = p[1];
@@ -632,7 +642,8 @@ __global__ __launch_bounds__(kThreads, groups(MT, D)) void attend_kernel(KvAtten
                 const int row = row0 + mt * 16 + c;
                 if (row >= rows) continue;
                 const float inv = ll[mt] > 0.f ? 1.f / ll[mt] : 0.f;
-                const size_t at = ((size_t)(t0 + row / a.G) * a.Hq + h * a.G + row % a.G) * D;
+                const int tok = token_of(row, inv_g);
+                const size_t at = ((size_t)(t0 + tok) * a.Hq + h * a.G + row - tok * a.G) * D;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int d = (4 * g + i) * C;
@@ -683,10 +694,11 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(KvAttendArgs a) {
     const uint64_t in = __ballot(incl > (int)blockIdx.x);
     if (in == 0) return;
     const int s = __ffsll((unsigned long long)in) - 1;
-    const int steps = __shfl(un.steps, s), rows = __shfl(un.rows, s), mbs = __shfl(un.mb, s);
-    const int rel = (int)blockIdx.x - (__shfl(incl, s) - __shfl(cnt, s));
+    const int steps = __builtin_amdgcn_readlane(un.steps, s), rows = __builtin_amdgcn_readlane(un.rows, s);
+    const int mbs = __builtin_amdgcn_readlane(un.mb, s);
+    const int rel = (int)blockIdx.x - (__builtin_amdgcn_readlane(incl, s) - __builtin_amdgcn_readlane(cnt, s));
     const int h = rel / rows, row = rel - h * rows, unit = h * mbs + row / BR, rb = row % BR;
-    const long long u0 = __shfl(un.incl, s) - (long long)steps * mbs * r.Hkv + (long long)unit * steps, u1 = u0 + steps;
+    const long long u0 = lane_of(un.incl, s) - (long long)steps * mbs * r.Hkv + (long long)unit * steps, u1 = u0 + steps;
     const int w0 = __builtin_amdgcn_readfirstlane((int)quotient(u0, share)), w1 = __builtin_amdgcn_readfirstlane((int)quotient(u1 - 1, share));
     if (w0 == w1) return;
     const float *ml = a.part;
@@ -731,14 +743,10 @@ template <int MT, int D, bool F32>
 hipError_t attend_launch(const KvAttendArgs &a, hipStream_t s) {
     constexpr int lds = attend_lds_bytes<MT, D, F32>();
     static_assert(lds <= 160 * 1024 - 2 * kWaves * MT * 16 * 4, "one compute unit's LDS");
-    if (lds > 32768) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(attend_kernel<MT, D, F32>),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-        if (e != hipSuccess) return e;
-    }
-    hipLaunchKernelGGL((attend_kernel<MT, D, F32>), dim3(a.nwg), dim3(kThreads), lds, s, a);
-    const hipError_t e = hipGetLastError();
+    hipError_t e = allow_lds<attend_kernel<MT, D, F32>>(lds);
     if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((attend_kernel<MT, D, F32>), dim3(a.nwg), dim3(kThreads), lds, s, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
     hipLaunchKernelGGL((combine_kernel<D, F32>), dim3(a.T * a.Hq), dim3(kThreads), 0, s, a);
     return hipGetLastError();
 }

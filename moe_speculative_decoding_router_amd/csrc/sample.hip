@@ -1666,8 +1666,7 @@ hipError_t rows(const SampleArgs &a, Work w, const Layout &l, const float *u, in
     if (small) {
         const int lds = (a.V + kSmallRound - 1) / kSmallRound * kSmallRound * 4;
         Header *head = a.T <= l.rows ? w.head : nullptr;  // acceptance counts in it
-        hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(small_kernel<F32>),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, kSmall * 4);
+        hipError_t e = allow_lds<small_kernel<F32>>(kSmall * 4);
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL((small_kernel<F32>), dim3(a.T), dim3(kSmallThreads), lds, s, a, w.states, head, u, token, prob);
         if ((e = hipGetLastError()) != hipSuccess) return e;

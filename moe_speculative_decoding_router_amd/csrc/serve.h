@@ -6,9 +6,25 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "internal.h"
 
 namespace moe {
+
+// Allows a kernel `lds` bytes of dynamic LDS, once per device.  (Doing it
+// twice is harmless, so two threads need no order.)
+template <auto Kernel>
+hipError_t allow_lds(int lds) {
+    static std::atomic<uint64_t> done{0};  // a bit a device
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev) & 1) return hipSuccess;
+    e = hipFuncSetAttribute(reinterpret_cast<const void *>(Kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e == hipSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+    return e;
+}
 
 // The cache and the rows of one call, by value in the kernel arguments.
 struct KvRows {
