@@ -104,6 +104,33 @@ def test_append_bytes(D, dtype, page, Hkv):
         assert got.dtype == DT[dtype] and np.array_equal(got.double().cpu().numpy(), okv.quantise(x)[2])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_append_every_rounding(dtype):
+    """Each border between two codes, its neighbours on both sides and each
+    code's own value, of both signs, under scales from the least to the largest."""
+    D, page = 64, 16
+    ulp = 2.0 ** (-23 if dtype == "f32" else -7)
+    exps = [-100, -99, -64, -3, -1, 0, 1, 5, 60, 124, 125]
+    k = np.zeros((len(exps), 1, D))
+    for i, e in enumerate(exps):
+        at = [6.0] + [b for c in (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0)
+                      for b in (c - 2.0 ** np.floor(np.log2(c)) * ulp, c, c + 2.0 ** np.floor(np.log2(c)) * ulp)]
+        at += [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 1e-9, 2.0 ** -20, 0.1]
+        k[i, 0, :32] = np.array(at) * 2.0 ** e
+        k[i, 0, 32:] = -k[i, 0, :32]
+    kd = dev(k.astype(np.float32)).to(DT[dtype])
+    k = kd.double().cpu().numpy()
+    vd = kd.flip(-1).contiguous()
+    offsets, lens = [0, len(exps)], [1]
+    _, table, data = setup(9, D, 1, page, lens, offsets)
+    c = cache_of(dev(data), D, 1, page)
+    stored = m.kv4_append(c, kd, vd, dev(table), dev(np.array(lens, dtype=np.int32)), offsets, return_stored=True)
+    okv.append(data, k, k[..., ::-1], table, lens, offsets)
+    assert np.array_equal(c.data.cpu().numpy(), data)
+    assert np.array_equal(stored[0].double().cpu().numpy(), okv.quantise(k)[2])
+    assert np.array_equal(stored[1].double().cpu().numpy(), okv.quantise(k[..., ::-1])[2])
+
+
 def test_append_from_a_fused_projection():
     D, Hkv, page, offsets, lens = 128, 2, 32, [0, 9], [31]
     rng, table, data = setup(1, D, Hkv, page, lens, offsets)

@@ -152,6 +152,69 @@ def test_temperatures_and_edges_of_the_filters():
         assert ((tok >= 0) & (tok < V)).all()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [32767, 32768, 32769, 65541])
+def test_mixed_filters_large(V, dtype):
+    rng = np.random.default_rng(V)
+    T = 20
+    x, xd = logits_of(rng, T, V, dtype)
+    check(x, xd, rng.random(T), rng.choice([0.0, 0.3, 1.0, 2.5], T),
+          [0, 1, 5, 127, 128, 129, 400, 895, 897, 2047, 2049, 8191, 8193, V // 8 * 7, V - 1, V, 0, 0, 0, 0],
+          rng.choice([0.0, 0.3, 0.9, 0.99, 1.0], T), rng.choice([0.0, 0.02, 0.3], T))
+    check(x, xd, rng.random(T), min_p=rng.choice([0.0, 1e-4, 0.02, 0.3, 1.0], T))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [32000, 50021])
+def test_ties_masks_and_flat_rows_large(V, dtype):
+    """Rows where the filters' cut falls among equal values, or none of the row is below the others."""
+    rng = np.random.default_rng(V)
+    T = 14
+    x = rng.integers(-3, 4, size=(T, V)).astype(np.float64)
+    x[0] = 1.5
+    x[1] = -np.inf
+    x[2, rng.random(V) < 0.999] = -np.inf
+    x[3] = np.nan
+    x[4, 33333 % V] = np.inf
+    x[5, [7, V - 1]] = np.inf
+    x[6, ::3] = np.nan
+    x[7] = -3.3895313892515355e38              # the lowest finite value of both types
+    x[8, 1:] = -3.3895313892515355e38
+    x[9] = 1e-3 * rng.normal(size=V)           # nearly flat: every token is needed for a large mass
+    x[10] = -np.inf
+    x[10, -1] = 0.0
+    x[11, V // 2:] = -np.inf
+    xd = dev(x.astype(np.float32)).to(DT[dtype])
+    x = xd.double().cpu().numpy()
+    u = rng.random(T)
+    for kw in ({}, {"top_k": 3}, {"top_k": 1000}, {"top_k": 9000}, {"top_k": V - 5}, {"top_p": 0.5}, {"top_p": 0.99999},
+               {"min_p": 0.04}, {"top_k": 20000, "top_p": 0.7, "min_p": 0.01}, {"temperature": 0.0}):
+        check(x, xd, u, **{k: [v] * T for k, v in kw.items()})
+
+
+@pytest.mark.parametrize("T,V", [(2100, 600), (700, 200003), (2100, 33000)])
+def test_rows_do_not_depend_on_the_batch(T, V):
+    """More rows than one pass holds: each row as it is alone, and some against the oracle."""
+    g = torch.Generator(device=DEV).manual_seed(V)
+    xd = torch.randn((T, V), generator=g, device=DEV).mul_(3).to(torch.bfloat16)
+    u = torch.rand(T, generator=g, device=DEV)
+    topk = torch.randint(0, 400, (T,), generator=g, device=DEV, dtype=torch.int32)
+    topp = 0.2 + 0.8 * torch.rand(T, generator=g, device=DEV)
+    for kw in ({}, {"top_k": topk, "top_p": topp}):
+        tok, prob, full = m.sample_tokens(xd, u, return_probs=True, **kw)
+        assert torch.equal(prob, full.gather(1, tok.long()[:, None])[:, 0])
+        for a in (0, T // 2 - 3, 2046, T - 5):
+            if a + 5 > T:
+                continue
+            w = slice(a, a + 5)
+            part = m.sample_tokens(xd[w], u[w], return_probs=True, **{n: t[w] for n, t in kw.items()})
+            for p, q in zip(part, (tok, prob, full)):
+                assert torch.equal(p, q[w])
+            got = check(xd[w].double().cpu().numpy(), xd[w], u[w].cpu().numpy(),
+                        **{n: t[w].cpu().numpy() for n, t in kw.items()})
+            assert (got == tok[w].cpu().numpy()).all()
+
+
 def test_no_rows():
     tok, prob, probs = m.sample_tokens(torch.empty((0, 100), device=DEV), torch.empty(0, device=DEV), return_probs=True)
     assert tok.shape == (0,) and prob.shape == (0,) and probs.shape == (0, 100)
