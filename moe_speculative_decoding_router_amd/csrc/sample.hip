@@ -725,12 +725,16 @@ __device__ unsigned key_of_rank(unsigned key, int k, uint64_t *sh) {
 struct Bins {
     unsigned cnt[kBins];
     unsigned long long mass[kBins];
-    uint64_t wc[16], wm[16];
+    uint64_t wsum[16];
     Plan plan;
 };
 
-__device__ __forceinline__ void clear_bins(Bins &h, int nt) {
-    for (int b = threadIdx.x; b < kBins; b += nt) h.cnt[b] = 0, h.mass[b] = 0;
+__device__ __forceinline__ void clear_bins(Bins &h, int nt, bool by_k) {
+    for (int b = threadIdx.x; b < kBins; b += nt)
+        if (by_k)
+            h.cnt[b] = 0;
+        else
+            h.mass[b] = 0;
 }
 
 // Tokens below `cut` are left out, and so is the last bin; a threshold in them
@@ -740,8 +744,10 @@ __device__ __forceinline__ void count_token(Bins &h, const Kind &kind, float x, 
                                             double invt, const ExpTable &et) {
     const int b = bin_of(x, first, scale);
     if (b == kBins - 1 || key_of(x) < cut) return;
-    atomicAdd(&h.cnt[b], 1u);
-    if (!kind.by_k) atomicAdd(&h.mass[b], (unsigned long long)units(weight(et, x, first, invt)));
+    if (kind.by_k)
+        atomicAdd(&h.cnt[b], 1u);
+    else
+        atomicAdd(&h.mass[b], (unsigned long long)units(weight(et, x, first, invt)));
 }
 
 // The plan of a whole row's histogram, by 1024 threads; the block gets it in
@@ -749,33 +755,29 @@ __device__ __forceinline__ void count_token(Bins &h, const Kind &kind, float x, 
 // counted; `cap`: of the list.
 __device__ void plan_row(Bins &h, const Filter &f, const Kind &kind, uint64_t mass, unsigned cut, int cap) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const uint64_t n0 = h.cnt[2 * tid], n1 = h.cnt[2 * tid + 1];
-    const uint64_t m0 = kind.by_k ? 0 : h.mass[2 * tid], m1 = kind.by_k ? 0 : h.mass[2 * tid + 1];
-    uint64_t nb = (uint64_t)wave_incl_scan((int)(n0 + n1)) - n0 - n1;  // counts are below 2^18
-    uint64_t mb = kind.by_k ? 0 : wave_scan_u64(m0 + m1) - m0 - m1;
-    if (lane == 63) h.wc[wave] = nb + n0 + n1, h.wm[wave] = mb + m0 + m1;
+    const uint64_t v0 = kind.by_k ? h.cnt[2 * tid] : h.mass[2 * tid], v1 = kind.by_k ? h.cnt[2 * tid + 1] : h.mass[2 * tid + 1];
+    uint64_t run = wave_scan_u64(v0 + v1) - v0 - v1;
+    if (lane == 63) h.wsum[wave] = run + v0 + v1;
     if (tid == 0) h.plan = Plan{0, kBins - 1, 1, 1u, 0, mass};  // not among the counted
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-        if (i < wave) nb += h.wc[i], mb += h.wm[i];
+        if (i < wave) run += h.wsum[i];
     const uint64_t want = kind.by_k ? (uint64_t)kind.k : max((uint64_t)1, (uint64_t)ceil((double)f.topp * (double)mass));
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
-        const uint64_t c = y ? n1 : n0, v = y ? m1 : m0;
-        const uint64_t lo = kind.by_k ? nb : mb, hi = lo + (kind.by_k ? c : v);
-        if (lo < want && want <= hi) {
+        const uint64_t v = y ? v1 : v0;
+        if (run < want && want <= run + v) {
             Plan p;
             p.sure = kind.by_k ? 0 : 2 * tid + y;  // by_k: the sum of the first top_k comes from the list
             p.end = 2 * tid + y;
-            p.slow = (kind.by_k ? hi : c) > (uint64_t)cap;
+            p.slow = kind.by_k && run + v > (uint64_t)cap;
             p.cut = cut;
-            p.above_mass = mb;
+            p.above_mass = kind.by_k ? 0 : run;
             p.mass = mass;
             h.plan = p;
         }
-        nb += c;
-        mb += v;
+        run += v;
     }
     __syncthreads();
 }
@@ -815,7 +817,7 @@ __global__ __launch_bounds__(kHistThreads) void hist_kernel(SampleArgs a, Work w
     float x[E][Q];
     load_block<kHistThreads, F32>(a, t, hc * kHistChunks * kChunk, x);
     if (!kind.by_k) et.fill();
-    clear_bins(h, kHistThreads);
+    clear_bins(h, kHistThreads, kind.by_k);
     __syncthreads();
     const float first = of_key(kind.km), scale = bin_scale(f.invt);
     const uint64_t mass = kind.by_k ? 0 : (uint64_t)row_mass(et, w, row, f, kind.km);
@@ -827,26 +829,34 @@ __global__ __launch_bounds__(kHistThreads) void hist_kernel(SampleArgs a, Work w
             if (x[e][i] != -INFINITY) count_token(h, kind, x[e][i], cut, first, scale, f.invt, et);
     __syncthreads();
     if (w.H > 1) {
+        // bins past that of the least key counted are empty in all of them
+        const int bins = cut > 1u ? bin_of(of_key(cut), first, scale) + 1 : kBins;
         const size_t at = (size_t)row * w.H * kBins;
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
             const int b = y * kHistThreads + tid;
-            put(w.hcnt + at + hc * kBins + b, h.cnt[b]);
-            if (!kind.by_k) put(w.hmass + at + hc * kBins + b, (uint64_t)h.mass[b]);
+            if (b >= bins) continue;
+            if (kind.by_k)
+                put(w.hcnt + at + hc * kBins + b, h.cnt[b]);
+            else
+                put(w.hmass + at + hc * kBins + b, (uint64_t)h.mass[b]);
         }
         if (!last_of(&w.head[row].hist_done, w.H, &sh)) return;
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
             const int b = y * kHistThreads + tid;
-            unsigned n = 0;
-            uint64_t m = 0;
-#pragma unroll 4
-            for (int i = 0; i < w.H; ++i) {
-                n += get(w.hcnt + at + i * kBins + b);
-                if (!kind.by_k) m += get(w.hmass + at + i * kBins + b);
+            if (b >= bins) continue;
+            if (kind.by_k) {
+                unsigned n = 0;
+#pragma unroll 8
+                for (int i = 0; i < w.H; ++i) n += get(w.hcnt + at + i * kBins + b);
+                h.cnt[b] = n;
+            } else {
+                uint64_t m = 0;
+#pragma unroll 8
+                for (int i = 0; i < w.H; ++i) m += get(w.hmass + at + i * kBins + b);
+                h.mass[b] = m;
             }
-            h.cnt[b] = n;
-            h.mass[b] = m;
         }
         __syncthreads();
     }
