@@ -328,6 +328,13 @@ constexpr int attend_lds_bytes() {
 // float32 type's three-term operands beside them, have to fit the registers.
 constexpr int max_mt(int D, bool f32) { return D == 64 ? 4 : D == 128 ? (f32 ? 2 : 4) : 1; }
 
+// Whether the queries' operand terms stay in registers beside the accumulators
+// over all steps of a unit, or come from LDS again in every step, one k step
+// ahead of their products.
+constexpr int kAhead = 2;
+template <int MT, int D, bool F32>
+constexpr bool kQueriesStay = D == 256 || MT * (D / 8 * (F32 ? 3 : 1) + D / 4) <= 128;
+
 template <int MT, int D, bool F32>
 __global__ __launch_bounds__(kThreads, groups(MT, D)) void attend_kernel(KvAttendArgs a) {
     constexpr int NS = F32 ? 3 : 1;  // bf16 terms of q and of the probabilities
@@ -456,6 +463,18 @@ __global__ __launch_bounds__(kThreads, groups(MT, D)) void attend_kernel(KvAtten
             for (int i = 0; i < C; ++i) o[mt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
         lds_barrier();  // the queries are there; the loads go on
+        constexpr bool kStay = kQueriesStay<MT, D, F32>;
+        auto query = [&](int mt, int y, int ks) {
+            return *reinterpret_cast<const bf16x8 *>(lq + ((size_t)((mt * NS + y) * KS + ks) * 64 + lane) * 8);
+        };
+        // term i of a step, in the order of the products: the smaller terms first
+        constexpr int N = MT * NS * KS, NQ = kStay ? N : kAhead;
+        auto term = [&](int i) { return query(i / NS % MT, NS - 1 - i % NS, i / (NS * MT)); };
+        bf16x8 q[NQ];
+        if constexpr (kStay) {
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) q[i] = term(i);
+        }
 
         int get = 0;
         for (int st = st0 + wave; st < se; st += kWaves) {
@@ -468,6 +487,10 @@ __global__ __launch_bounds__(kThreads, groups(MT, D)) void attend_kernel(KvAtten
             }
             next += kWaves;
             put = put + 1 == kStages ? 0 : put + 1;
+            if constexpr (!kStay) {
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) q[i] = term(i);
+            }
             Frag<D> f;
             read_frag<D>(f, ring_at + get * 2 * Tile<D>::kBytes);
             get = get + 1 == kStages ? 0 : get + 1;
@@ -484,10 +507,15 @@ __global__ __launch_bounds__(kThreads, groups(MT, D)) void attend_kernel(KvAtten
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int y = 0; y < NS; ++y) {
-                        const bf16x8 q = *reinterpret_cast<const bf16x8 *>(
-                            lq + ((size_t)((mt * NS + NS - 1 - y) * KS + ks) * 64 + lane) * 8);
-                        sc[mt][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[0], q, sc[mt][0], 0, 0, 0);
-                        sc[mt][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[1], q, sc[mt][1], 0, 0, 0);
+                        const int i = (ks * MT + mt) * NS + y;
+                        bf16x8 &qf = q[i % NQ];
+                        sc[mt][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[0], qf, sc[mt][0], 0, 0, 0);
+                        sc[mt][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[1], qf, sc[mt][1], 0, 0, 0);
+                        if constexpr (!kStay)
+                            if (i + NQ < N) {
+                                qf = term(i + NQ);
+                                __builtin_amdgcn_sched_barrier(6);  // only other ALU work moves across
+                            }
                     }
             }
             const unsigned ok = (pool >> (2 * (kStages - 1))) & 3u;
@@ -709,22 +737,35 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(KvAttendArgs a) {
     const float *ml = a.part;
     const float *po = a.part + (size_t)a.nwg * 2 * BR * 2 + lane * E;
     auto at = [&](int w) { return ((size_t)w * 2 + (w == w0 ? 1 : 0)) * BR + rb; };
-    float m = kNone;
-    for (int w = w0 + lane; w <= w1; w += 64) m = fmaxf(m, ml[at(w) * 2]);
+    auto stats = [&](int w) { return w <= w1 ? *reinterpret_cast<const f32x2 *>(ml + at(w) * 2) : f32x2{kNone, 0.f}; };
+    f32x2 ms = stats(w0 + lane);
+    float m = ms[0];
+    for (int w = w0 + 64 + lane; w <= w1; w += 64) m = fmaxf(m, ml[at(w) * 2]);
     m = wave_max(m);
     float l = 0.f, o[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) o[i] = 0.f;
     for (int b = w0; b <= w1; b += 64) {
-        const int w = b + lane;
-        const float k = w <= w1 ? __builtin_amdgcn_exp2f(ml[at(w) * 2] - m) : 0.f;
-        if (w <= w1) l += k * ml[at(w) * 2 + 1];
+        if (b > w0) ms = stats(b + lane);
+        const float k = __builtin_amdgcn_exp2f(ms[0] - m);
+        l += k * ms[1];
         const int n = min(64, w1 - b + 1);
-        for (int i = wave; i < n; i += kWaves) {
-            const float ki = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(k), i));
-            const float *p = po + at(b + i) * D;
+        constexpr int kTogether = 8;  // loads under way: their latency is what this kernel takes
+        for (int i0 = wave; i0 < n; i0 += kTogether * kWaves) {
+            float p[kTogether][E];
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] += ki * p[e];
+            for (int y = 0; y < kTogether; ++y) {
+                const float *from = po + at(b + min(i0 + y * kWaves, n - 1)) * D;
+#pragma unroll
+                for (int e = 0; e < E; ++e) p[y][e] = from[e];
+            }
+#pragma unroll
+            for (int y = 0; y < kTogether; ++y) {
+                const int i = i0 + y * kWaves;
+                const float ki = i < n ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(k), i & 63)) : 0.f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] += ki * p[y][e];
+            }
         }
     }
     l = wave_sum(l);
