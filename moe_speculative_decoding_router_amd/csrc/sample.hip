@@ -37,6 +37,7 @@ constexpr int kBins = 2048;              // the last holds all that lies beyond
 constexpr double kBinsPerNat = 64.0;
 constexpr int kGroups = kChunk / 256;
 constexpr int kList = 8192;              // tokens in the bins of the thresholds
+constexpr int kBatchChunks = 16384;      // of the rows that are worked on together; bounds the workspace
 constexpr double kUnit = 35184372088832.0;         // 2^45
 constexpr double kUnitP = 2251799813685248.0;       // 2^51, of probabilities (their sum is 1)
 
@@ -297,12 +298,11 @@ struct Work {
     uint64_t *sum;     // [rows][C]
     Header *head;      // [rows]
     Plan *plan;        // [rows]
-    uint64_t *list;    // [rows][L] ~key, index
+    uint64_t *list;    // [rows][kList] ~key, index
     unsigned *hcnt;    // [rows][H][kBins]
     uint64_t *hmass;   // [rows][H][kBins]
     int row0, C;
     int H;             // histograms of a row
-    int L;             // entries of a list, min(kList, V) at least
 };
 
 template <typename T>
@@ -935,8 +935,8 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a, Work w) 
                 for (int e = 0; e < E; ++e)
 #pragma unroll
                     for (int i = 0; i < Q; ++i)
-                        if ((in >> (Q * e + i)) & 1 && at < w.L)
-                            w.list[(size_t)row * w.L + at++] =
+                        if ((in >> (Q * e + i)) & 1 && at < kList)
+                            w.list[(size_t)row * kList + at++] =
                                 entry_of(x[e][i], token_at<kThreads, F32>(c * kChunk, e) + i);
             }
         }
@@ -1153,7 +1153,7 @@ __global__ __launch_bounds__(kRowThreads) void resolve_kernel(SampleArgs a, Work
     const int row = blockIdx.x, t = w.row0 + row, tid = threadIdx.x, lane = tid & 63;
     // everything that does not wait for anything else first
     const uint64_t mine = tid < w.C ? w.sum[row * w.C + tid] : 0;
-    const uint64_t head = w.list[(size_t)row * w.L + min(tid, w.L - 1)];  // most lists end in it; not read past their length
+    const uint64_t head = w.list[(size_t)row * kList + tid];  // most lists end in it; not read past their length
     int n = w.head[row].listed;
     Plan p = w.plan[row];
     const float uu = u ? u[t] : 0.f;
@@ -1180,9 +1180,8 @@ __global__ __launch_bounds__(kRowThreads) void resolve_kernel(SampleArgs a, Work
     } else {
         bool slow = p.slow;
         if (planned && !slow) {
-            n = min(n, w.L);  // V <= L where that is below kList
             if (tid < n) s.l.list[tid] = head;
-            for (int i = kRowThreads + tid; i < n; i += kRowThreads) s.l.list[i] = w.list[(size_t)row * w.L + i];
+            for (int i = kRowThreads + tid; i < n; i += kRowThreads) s.l.list[i] = w.list[(size_t)row * kList + i];
             __syncthreads();
             slow = !resolve_list<kRowThreads>(s.l, n, f, kind, p, et, st,
                                               [&](int i, uint64_t m) { atomicAdd(&cs[i / kChunk], (unsigned long long)m); });
@@ -1464,7 +1463,7 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
         st.sum = (double)total;
     }
     if (tid == 0) {
-        if (head) head[t] = Header{0, 0, 0, 0};
+        head[t] = Header{0, 0, 0, 0};
         finish_row(a, et, st, states, t, st.token >= 0 ? tokens[st.token] : 0.f, token, prob);
     }
 }
@@ -1568,8 +1567,9 @@ __global__ __launch_bounds__(kRowThreads) void chain_kernel(SampleArgs a, Accept
     const RowState st = w.states[t];
     const double scale = st.sum > 0.0 ? kUnit / st.sum : 0.0;
     const float *q = c.q + (size_t)t * a.V;
+    // q is not below 0, so that the sum is p's at most, whatever q holds
     auto mass = [&](float x, int i) {
-        const double v = fmax(p_of(st, scale, x, i) - (rest ? (double)q[i] : 0.0), 0.0);
+        const double v = fmax(p_of(st, scale, x, i) - (rest ? fmax((double)q[i], 0.0) : 0.0), 0.0);
         return (uint64_t)__double_as_longlong(fma(v, kUnitP, 4503599627370496.0)) & 0xFFFFFFFFFFFFFull;
     };
     float x[E][Q];
@@ -1613,35 +1613,34 @@ __global__ __launch_bounds__(kRowThreads) void chain_kernel(SampleArgs a, Accept
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 struct Layout {
-    int C, H, L, rows;  // as in Work; rows of a batch
+    int C, H, rows;  // as in Work; rows of a batch
     size_t states, drawn, kmax, count, group, sum, head, plan, list, hcnt, hmass, total;
 };
 
 Layout layout(int T, int V) {
+    const bool small = V <= kSmall;  // one launch for all rows, and only the sums of acceptance
     Layout l{};
     l.C = (V + kChunk - 1) / kChunk;
     l.H = (l.C + kHistChunks - 1) / kHistChunks;
-    l.L = V < kList ? (V + 63) & ~63 : kList;
-    l.rows = l.C > 8 ? 16384 / l.C : 2048;
-    if (l.rows > T) l.rows = T;
+    l.rows = small || T < kBatchChunks / l.C ? T : kBatchChunks / l.C;
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
         off = align256(off + bytes);
         return at;
     };
-    const size_t rc = (size_t)l.rows * l.C, rh = (size_t)l.rows * l.H;
     l.states = take((size_t)T * sizeof(RowState));
     l.drawn = take((size_t)T * 4);
-    l.kmax = take(rc * 4);
-    l.count = take(rc * 4);
-    l.group = take(rc * kGroups * 4);
-    l.sum = take(rc * 8);
+    l.sum = take((size_t)l.rows * l.C * 8);
     l.head = take((size_t)l.rows * sizeof(Header));
-    l.plan = take((size_t)l.rows * sizeof(Plan));
-    l.list = take((size_t)l.rows * l.L * 8);
-    l.hcnt = take(rh * kBins * 4);
-    l.hmass = take(rh * kBins * 8);
+    const size_t n = small ? 0 : l.rows;
+    l.kmax = take(n * l.C * 4);
+    l.count = take(n * l.C * 4);
+    l.group = take(n * l.C * kGroups * 4);
+    l.plan = take(n * sizeof(Plan));
+    l.list = take(n * kList * 8);
+    l.hcnt = take(n * l.H * kBins * 4);
+    l.hmass = take(n * l.H * kBins * 8);
     l.total = off;
     return l;
 }
@@ -1663,7 +1662,6 @@ Work work_of(const SampleArgs &a, const Layout &l) {
     w.row0 = 0;
     w.C = l.C;
     w.H = l.H;
-    w.L = l.L;
     return w;
 }
 
@@ -1675,10 +1673,9 @@ hipError_t rows(const SampleArgs &a, Work w, const Layout &l, const float *u, in
     const bool small = a.V <= kSmall;
     if (small) {
         const int lds = (a.V + kSmallRound - 1) / kSmallRound * kSmallRound * 4;
-        Header *head = a.T <= l.rows ? w.head : nullptr;  // acceptance counts in it
         hipError_t e = allow_lds<small_kernel<F32>>(kSmall * 4);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL((small_kernel<F32>), dim3(a.T), dim3(kSmallThreads), lds, s, a, w.states, head, u, token, prob);
+        hipLaunchKernelGGL((small_kernel<F32>), dim3(a.T), dim3(kSmallThreads), lds, s, a, w.states, w.head, u, token, prob);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     for (; w.row0 < a.T; w.row0 += l.rows) {

@@ -312,6 +312,24 @@ def test_accept_equal_distributions_and_masked_rows():
     assert (out[count[0] - 1:] == -1).all() or count[0] < 3
 
 
+@pytest.mark.parametrize("V", [600, 50000])
+def test_accept_with_a_bad_drafter(V):
+    """Distributions that are none (negative, huge, NaN, inf) give tokens of the vocabulary all the same."""
+    rng = np.random.default_rng(8)
+    counts, offsets = [4, 5, 1, 6], [0, 4, 9, 10, 16]
+    x, xd = logits_of(rng, 16, V, "f32")
+    u, uf = dev(rng.random(16).astype(np.float32)), dev(rng.random(4).astype(np.float32))
+    tokens = dev(rng.integers(0, V, 16).astype(np.int32))
+    for bad in (-1.0, -3e38, 3e38, np.inf, -np.inf, np.nan):
+        q = torch.full((16, V), bad, device=DEV)
+        q[:, ::3] = 0.0
+        out, path, count = m.accept_drafts(xd, tokens, offsets, u, draft_probs=q, u_final=uf)
+        for s, n in enumerate(counts):
+            k, o = int(count[s]), offsets[s]
+            assert 1 <= k <= n and path[o:o + k].tolist() == list(range(k))
+            assert ((out[o:o + k] >= 0) & (out[o:o + k] < V)).all() and (out[o + k:o + n] == -1).all()
+
+
 def test_captured_and_two_streams():
     rng = np.random.default_rng(7)
     V, offsets = 40009, [0, 5, 10]
