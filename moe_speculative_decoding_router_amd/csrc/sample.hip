@@ -1503,29 +1503,27 @@ __global__ __launch_bounds__(kThreads) void probs_kernel(SampleArgs a, Work w, f
 // ---------------------------------------------------------------------------
 // Acceptance
 // ---------------------------------------------------------------------------
-// Drafts matched against the target's own draws: one thread a sequence.
+// Drafts matched against the target's own draws: thread t finds whether row t
+// is hit and enters itself with its parent, where the first row wins; then a
+// thread a sequence follows the hits.  (Searching the children of each row on
+// the way instead takes 4.5 us where this takes 3.1.)
 __global__ __launch_bounds__(64) void match_kernel(AcceptArgs c, const int32_t *drawn) {
-    __shared__ int32_t tok[kMaxTokens], drew[kMaxTokens], parent[kMaxTokens];
-    const int s = threadIdx.x;
+    __shared__ int32_t drew[kMaxTokens], hit[kMaxTokens];
+    const int s = threadIdx.x, T = c.off[c.nseq];
     static_assert(kMaxTokens == 64 && kMaxSegments <= 64, "a thread each");
-    if (s < c.off[c.nseq]) tok[s] = c.tokens[s], drew[s] = drawn[s], parent[s] = c.parent[s];
+    int tok = 0, parent = -1;
+    if (s < T) tok = c.tokens[s], drew[s] = drawn[s], parent = c.parent[s];
+    hit[s] = INT_MAX;
+    __syncthreads();
+    if (parent >= 0 && tok >= 0 && tok == drew[parent]) atomicMin(&hit[parent], s);
     __syncthreads();
     if (s >= c.nseq) return;
     const int r0 = c.off[s], n = c.off[s + 1] - r0;
-    int cur = 0, k = 0;
-    if (n) {
-        while (true) {
-            c.path[r0 + k] = cur;
-            const int y = drew[r0 + cur];
-            c.out[r0 + k] = y;
-            ++k;
-            int next = -1;
-            if (y >= 0)
-                for (int j = cur + 1; j < n && next < 0; ++j)
-                    if (parent[r0 + j] == cur && tok[r0 + j] == y) next = j;
-            if (next < 0) break;
-            cur = next;
-        }
+    int k = 0;
+    for (int cur = n ? r0 : INT_MAX; cur != INT_MAX; cur = hit[cur]) {
+        c.path[r0 + k] = cur - r0;
+        c.out[r0 + k] = drew[cur];
+        ++k;
     }
     c.count[s] = k;
     for (int j = k; j < n; ++j) c.path[r0 + j] = c.out[r0 + j] = -1;

@@ -243,7 +243,7 @@ int accept_drafts(const void *logits, int64_t stride, int32_t T, int32_t V, int3
             const int p = parent ? parent[c.off[s] + j] : j - 1;
             if (draft_probs && p != j - 1)
                 return fail(MOE_ENOTSUP, "draft_probs are for chains: row %d has parent %d", c.off[s] + j, p);
-            c.parent[c.off[s] + j] = (int8_t)p;
+            c.parent[c.off[s] + j] = (int8_t)(p < 0 ? -1 : c.off[s] + p);
         }
     moe::SampleArgs a{};
     if ((rc = sampling_args(logits, stride, T, V, dtype, f, ws, ws_bytes, &a)) != MOE_OK) return rc;

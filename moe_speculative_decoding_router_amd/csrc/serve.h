@@ -77,7 +77,7 @@ struct AcceptArgs {
     int32_t *out, *path, *count;
     int nseq;
     int off[kMaxSegments + 1];
-    int8_t parent[kMaxTokens];
+    int8_t parent[kMaxTokens];  // row of the call, -1 for roots
 };
 hipError_t launch_accept(const SampleArgs &a, const AcceptArgs &c, hipStream_t s);
 
