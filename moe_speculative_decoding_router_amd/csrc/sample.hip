@@ -1361,16 +1361,16 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
                 const unsigned b0 = s.b[2 * tid], b1 = s.b[2 * tid + 1];
                 int incl = wave_incl_scan((int)(b0 + b1));
                 if (lane == 63) sn[wave] = incl;
-                if (tid == 0) ranks[0] = 2047, ranks[1] = -1;
+                if (tid == 0) ranks[0] = 2047, ranks[1] = -1;  // none above, the end not found
                 __syncthreads();
                 for (int i = 0; i < wave; ++i) incl += sn[i];
                 const unsigned after = (unsigned)incl, mid = after - b1;
                 const float goal = kind.by_k ? (float)kind.k : (float)(want * (131072.0 / kUnit)), slack = kind.by_k ? 0.f : goal * 1e-3f + 64.f;
-                // the list begins after the last part that surely lies above, and ends with the first that surely holds it
-                if ((float)mid < goal - slack) atomicMax(&ranks[1], 2 * tid);
-                if ((float)after < goal - slack) atomicMax(&ranks[1], 2 * tid + 1);
-                if ((float)mid >= goal + slack) atomicMin(&ranks[0], 2 * tid);
-                if ((float)after >= goal + slack) atomicMin(&ranks[0], 2 * tid + 1);
+                // the list begins after the last part that surely lies above, and ends with the first that
+                // surely holds it; sums do not fall, so one thread finds each (atomics of all to one word take 6 us)
+                const float ahead = (float)(after - b0 - b1), lo = goal - slack, hi = goal + slack;
+                if (ahead < lo && lo <= (float)after) ranks[1] = 2 * tid - ((float)mid >= lo);
+                if (ahead < hi && hi <= (float)after) ranks[0] = 2 * tid + ((float)mid < hi);
                 __syncthreads();
                 const float width = (st.first - low) / 2047.9f;
                 const int end = ranks[0], begin = ranks[1];
