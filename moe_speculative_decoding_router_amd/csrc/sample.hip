@@ -979,27 +979,45 @@ typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
 // Bitonic sort of `size` (a power of two >= 64) list entries by NT threads,
 // ascending: key descending, index ascending.  Strides up to 64 stay inside
 // the 128 entries of a wave and need no barrier of the block.
-// Up to NT / 2 entries (all different) are put in the place that the number of
-// smaller ones gives, two or four threads counting for each; the rest keep ~0.
+// Up to NT entries (all different) are put in the place that the number of
+// smaller ones gives, two or four threads counting for each, or two for two
+// (250 entries: 2.5 us, where the sort takes 8); the rest keep ~0.
 template <int NT>
 __device__ void sort_list(uint64_t *list, int n, int size) {
-    if (n <= NT / 2) {
+    if (n <= NT) {
         const int log = n <= NT / 4 ? 2 : 1;
-        const int i = threadIdx.x >> log, part = threadIdx.x & ((1 << log) - 1), each = ((n + 7) >> 3) << (3 - log);  // 8 | size
-        uint64_t mine = 0;
-        int rank = 0;
-        if (i < n) {
-            mine = list[i];
+        const int i0 = threadIdx.x >> log, i1 = i0 + NT / 2, part = threadIdx.x & ((1 << log) - 1);
+        const int each = ((n + 7) >> 3) << (3 - log);  // 8 | size
+        uint64_t mine0 = 0, mine1 = 0;
+        int rank0 = 0, rank1 = 0;
+        if (i0 < n) mine0 = list[i0];
+        if (i1 < n) mine1 = list[i1];
+        const u64x2 *from = reinterpret_cast<const u64x2 *>(list + part * each), *end = from + each / 2;
+        if (n <= NT / 2) {
+            if (i0 < n)
 #pragma unroll 2
-            for (int j = part * each; j < (part + 1) * each; j += 2) {
-                const u64x2 v = *reinterpret_cast<const u64x2 *>(list + j);
-                rank += (v[0] < mine) + (v[1] < mine);
+                for (; from != end; ++from) {
+                    const u64x2 v = *from;
+                    rank0 += (v[0] < mine0) + (v[1] < mine0);
+                }
+        } else {
+#pragma unroll 2
+            for (; from != end; ++from) {
+                const u64x2 v = *from;
+                rank0 += (v[0] < mine0) + (v[1] < mine0);
+                rank1 += (v[0] < mine1) + (v[1] < mine1);
             }
         }
-        rank += __builtin_amdgcn_update_dpp(0, rank, 0xB1, 0xF, 0xF, false);  // quad_perm 1, 0, 3, 2
-        if (log == 2) rank += __builtin_amdgcn_update_dpp(0, rank, 0x4E, 0xF, 0xF, false);  // quad_perm 2, 3, 0, 1
+        auto others = [&](int rank) {
+            rank += __builtin_amdgcn_update_dpp(0, rank, 0xB1, 0xF, 0xF, false);  // quad_perm 1, 0, 3, 2
+            if (log == 2) rank += __builtin_amdgcn_update_dpp(0, rank, 0x4E, 0xF, 0xF, false);  // quad_perm 2, 3, 0, 1
+            return rank;
+        };
+        rank0 = others(rank0);
+        rank1 = others(rank1);
         __syncthreads();
-        if (i < n && part == 0) list[rank] = mine;
+        if (i0 < n && part == 0) list[rank0] = mine0;
+        if (i1 < n && part == 0 && log == 1) list[rank1] = mine1;
         __syncthreads();
         return;
     }
