@@ -169,12 +169,16 @@ __global__ __launch_bounds__(kThreads) void append_kernel(KvAppendArgs a) {
 // ---------------------------------------------------------------------------
 constexpr float kNone = -3.402823466e38f;  // running maximum before the first score
 constexpr float kSlack = 8.f;              // a score may pass the maximum by this (log2) before it moves
-constexpr int kMinShare = 8;               // steps of a workgroup at least
+constexpr int kMinShare = 4;               // steps of a workgroup at least: one a wave
+// What a second unit costs a workgroup (queries, first loads, the waves'
+// exchange) in its steps.
+constexpr int kSecondUnit = 8;
 
 // The flat list: what sequence `lane` adds to it.
 struct Units {
     int len, total, steps, rows, mb;  // rows before the call, all rows, steps, query rows, row blocks
-    long long incl;                   // running sum of steps over heads and row blocks
+    int span;                         // of a unit in the list: its steps, or those rounded up to whole shares
+    long long incl;                   // running sum of spans over heads and row blocks
 };
 
 __device__ __forceinline__ long long lane_of(long long v, int lane) {
@@ -182,9 +186,18 @@ __device__ __forceinline__ long long lane_of(long long v, int lane) {
                        (unsigned)__builtin_amdgcn_readlane((int)v, lane));
 }
 
-__device__ __forceinline__ Units units_of(const KvRows &r, int G, int block_rows, long long &all) {
+// Quotient of non-negative numbers, short where both are.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
+    return a / b;
+}
+
+// The list, its length, and the steps of a workgroup: as few as nwg workgroups
+// leave.  Where it costs less than kSecondUnit steps, shares are as much
+// longer as it takes for each to lie in one unit.
+__device__ __forceinline__ Units units_of(const KvRows &r, int G, int block_rows, int nwg, long long &share, long long &all) {
     const int lane = threadIdx.x & 63;
-    Units u{0, 0, 0, 0, 0, 0};
+    Units u{0, 0, 0, 0, 0, 0, 0};
     if (lane < r.nseq) {
         const int n = r.off[lane + 1] - r.off[lane];
         const int cap = r.max_pages << r.page_shift;
@@ -194,8 +207,33 @@ __device__ __forceinline__ Units units_of(const KvRows &r, int G, int block_rows
         u.mb = (u.rows + block_rows - 1) / block_rows;
         u.steps = (u.total + 31) >> 5;
     }
-    // below 2^26 steps for each of 2^17 row blocks: sums of 24 low bits and of the rest fit an int
-    const long long mine = (long long)u.steps * u.mb * r.Hkv;
+    // below 2^26 steps for each of 2^17 units: sums of 24 low bits and of the rest fit an int
+    const int units = u.mb * r.Hkv;
+    long long mine = (long long)u.steps * units;
+    all = ((long long)wave_sum_int((int)(mine >> 24)) << 24) + wave_sum_int((int)(mine & 0xFFFFFF));
+    const long long least = quotient(all + nwg - 1, nwg);
+    share = least > kMinShare ? least : kMinShare;
+    u.span = u.steps;
+    if (share < 1 << 26 && wave_sum_int(units) <= nwg) {
+        auto parts_of = [&](unsigned s) { return ((unsigned)u.steps + s - 1) / s; };
+        auto count = [&](unsigned parts) { return wave_sum_int((int)parts * units); };  // all / s + units at most
+        const unsigned most = (unsigned)share + kSecondUnit;
+        unsigned s = (unsigned)share, parts = parts_of(most);
+        if (count(parts) <= nwg) {
+            while (s < most) {
+                const unsigned p = parts_of(s);
+                const int sum = count(p);
+                if (sum <= nwg) {
+                    parts = p;
+                    break;
+                }
+                s = min(max(s + 1, (unsigned)quotient((long long)s * sum, nwg)), most);
+            }
+            u.span = (int)(parts * s);
+            share = s;
+        }
+    }
+    mine = (long long)u.span * units;
     const int lo = wave_incl_scan((int)(mine & 0xFFFFFF)), hi = wave_incl_scan((int)(mine >> 24));
     u.incl = ((long long)hi << 24) + lo;
     all = lane_of(u.incl, 63);
@@ -206,17 +244,6 @@ __device__ __forceinline__ Units units_of(const KvRows &r, int G, int block_rows
 // half next to it lies 2^-14 at least from a whole number, and its error is
 // below 2^-16.
 __device__ __forceinline__ int token_of(int row, float inv_g) { return (int)(((float)row + 0.5f) * inv_g); }
-
-// Quotient of non-negative numbers, short where both are.
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-    if (((a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
-    return a / b;
-}
-
-__device__ __forceinline__ long long share_of(long long all, int nwg) {
-    const long long s = quotient(all + nwg - 1, nwg);
-    return s > kMinShare ? s : kMinShare;
-}
 
 // Values of one step in a lane's registers.
 template <int D>
@@ -352,9 +379,8 @@ __global__ __launch_bounds__(kThreads, groups(MT, D)) void attend_kernel(KvAtten
     uint8_t *ring = lds + ring_offset<MT, D, F32>() + wave * (kStages * 2 * Tile<D>::kBytes);
     const unsigned ring_at = (unsigned)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)ring;
 
-    long long all;
-    const Units un = units_of(r, a.G, BR, all);
-    const long long share = share_of(all, a.nwg);
+    long long share, all;
+    const Units un = units_of(r, a.G, BR, a.nwg, share, all);
     const long long x0 = (long long)blockIdx.x * share;
     long long x = x0, xe = x0 + share < all ? x0 + share : all;
     // the sign is the queries'; above 0, so that hidden rows' -inf stays what it is
@@ -368,9 +394,10 @@ __global__ __launch_bounds__(kThreads, groups(MT, D)) void attend_kernel(KvAtten
         const int steps = __builtin_amdgcn_readlane(un.steps, s), rows = __builtin_amdgcn_readlane(un.rows, s);
         const int mbs = __builtin_amdgcn_readlane(un.mb, s);
         const long long end_s = lane_of(un.incl, s);
-        const long long rel = x - (end_s - (long long)steps * mbs * r.Hkv);
-        const int unit = __builtin_amdgcn_readfirstlane((int)quotient(rel, steps));
-        const int st0 = __builtin_amdgcn_readfirstlane((int)(rel - (long long)unit * steps));
+        const int span = __builtin_amdgcn_readlane(un.span, s);
+        const long long rel = x - (end_s - (long long)span * mbs * r.Hkv);
+        const int unit = __builtin_amdgcn_readfirstlane((int)quotient(rel, span));
+        const int st0 = __builtin_amdgcn_readfirstlane((int)(rel - (long long)unit * span));
         const int h = unit / mbs, mb = unit - h * mbs;
         const int n = __builtin_amdgcn_readfirstlane((int)(xe - x < steps - st0 ? xe - x : steps - st0));
         const int row0 = mb * BR, t0 = r.off[s], se = st0 + n;
@@ -705,7 +732,7 @@ __global__ __launch_bounds__(kThreads, groups(MT, D)) void attend_kernel(KvAtten
                 if (!whole && g == 0) ml[2 * (mt * 16 + c)] = mm[mt], ml[2 * (mt * 16 + c) + 1] = ll[mt];
             }
         }
-        x += n;
+        x += xe - x < span - st0 ? xe - x : span - st0;
     }
 }
 
@@ -719,9 +746,8 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(KvAttendArgs a) {
     __shared__ float sum[kWaves][D];
     const KvRows &r = a.r;
     const int BR = 16 * a.mt, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    long long all;
-    const Units un = units_of(r, a.G, BR, all);
-    const long long share = share_of(all, a.nwg);
+    long long share, all;
+    const Units un = units_of(r, a.G, BR, a.nwg, share, all);
     // the block's row: rows are counted over sequences and heads
     const int cnt = un.rows * r.Hkv, incl = wave_incl_scan(cnt);
     const uint64_t in = __ballot(incl > (int)blockIdx.x);
@@ -731,7 +757,8 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(KvAttendArgs a) {
     const int mbs = __builtin_amdgcn_readlane(un.mb, s);
     const int rel = (int)blockIdx.x - (__builtin_amdgcn_readlane(incl, s) - __builtin_amdgcn_readlane(cnt, s));
     const int h = rel / rows, row = rel - h * rows, unit = h * mbs + row / BR, rb = row % BR;
-    const long long u0 = lane_of(un.incl, s) - (long long)steps * mbs * r.Hkv + (long long)unit * steps, u1 = u0 + steps;
+    const int span = __builtin_amdgcn_readlane(un.span, s);
+    const long long u0 = lane_of(un.incl, s) - (long long)span * mbs * r.Hkv + (long long)unit * span, u1 = u0 + steps;
     const int w0 = __builtin_amdgcn_readfirstlane((int)quotient(u0, share)), w1 = __builtin_amdgcn_readfirstlane((int)quotient(u1 - 1, share));
     if (w0 == w1) return;
     const float *ml = a.part;
