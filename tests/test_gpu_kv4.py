@@ -208,6 +208,55 @@ def test_attend(D, dtype, Hkv, G, page, lens, counts, kind):
     assert torch.equal(out, again)
 
 
+def any_rows(rng, data, D):
+    """Every row of the pool holds codes and scales of some values."""
+    data[:] = rng.integers(0, 256, data.shape, dtype=np.uint8)
+    for at in (8 * D, 33 * D // 2):
+        data[..., at:at + D // 2] = rng.integers(122, 128, data.shape[:-1] + (D // 2,), dtype=np.uint8)
+
+
+@pytest.mark.parametrize("D,dtype,Hkv,G,lens,counts", [
+    (64, "bf16", 2, 8, [300, 77], [5, 6]), (64, "bf16", 1, 8, [40, 1000], [8, 7]), (64, "f32", 2, 16, [333], [7]),
+    (64, "f32", 1, 11, [0, 64], [4, 1]), (128, "bf16", 2, 8, [300, 77], [5, 6]), (128, "bf16", 1, 16, [40, 1000], [8, 7]),
+    (128, "f32", 2, 16, [333, 31], [7, 1]), (256, "bf16", 1, 16, [150], [6]),
+])
+def test_attend_wide_table(D, dtype, Hkv, G, lens, counts):
+    """Tables far wider than the sequences: row blocks of up to 64 rows."""
+    offsets, page = [0] + [int(x) for x in np.cumsum(counts)], 64
+    rng, table, data = setup(D + G, D, Hkv, page, lens, offsets)
+    table = np.pad(table, ((0, 0), (0, 20000 - table.shape[1])), constant_values=-1)
+    any_rows(rng, data, D)
+    T = offsets[-1]
+    parent = sum((tree(n, "binary") for n in counts), [])
+    kd, vd = rounded(rng, (T, Hkv, D), dtype)[1], rounded(rng, (T, Hkv, D), dtype)[1]
+    q, qd = rounded(rng, (T, Hkv * G, D), dtype)
+    c, td, ld = cache_of(dev(data), D, Hkv, page), dev(table), dev(np.array(lens, dtype=np.int32))
+    m.kv4_append(c, kd, vd, td, ld, offsets)
+    data = c.data.cpu().numpy()
+    out = m.kv4_attend(c, qd, td, ld, offsets, parent=parent)
+    check_attend(out, q, data, table, lens, offsets, parent, D ** -0.5, dtype)
+
+
+@pytest.mark.parametrize("D,dtype,Hkv,lens", [
+    (64, "bf16", 24, [7 + 3 * s for s in range(64)]), (128, "bf16", 12, [(37 * s) % 301 for s in range(64)]),
+    (128, "f32", 16, [900] + [5] * 63), (256, "bf16", 8, [(53 * s) % 211 for s in range(64)]),
+    (64, "f32", 3, [2500, 1, 0, 90, 1700]),
+])
+def test_attend_many_sequences(D, dtype, Hkv, lens):
+    """More units than workgroups, and units of very different lengths."""
+    offsets, page = list(range(len(lens) + 1)), 16
+    rng, table, data = setup(Hkv, D, Hkv, page, lens, offsets)
+    any_rows(rng, data, D)
+    T = len(lens)
+    kd, vd = rounded(rng, (T, Hkv, D), dtype)[1], rounded(rng, (T, Hkv, D), dtype)[1]
+    q, qd = rounded(rng, (T, 2 * Hkv, D), dtype)
+    c, td, ld = cache_of(dev(data), D, Hkv, page), dev(table), dev(np.array(lens, dtype=np.int32))
+    m.kv4_append(c, kd, vd, td, ld, offsets)
+    data = c.data.cpu().numpy()
+    out = m.kv4_attend(c, qd, td, ld, offsets)
+    check_attend(out, q, data, table, lens, offsets, None, D ** -0.5, dtype)
+
+
 @pytest.mark.parametrize("D,dtype,n", [(128, "bf16", 3), (64, "f32", 1), (256, "bf16", 2)])
 def test_attend_long_split(D, dtype, n):
     """One sequence over many workgroups; a few rows far apart hold most of the weight."""
