@@ -155,7 +155,8 @@ __global__ __launch_bounds__(kThreads) void append_kernel(KvAppendArgs a) {
 // 16 MT query rows), each unit its steps of 32 cache rows; every workgroup
 // takes an equal share of consecutive steps, whatever the lengths are, and
 // its waves take the steps of a unit in turn.  A unit that more than one
-// workgroup worked on is joined by combine_kernel.
+// workgroup worked on is joined by combine_kernel.  The lengths are the
+// device's, so every workgroup lays the list out for itself.
 //
 // A step is two tiles of 16 cache rows, which each wave loads straight into a
 // ring of its own in LDS, two steps ahead.  S^T = K Q^T leaves lane (g, c) =
@@ -166,12 +167,25 @@ __global__ __launch_bounds__(kThreads) void append_kernel(KvAppendArgs a) {
 // v_cvt_scalef32_pk_bf16_fp4, exactly (2 significant bits and a power of two).
 // The maximum is moved only when a score passes it by 2^8, so most steps need
 // no exchange between lanes.
+//
+// What bounds it: 60 query rows a head over 131086 rows of 8 heads of 128 (143
+// MB) take 63 us (2.3 TB/s, 510 TFLOP/s); a step is 64 matrix and about 390
+// vector instructions (codes to bf16, exponentials, sums), which keep the
+// vector unit busy 57% and the matrix unit 30% of the time.  Few query rows
+// over many cache rows are bound by memory: eight float32 rows a head over 600000
+// rows (660 MB) take 147 us, 4.5 TB/s, where the loads alone take 126.  Short
+// calls are latency: 200 rows take 6 us.  Matrix instructions on the codes
+// themselves would need q in 8-bit terms and the probabilities without the
+// rows' own scales, so the codes are converted.
 // ---------------------------------------------------------------------------
 constexpr float kNone = -3.402823466e38f;  // running maximum before the first score
 constexpr float kSlack = 8.f;              // a score may pass the maximum by this (log2) before it moves
-constexpr int kMinShare = 4;               // steps of a workgroup at least: one a wave
+// Steps of a workgroup at least: one a wave.  (One sequence of 4000 rows, 4
+// heads: 14.8 us, with 2 steps 16.9, with 8 15.3.)
+constexpr int kMinShare = 4;
 // What a second unit costs a workgroup (queries, first loads, the waves'
-// exchange) in its steps.
+// exchange) in its steps.  (Shares that lie in one unit: 4 x 5 tokens over 23000
+// rows 26.5 us, 31.3 without.)
 constexpr int kSecondUnit = 8;
 
 // The flat list: what sequence `lane` adds to it.
@@ -336,7 +350,9 @@ __device__ __forceinline__ void settle(T &v) {
 }
 
 // Workgroups of a compute unit, by the registers and the LDS they take, and
-// the steps of a wave's ring that this leaves room for.
+// the steps of a wave's ring that this leaves room for.  (Three with a ring of
+// two steps against two with three, D = 128: the 600000 rows above 146 us
+// against 154.  Twice the workgroups that run at once gain nothing anywhere.)
 constexpr int groups(int MT, int D) { return D == 256 ? 1 : MT > 1 ? 2 : D == 128 ? 3 : 4; }
 constexpr int stages(int MT, int D) { return D == 128 && MT == 1 ? 2 : 3; }
 
@@ -356,8 +372,9 @@ constexpr int attend_lds_bytes() {
 constexpr int max_mt(int D, bool f32) { return D == 64 ? 4 : D == 128 ? (f32 ? 2 : 4) : 1; }
 
 // Whether the queries' operand terms stay in registers beside the accumulators
-// over all steps of a unit, or come from LDS again in every step, one k step
-// ahead of their products.
+// over all steps of a unit, or come from LDS again in every step, two terms
+// ahead of their products.  (All from LDS: the 600000 rows above 148 us instead
+// of 146; all in registers with 4 row tiles: spills.)
 constexpr int kAhead = 2;
 template <int MT, int D, bool F32>
 constexpr bool kQueriesStay = D == 256 || MT * (D / 8 * (F32 ? 3 : 1) + D / 4) <= 128;
@@ -739,7 +756,9 @@ __global__ __launch_bounds__(kThreads, groups(MT, D)) void attend_kernel(KvAtten
 // Joins the parts of a unit, one workgroup a query row of it: lane i of every
 // wave takes the statistics of part i, the waves take the parts in turn.  A
 // workgroup's part of a unit that began before it is its slot 0, of one that
-// begins in it slot 1.
+// begins in it slot 1.  64 parts of each of 480 rows take 6.5 us: the latency
+// of the list, the statistics and two rounds of parts (9.9 us with one load at
+// a time).
 template <int D, bool F32>
 __global__ __launch_bounds__(kThreads) void combine_kernel(KvAttendArgs a) {
     constexpr int E = D / 64;  // elements of a lane
