@@ -57,8 +57,16 @@ struct RowState {
     double sum;       // weights kept, in units
 };
 
-// Value of a row's token; NaN becomes -inf, +inf the largest float, -0 +0.
-__device__ __forceinline__ float clean(float x) { return (x != x ? -INFINITY : fminf(x, 3.402823466e38f)) + 0.f; }
+// Value of a row's token; NaN becomes -inf, +inf the largest float, -0 +0.  The
+// sum makes -0 +0 and a signalling NaN quiet; the median of a NaN and two
+// numbers is the smaller number.  (Written out: the compiler folds a clamp by
+// comparisons on the ground that no NaN reaches it, and one that tells NaN
+// apart takes five instructions.)
+__device__ __forceinline__ float clean(float x) {
+    float y;
+    asm("v_med3_f32 %0, %1, %2, %3" : "=v"(y) : "v"(x + 0.f), "v"(-INFINITY), "s"(3.402823466e38f));
+    return y;
+}
 
 template <bool F32>
 __device__ __forceinline__ float value(const void *row, int i) {
@@ -370,15 +378,43 @@ __device__ __forceinline__ int token_at(int first, int e) {
 template <int NT, bool F32, int N = kChunk>
 constexpr int kRounds = N / kVec<F32> / NT;
 
+// All loads of a block are under way together, those of a row's last tokens
+// too: one at a time they take most of a kernel's time.
 template <int NT, bool F32, int E>
 __device__ __forceinline__ void load_block(const SampleArgs &a, int t, int first, float (&x)[E][kVec<F32>]) {
+    constexpr int Q = kVec<F32>;
     const void *row = row_of<F32>(a, t);
+    if (first + NT * Q * E <= a.V) {
+        if constexpr (F32) {
+            f32x4 v[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) load_tokens<F32>(row, token_at<NT, F32>(first, e), a.V, x[e]);
+            for (int e = 0; e < E; ++e) v[e] = *reinterpret_cast<const f32x4_any *>((const float *)row + token_at<NT, F32>(first, e));
 #pragma unroll
-    for (int e = 0; e < E; ++e)
+            for (int e = 0; e < E; ++e)
 #pragma unroll
-        for (int i = 0; i < kVec<F32>; ++i) x[e][i] = clean(x[e][i]);
+                for (int i = 0; i < Q; ++i) x[e][i] = clean(v[e][i]);
+        } else {
+            u32x4 v[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] = *reinterpret_cast<const u32x4_any *>((const uint16_t *)row + token_at<NT, F32>(first, e));
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+#pragma unroll
+                for (int i = 0; i < Q; ++i) x[e][i] = clean(__uint_as_float(i & 1 ? v[e][i >> 1] & 0xffff0000u : v[e][i >> 1] << 16));
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                const int at = min(token_at<NT, F32>(first, e) + i, a.V - 1);
+                x[e][i] = F32 ? ((const float *)row)[at] : bf16_to_f32(((const uint16_t *)row)[at]);
+            }
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+            for (int i = 0; i < Q; ++i) x[e][i] = token_at<NT, F32>(first, e) + i < a.V ? clean(x[e][i]) : -INFINITY;
+    }
 }
 
 __device__ __forceinline__ unsigned wave_max_u32(unsigned v) {
