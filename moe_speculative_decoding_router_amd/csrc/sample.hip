@@ -855,18 +855,19 @@ __global__ __launch_bounds__(kHistThreads) void hist_kernel(SampleArgs a, Work w
     const int hc = blockIdx.x, row = blockIdx.y, t = w.row0 + row, tid = threadIdx.x;
     const unsigned group = hc == 0 && tid < w.C * kGroups ? w.group[row * w.C * kGroups + tid] : 0;
     const Filter f = filter_of(a, t);
-    const Kind kind = kind_of(f, w, row, a.V);
-    if (!kind.by_k && !kind.by_p) return;  // the whole row's workgroups
     // a small top_k against the groups: no histogram.  At 7 / 8 of the groups
     // about 2 tokens a group lie above the cut.
-    if (kind.by_k && kind.k <= w.C * kGroups * 7 / 8 && kind.k <= kList / 4) {
+    const bool ranked = f.topk > 0 && f.topk < a.V && f.topk <= w.C * kGroups * 7 / 8 && f.topk <= kList / 4;
+    float x[E][Q];
+    if (!ranked) load_block<kHistThreads, F32>(a, t, hc * kHistChunks * kChunk, x);
+    const Kind kind = kind_of(f, w, row, a.V);
+    if (!kind.by_k && !kind.by_p) return;  // the whole row's workgroups
+    if (ranked) {
         if (hc) return;
         const unsigned cut = key_of_rank<kHistThreads>(group, kind.k, ranks);
         if (tid == 0) w.plan[row] = Plan{0, kBins - 1, 0, cut, 0, 0};
         return;
     }
-    float x[E][Q];
-    load_block<kHistThreads, F32>(a, t, hc * kHistChunks * kChunk, x);
     if (!kind.by_k) et.fill();
     clear_bins(h, kHistThreads, kind.by_k);
     __syncthreads();
@@ -928,14 +929,15 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a, Work w) 
     __shared__ uint64_t sums[kThreads / 64];
     __shared__ int sh;
     const int c = blockIdx.x, row = blockIdx.y, t = w.row0 + row, tid = threadIdx.x;
+    // all loads before the first wait: none needs another's result
+    Plan p = w.plan[row];
     const Filter f = filter_of(a, t);
-    const Kind kind = kind_of(f, w, row, a.V);
-    const bool planned = kind.by_k || kind.by_p;
-    Plan p{kBins, -1, 0, 1u, 0, 0};
-    if (planned) p = w.plan[row];
-    if (p.slow) return;
     float x[E][Q];
     load_block<kThreads, F32>(a, t, c * kChunk, x);
+    const Kind kind = kind_of(f, w, row, a.V);
+    const bool planned = kind.by_k || kind.by_p;
+    if (!planned) p = Plan{kBins, -1, 0, 1u, 0, 0};
+    if (p.slow) return;
     et.fill();
     if (tid == 0) sh = f.one ? INT_MAX : 0;
     __syncthreads();
