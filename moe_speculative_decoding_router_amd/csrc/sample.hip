@@ -547,7 +547,7 @@ __device__ __forceinline__ void finish_row(const SampleArgs &a, const ExpTable &
 // Without filters
 // ---------------------------------------------------------------------------
 // Each chunk's largest value and its sum relative to it.  256 rows of 131072
-// float32 logits (134 MB): 36 to 40 us, 3.5 TB/s, of which the exponentials
+// float32 logits (134 MB): 34 to 38 us, 3.7 TB/s, of which the exponentials
 // are about 20.
 template <bool F32>
 __global__ __launch_bounds__(kThreads) void part_kernel(SampleArgs a, Work w) {
@@ -591,7 +591,7 @@ __global__ __launch_bounds__(kThreads) void part_kernel(SampleArgs a, Work w) {
 // The chunks' sums are relative to their own largest values and joined in
 // float64 in chunk order; the draw is made inside its chunk in that chunk's
 // units.  256 rows: 7.5 us.  (Joining in every workgroup of probs_kernel
-// instead takes that from 48 to 71 us: the draw's registers halve its waves.)
+// instead takes that from 47 to 71 us: the draw's registers halve its waves.)
 template <bool F32>
 __global__ __launch_bounds__(kRowThreads) void join_kernel(SampleArgs a, Work w, const float *u, int32_t *token, float *prob) {
     __shared__ ExpTable et;
@@ -645,7 +645,7 @@ __global__ __launch_bounds__(kRowThreads) void join_kernel(SampleArgs a, Work w,
 // ---------------------------------------------------------------------------
 // Largest keys of the chunk and of its groups (16 lanes each), and for rows
 // with top_p alone the sum of its weights relative to its largest value.  64
-// rows of 150001 bf16 logits (19 MB): 8.6 us.
+// rows of 150001 bf16 logits (19 MB): 7.7 us.
 template <bool F32>
 __global__ __launch_bounds__(kThreads) void max_kernel(SampleArgs a, Work w) {
     constexpr int E = kRounds<kThreads, F32>, Q = kVec<F32>;
@@ -921,7 +921,7 @@ __device__ __forceinline__ unsigned entry_key(uint64_t e) { return ~(unsigned)(e
 __device__ __forceinline__ uint64_t entry_of(float x, int i) { return ((uint64_t)~key_of(x) << 32) | (unsigned)i; }
 
 // The list, and the sums of what is kept for sure.  Reads the logits again,
-// from the caches: 64 rows of 150001 bf16 in 10 to 12 us.
+// from the caches: 64 rows of 150001 bf16 in 9 to 11 us.
 template <bool F32>
 __global__ __launch_bounds__(kThreads) void gather_kernel(SampleArgs a, Work w) {
     constexpr int E = kRounds<kThreads, F32>, Q = kVec<F32>;
@@ -1551,7 +1551,7 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
 // The whole distribution of a row
 // ---------------------------------------------------------------------------
 // 256 rows of 131072 float32 logits (134 MB in, out of the caches in part, 134
-// MB out): 47 to 50 us, 5.5 TB/s: memory.
+// MB out): 45 to 48 us, 5.7 TB/s: memory.
 template <bool F32>
 __global__ __launch_bounds__(kThreads) void probs_kernel(SampleArgs a, Work w, float *probs) {
     constexpr int E = kRounds<kThreads, F32>, Q = kVec<F32>;
