@@ -240,10 +240,10 @@ def test_attend_wide_table(D, dtype, Hkv, G, lens, counts):
 @pytest.mark.parametrize("D,dtype,Hkv,lens", [
     (64, "bf16", 24, [7 + 3 * s for s in range(64)]), (128, "bf16", 12, [(37 * s) % 301 for s in range(64)]),
     (128, "f32", 16, [900] + [5] * 63), (256, "bf16", 8, [(53 * s) % 211 for s in range(64)]),
-    (64, "f32", 3, [2500, 1, 0, 90, 1700]),
+    (64, "f32", 3, [2500, 1, 0, 90, 1700]), (256, "bf16", 4, [1500 + (997 * s) % 1703 for s in range(32)]),
 ])
 def test_attend_many_sequences(D, dtype, Hkv, lens):
-    """More units than workgroups, and units of very different lengths."""
+    """More units than workgroups, units of very different lengths, and long ones that shares do not divide."""
     offsets, page = list(range(len(lens) + 1)), 16
     rng, table, data = setup(Hkv, D, Hkv, page, lens, offsets)
     any_rows(rng, data, D)
