@@ -26,6 +26,8 @@
 // time is the chain of dependent steps, each some latencies of memory and LDS
 // long, and for large batches the float64 exponentials.  float64 costs as much
 // as float32 here; a weight with its units takes about 25 instructions.
+#include <type_traits>
+
 #include "common.h"
 #include "serve.h"
 
@@ -35,7 +37,6 @@ namespace {
 constexpr int kThreads = 256;            // of the kernels with a workgroup a chunk
 constexpr int kRowThreads = 512;         // of those with a workgroup a row
 constexpr int kChunk = 4096;             // tokens
-constexpr int kRowWaves = kRowThreads / 64;
 constexpr int kMaxChunks = 64;           // of a row of 2^18 tokens: a lane each
 constexpr int kHistThreads = 1024;       // of hist_kernel, which takes kHistChunks chunks
 constexpr int kHistChunks = 4;
@@ -536,7 +537,7 @@ __device__ int find_in_chunk(const SampleArgs &a, int t, int c, uint64_t want, F
     return r;
 }
 
-__device__ __forceinline__ void finish_row(const SampleArgs &a, const ExpTable &et, const RowState &st, RowState *states, int t,
+__device__ __forceinline__ void finish_row(const ExpTable &et, const RowState &st, RowState *states, int t,
                                            float x, int32_t *token, float *prob) {
     states[t] = st;
     if (token) token[t] = st.token;
@@ -637,7 +638,7 @@ __global__ __launch_bounds__(kRowThreads) void join_kernel(SampleArgs a, Work w,
         if (f.one) st.key = km, st.last = st.token;
         x = value<F32>(row_of<F32>(a, t), st.token);
     }
-    if (threadIdx.x == 0) finish_row(a, et, st, w.states, t, x, token, prob);
+    if (threadIdx.x == 0) finish_row(et, st, w.states, t, x, token, prob);
 }
 
 // ---------------------------------------------------------------------------
@@ -1279,7 +1280,7 @@ __global__ __launch_bounds__(kRowThreads) void resolve_kernel(SampleArgs a, Work
         st.sum = (double)total;
     }
     if (st.token >= 0) x = value<F32>(r, st.token);
-    if (tid == 0) finish_row(a, et, st, w.states, t, x, token, prob);
+    if (tid == 0) finish_row(et, st, w.states, t, x, token, prob);
 }
 
 // ---------------------------------------------------------------------------
@@ -1319,33 +1320,46 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
     f32x4 *own = reinterpret_cast<f32x4 *>(tokens) + tid;  // round e at own[e * NT]
     float v = -INFINITY;  // this thread's largest
     int nv = 0;
-    {
-        constexpr int Q = kVec<F32>, B = kSmall / Q / NT;
-        float x[B][Q];
-#pragma unroll
-        for (int y = 0; y < B; ++y) {
-            const int i = Q * (y * NT + tid);
-            if (i < a.V) {
-                load_tokens<F32>(r, i, a.V, x[y]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < Q; ++e) x[y][e] = -INFINITY;
-            }
-        }
-#pragma unroll
-        for (int y = 0; y < B; ++y) {
-            const int i = Q * (y * NT + tid);
-            if (i < E * kSmallRound) {
-#pragma unroll
-                for (int e = 0; e < Q; e += 4)
-                    *reinterpret_cast<f32x4 *>(tokens + i + e) =
-                        f32x4{clean(x[y][e]), clean(x[y][e + 1]), clean(x[y][e + 2]), clean(x[y][e + 3])};
-            }
-        }
-    }
     const Filter f = filter_of(a, t);
     const float uu = u ? u[t] : 0.f;
-    et.fill();
+    constexpr int Q = kVec<F32>, B = kSmall / Q / NT;
+    if (a.V >= Q) {
+        // every load is whole and under way at once; the last one, moved into the row,
+        // writes some of its neighbour's tokens again
+        typedef typename std::conditional<F32, f32x4_any, u32x4_any>::type Raw;
+        constexpr int size = F32 ? 4 : 2;
+        typename std::conditional<F32, f32x4, u32x4>::type raw[B];
+#pragma unroll
+        for (int y = 0; y < B; ++y)
+            raw[y] = *reinterpret_cast<const Raw *>((const char *)r + size * min(Q * (y * NT + tid), a.V - Q));
+        et.fill();
+#pragma unroll
+        for (int y = 0; y < B; ++y) {
+            const int i = Q * (y * NT + tid);
+            float x[Q];
+#pragma unroll
+            for (int e = 0; e < Q; ++e) {
+                if constexpr (F32)
+                    x[e] = clean(raw[y][e]);
+                else
+                    x[e] = clean(__uint_as_float(e & 1 ? raw[y][e >> 1] & 0xffff0000u : raw[y][e >> 1] << 16));
+            }
+            if (i + Q <= a.V) {
+#pragma unroll
+                for (int e = 0; e < Q; e += 4)
+                    *reinterpret_cast<f32x4 *>(tokens + i + e) = f32x4{x[e], x[e + 1], x[e + 2], x[e + 3]};
+            } else if (i < E * kSmallRound) {
+#pragma unroll
+                for (int e = 0; e < Q; ++e) {
+                    if (i < a.V) tokens[a.V - Q + e] = x[e];
+                    if (i + e >= a.V) tokens[i + e] = -INFINITY;
+                }
+            }
+        }
+    } else {
+        et.fill();
+        for (int i = tid; i < kSmallRound; i += NT) tokens[i] = i < a.V ? value<F32>(r, i) : -INFINITY;
+    }
     __syncthreads();
 #pragma unroll 1
     for (int e = 0; e < E; ++e) {
@@ -1543,7 +1557,7 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
     }
     if (tid == 0) {
         head[t] = Header{0, 0, 0, 0};
-        finish_row(a, et, st, states, t, st.token >= 0 ? tokens[st.token] : 0.f, token, prob);
+        finish_row(et, st, states, t, st.token >= 0 ? tokens[st.token] : 0.f, token, prob);
     }
 }
 
