@@ -537,11 +537,12 @@ __device__ int find_in_chunk(const SampleArgs &a, int t, int c, uint64_t want, F
     return r;
 }
 
+// The probability is computed as probs_kernel does, to the same bits.
 __device__ __forceinline__ void finish_row(const ExpTable &et, const RowState &st, RowState *states, int t,
                                            float x, int32_t *token, float *prob) {
     states[t] = st;
     if (token) token[t] = st.token;
-    if (prob) prob[t] = st.token < 0 ? 0.f : (float)(kept_weight(et, st, x, st.token) * kUnit / st.sum);
+    if (prob) prob[t] = st.token < 0 ? 0.f : (float)(kept_weight(et, st, x, st.token) * (kUnit / st.sum));
 }
 
 // ---------------------------------------------------------------------------
