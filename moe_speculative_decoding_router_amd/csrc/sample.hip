@@ -29,6 +29,7 @@
 #include <type_traits>
 
 #include "common.h"
+#include "narrow.h"
 #include "serve.h"
 
 namespace moe {
@@ -1346,7 +1347,7 @@ constexpr int kSmall = 8 * kSmallRound;
 constexpr int kSmallList = 2048;
 
 union SmallShared {
-    unsigned b[2048];
+    unsigned b[kParts];
     ListShared<kSmallList> l;
     Histogram h;
 };
@@ -1481,10 +1482,10 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
                 before = block_before<NT>(mine, sn, n);
             };
             count();
-            if (narrow && n > kSmallList && low > -1e30f && st.first > low) {
-                const float part = 2047.9f / (st.first - low);
+            if (narrow && n > kSmallList && can_narrow(low, st.first)) {
+                const float part = parts_per_unit(low, st.first);
                 const float scale = (float)fmin(f.invt * 1.4426950408889634, 1e30);
-                for (int i = tid; i < 2048; i += NT) s.b[i] = 0;
+                for (int i = tid; i < kParts; i += NT) s.b[i] = 0;
                 __syncthreads();
                 if (v >= low)
 #pragma unroll 1
@@ -1493,7 +1494,7 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             if (x[i] >= low)
-                                atomicAdd(&s.b[(int)((st.first - x[i]) * part)],
+                                atomicAdd(&s.b[part_at(st.first, x[i], part)],
                                           kind.by_k ? 1u : (unsigned)(131072.f * __builtin_amdgcn_exp2f((x[i] - st.first) * scale) + 0.5f));
                     }
                 __syncthreads();
@@ -1501,7 +1502,7 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
                 const unsigned b0 = s.b[2 * tid], b1 = s.b[2 * tid + 1];
                 int incl = wave_incl_scan((int)(b0 + b1));
                 if (lane == 63) sn[wave] = incl;
-                if (tid == 0) ranks[0] = 2047, ranks[1] = -1;  // none above, the end not found
+                if (tid == 0) ranks[0] = kParts - 1, ranks[1] = -1;  // none above, the end not found
                 __syncthreads();
                 for (int i = 0; i < wave; ++i) incl += sn[i];
                 const unsigned after = (unsigned)incl, mid = after - b1;
@@ -1512,10 +1513,10 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
                 if (ahead < lo && lo <= (float)after) ranks[1] = 2 * tid - ((float)mid >= lo);
                 if (ahead < hi && hi <= (float)after) ranks[0] = 2 * tid + ((float)mid < hi);
                 __syncthreads();
-                const float width = (st.first - low) / 2047.9f;
+                const float width = (st.first - low) / (kParts - 0.1f);
                 const int end = ranks[0], begin = ranks[1];
                 // a little beyond the parts' edges, which are rounded differently
-                if (end < 2047) low = fmaxf(low, st.first - width * ((float)end + 1.01f));
+                if (end < kParts - 1) low = fmaxf(low, st.first - width * ((float)end + 1.01f));
                 if (!kind.by_k && begin >= 0) top = st.first - width * ((float)begin + 0.99f);
                 __syncthreads();
                 count();
