@@ -18,9 +18,11 @@
 //   gather_kernel   sums of the kept, a list of the tokens in those few bins
 //   resolve_kernel  a workgroup a row: sorts the list, fixes the threshold and
 //                   draws
-// A row whose list would be too long (flat or tied rows, large top-k with
-// distant tails) is resolved by a radix descent over the whole row instead.
-// Rows of up to 32768 tokens take one launch, small_kernel.
+// A row whose list would be too long is resolved by a radix descent over the
+// whole row instead: where the threshold lies among too many equal or close
+// values (a mask of one finite value too, if top_k counts more than the allowed
+// tokens), and for a top_k above the list.  Rows of up to 32768 tokens take one
+// launch, small_kernel.
 //
 // The logits are few bytes (64 rows of 150001 bf16: 19 MB, 4 us): what takes
 // time is the chain of dependent steps, each some latencies of memory and LDS
@@ -1083,12 +1085,14 @@ typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
 // Bitonic sort of `size` (a power of two >= 64) list entries by NT threads,
 // ascending: key descending, index ascending.  Strides up to 64 stay inside
 // the 128 entries of a wave and need no barrier of the block.
-// Up to NT entries (all different) are put in the place that the number of
+// Up to 512 entries (all different) are put in the place that the number of
 // smaller ones gives, two or four threads counting for each, or two for two
-// (250 entries: 2.5 us, where the sort takes 8); the rest keep ~0.
+// (250 entries: 2.5 us, where the sort takes 8; a call with 300 of them, 512
+// threads: 43.4 against 46.7, with 1000, 1024 threads: 32.6 against 23.6); the
+// rest keep ~0.
 template <int NT>
 __device__ void sort_list(uint64_t *list, int n, int size) {
-    if (n <= NT) {
+    if (n <= (NT < 512 ? NT : 512)) {
         const int log = n <= NT / 4 ? 2 : 1;
         const int i0 = threadIdx.x >> log, i1 = i0 + NT / 2, part = threadIdx.x & ((1 << log) - 1);
         const int each = ((n + 7) >> 3) << (3 - log);  // 8 | size
@@ -1443,14 +1447,27 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
             // tokens of at least `top` are kept, those of at least `low` and less than `top` listed
             Plan p{0, kBins - 1, 0, 1u, 0, 0};
             float low = -3.402823466e38f, top = INFINITY;
-            bool narrow = true;
             double want = (double)kind.k;
-            if (kind.by_k) {  // a thread's tokens are a group
-                if (kind.k <= NT * 7 / 8) {
-                    low = of_key(key_of_rank<NT>(mykey, kind.k, sums));
-                    narrow = false;
-                } else {  // the least of the groups' largest, which must have the first k above it
-                    low = of_key(~block_max_u32<NT>(~mykey, sk));
+            if (kind.by_k) {
+                // Longer lists than a thread an entry take longer to sort than a descent over
+                // one round of tokens (3000 tokens, top_k 1500: 29.3 us against 25.0).
+                if (kind.k > (E > 1 ? kSmallList : NT)) {
+                    low = INFINITY;
+                } else {
+                    // a thread's tokens are a group: the k-th of their largest, or for a large k the
+                    // least of them, which must have the first k above it
+                    unsigned cut = kind.k <= NT * 7 / 8 ? key_of_rank<NT>(mykey, kind.k, sums) : ~block_max_u32<NT>(~mykey, sk);
+                    if (cut <= 1u) {  // too few groups hold a token: from the row's least on
+                        float least = INFINITY;
+#pragma unroll 1
+                        for (int e = 0; e < E; ++e) {
+                            const f32x4 x = own[e * NT];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) least = fminf(least, x[i] == -INFINITY ? INFINITY : x[i]);
+                        }
+                        cut = ~block_max_u32<NT>(~key_of(least), sk);
+                    }
+                    low = of_key(cut);
                 }
             } else {
                 uint64_t m = 0;
@@ -1482,7 +1499,7 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
                 before = block_before<NT>(mine, sn, n);
             };
             count();
-            if (narrow && n > kSmallList && can_narrow(low, st.first)) {
+            if (n > kSmallList && can_narrow(low, st.first)) {
                 const float part = parts_per_unit(low, st.first);
                 const float scale = (float)fmin(f.invt * 1.4426950408889634, 1e30);
                 for (int i = tid; i < kParts; i += NT) s.b[i] = 0;

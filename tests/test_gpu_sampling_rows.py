@@ -34,3 +34,65 @@ def test_values_that_lie_next_to_each_other(V):
     check(x, xd, u, top_k=[V - 7] * T, top_p=[0.5] * T)
     check(x, xd, u, top_p=[0.9] * T)
     check(x, xd, u, top_p=[0.9] * T, temperature=[1e-37, 1e-43, 1e-45, 1e-30, 1e-38, 1e-37])
+
+
+def fastest(x, u, **kw):
+    """us of a call, the least of several runs of calls that follow each other."""
+    ws = torch.empty(m.lib().sample_workspace_bytes(*x.shape), dtype=torch.uint8, device=DEV)
+    best = float("inf")
+    for _ in range(6):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        for _ in range(10):
+            m.sample_tokens(x, u, workspace=ws, **kw)
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) * 100)
+    return best
+
+
+def descent(T, V, u, dtype=torch.float32, top_k=None):
+    """us of rows that only the descent over the whole row settles: equal values."""
+    k = torch.full((T,), V // 2, dtype=torch.int32, device=DEV)
+    return fastest(torch.zeros((T, V), dtype=dtype, device=DEV), u, top_k=k)
+
+
+def allowed(rng, T, V, n, together):
+    """Rows of which n tokens are allowed, next to each other or anywhere; the others are -inf."""
+    x = np.full((T, V), -np.inf)
+    for i in range(T):
+        at = 1 + int(rng.integers(0, V - n)) + np.arange(n) if together else rng.permutation(V)[:n]
+        x[i, at] = 2 * rng.normal(size=n)
+    return x.astype(np.float32)
+
+
+@pytest.mark.parametrize("V,n,together,k", [
+    (32000, 30, True, 50), (32000, 30, True, 30), (32000, 20, False, 50), (32000, 1500, False, 1000), (32000, 1500, False, 1500),
+    (32000, 3000, True, 800), (32000, 5000, False, 1000), (32000, 2000, True, 2047), (20000, 896, True, 896), (32768, 1, True, 2),
+    (32000, 31990, True, 896),
+])
+def test_few_allowed_tokens(V, n, together, k):
+    """Fewer of the search's groups hold a token than top_k counts, or more tokens lie above the groups' cut than a
+    list holds: the row is listed or narrowed, and far from the time of a descent over the whole row."""
+    rng = np.random.default_rng(n + k)
+    T = 6
+    x = allowed(rng, T, V, n, together)
+    xd, u = dev(x), rng.random(T)
+    check(x.astype(np.float64), xd, u, top_k=[k] * T)
+    check(x.astype(np.float64), xd, u, top_k=[k] * T, top_p=[0.9, 0.99, 0.5, 1.0, 0.999, 0.2], temperature=[0.7] * T)
+    ud = dev(u.astype(np.float32))
+    own = fastest(xd, ud, top_k=torch.full((T,), k, dtype=torch.int32, device=DEV))
+    all_ = descent(T, V, ud)
+    print(f"    {own:.1f} us, by descent {all_:.1f}")
+    assert own < 0.5 * all_
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V,k", [(200, 100), (1000, 300), (1500, 1000), (3000, 1000), (4093, 4000)])
+def test_top_k_beyond_the_groups(V, k, dtype):
+    """Short rows whose top_k is above the number of groups that hold a token."""
+    rng = np.random.default_rng(V)
+    T = 8
+    x, xd = base.logits_of(rng, T, V, dtype)
+    check(x, xd, rng.random(T), top_k=[k] * T)
+    check(x, xd, rng.random(T), top_k=[k] * T, top_p=rng.choice([0.3, 0.9, 0.99], T), min_p=rng.choice([0.0, 0.02], T))
