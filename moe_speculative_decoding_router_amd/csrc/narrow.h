@@ -1,5 +1,5 @@
 // Arithmetic of the narrowing in small_kernel (sample.hip): where among equal
-// parts of [low, first] a row's token falls.  constexpr, so that the same
+// parts of [low, first] a row's token falls, and what it weighs.  constexpr, so that the same
 // functions run in the kernels and in the host's tests.
 #pragma once
 
@@ -20,5 +20,19 @@ constexpr int part_at(float first, float x, float per) {
     const float d = (first - x) * per;
     return d < (float)(kParts - 1) ? (int)d : kParts - 1;
 }
+
+// Weights of a top-p narrowing, float32 numbers relative to the first, are
+// added as integers in units of 1 / kNarrowMass of the row's sum: a tail's
+// tokens hold units however far below the first they lie, and whole rows stay
+// below 2^31.
+constexpr double kNarrowMass = 2.13e9;
+constexpr unsigned narrow_mass(float unit, float w) { return (unsigned)(unit * w + 0.5f); }
+
+// What a sum of n of them may be off by.  Half a unit each; and of the sum
+// 3 * 2^-24 * 40 * ln 2 = 5.0e-6 for the exponents (three roundings, at most 40
+// bits: the least token counted weighs (1 - top_p) / 2V, 2^-40, of the sum),
+// 1.2e-7 for exp2 and 2.4e-7 for the products and the comparison's
+// conversions, 11500 units in all.
+constexpr float narrow_slack(int n) { return 14000.f + 0.5f * (float)n; }
 
 }  // namespace moe

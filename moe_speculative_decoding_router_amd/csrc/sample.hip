@@ -1444,7 +1444,7 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
     } else if (km) {
         bool summed = false;
         if (kind.by_k || kind.by_p) {
-            // tokens of at least `top` are kept, those of at least `low` and less than `top` listed
+            // tokens above `top` are kept, those from `low` to `top` listed
             Plan p{0, kBins - 1, 0, 1u, 0, 0};
             float low = -3.402823466e38f, top = INFINITY;
             double want = (double)kind.k;
@@ -1483,9 +1483,8 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
                 if (cut > 1u) low = of_key(cut);
             }
             // Narrowing, where too many are left: a histogram of 2048 equal parts of
-            // [low, first], by the count or by float32 weights in 2^-17 of the first's
-            // (whole rows fit 32 bits).  Those sums are good to 2^-12 or so; the part
-            // is widened by that, and the sum above the list taken again in units.
+            // [low, first], by the count or by float32 weights (narrow.h).  The list
+            // is widened by those sums' error, and the sum above it taken again in units.
             int n, before = 0;
             auto count = [&]() {  // of the list: this thread's place in it, and its length
                 int mine = 0;
@@ -1494,7 +1493,7 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
                     for (int e = 0; e < E; ++e) {
                         const f32x4 x = own[e * NT];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) mine += x[i] >= low && x[i] < top;
+                        for (int i = 0; i < 4; ++i) mine += x[i] >= low && x[i] <= top;
                     }
                 before = block_before<NT>(mine, sn, n);
             };
@@ -1502,6 +1501,8 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
             if (n > kSmallList && can_narrow(low, st.first)) {
                 const float part = parts_per_unit(low, st.first);
                 const float scale = (float)fmin(f.invt * 1.4426950408889634, 1e30);
+                const double per_unit = kind.by_k ? 1.0 : kNarrowMass / (double)p.mass;
+                const float unit = (float)(per_unit * kUnit);
                 for (int i = tid; i < kParts; i += NT) s.b[i] = 0;
                 __syncthreads();
                 if (v >= low)
@@ -1512,7 +1513,7 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
                         for (int i = 0; i < 4; ++i)
                             if (x[i] >= low)
                                 atomicAdd(&s.b[part_at(st.first, x[i], part)],
-                                          kind.by_k ? 1u : (unsigned)(131072.f * __builtin_amdgcn_exp2f((x[i] - st.first) * scale) + 0.5f));
+                                          kind.by_k ? 1u : narrow_mass(unit, __builtin_amdgcn_exp2f((x[i] - st.first) * scale)));
                     }
                 __syncthreads();
                 // parts from the first down, two a thread
@@ -1523,7 +1524,7 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
                 __syncthreads();
                 for (int i = 0; i < wave; ++i) incl += sn[i];
                 const unsigned after = (unsigned)incl, mid = after - b1;
-                const float goal = kind.by_k ? (float)kind.k : (float)(want * (131072.0 / kUnit)), slack = kind.by_k ? 0.f : goal * 1e-3f + 64.f;
+                const float goal = (float)(want * per_unit), slack = kind.by_k ? 0.f : narrow_slack(n);
                 // the list begins after the last part that surely lies above, and ends with the first that
                 // surely holds it; sums do not fall, so one thread finds each (atomics of all to one word take 6 us)
                 const float ahead = (float)(after - b0 - b1), lo = goal - slack, hi = goal + slack;
@@ -1532,7 +1533,8 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
                 __syncthreads();
                 const float width = (st.first - low) / (kParts - 0.1f);
                 const int end = ranks[0], begin = ranks[1];
-                // a little beyond the parts' edges, which are rounded differently
+                // a little beyond the parts' edges, which are rounded differently; a token on the rounded
+                // `top` itself goes to the list
                 if (end < kParts - 1) low = fmaxf(low, st.first - width * ((float)end + 1.01f));
                 if (!kind.by_k && begin >= 0) top = st.first - width * ((float)begin + 0.99f);
                 __syncthreads();
@@ -1546,14 +1548,14 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
 #pragma unroll 1
                 for (int e = 0; e < E; ++e) {
                     const f32x4 x = own[e * NT];
-                    const bool some = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= top;
+                    const bool some = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) > top;
                     if (!__any(some)) continue;
                     uint64_t m = 0, kept = 0;
                     if (some)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const double w = weight(et, x[i], st.first, f.invt);
-                            const uint64_t q = x[i] >= top ? units(w) : 0;
+                            const uint64_t q = x[i] > top ? units(w) : 0;
                             m += q;
                             kept += w >= st.minp ? q : 0;
                         }
@@ -1569,7 +1571,7 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
                     const f32x4 x = own[e * NT];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (x[i] >= low && x[i] < top) s.l.list[before++] = entry_of(x[i], 4 * (e * NT + tid) + i);
+                        if (x[i] >= low && x[i] <= top) s.l.list[before++] = entry_of(x[i], 4 * (e * NT + tid) + i);
                 }
             __syncthreads();
             // Ties, or a first k beyond the list; and a narrowing that the exact sums

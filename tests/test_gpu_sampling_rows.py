@@ -96,3 +96,20 @@ def test_top_k_beyond_the_groups(V, k, dtype):
     x, xd = base.logits_of(rng, T, V, dtype)
     check(x, xd, rng.random(T), top_k=[k] * T)
     check(x, xd, rng.random(T), top_k=[k] * T, top_p=rng.choice([0.3, 0.9, 0.99], T), min_p=rng.choice([0.0, 0.02], T))
+
+
+@pytest.mark.parametrize("V,top_p,temperature", [(32000, 0.99, 1.0), (32768, 0.995, 1.0), (32000, 0.999, 0.7), (20000, 0.999, 1.5),
+                                                 (32000, 0.9999, 1.0), (32768, 0.99, 1.1)])
+def test_long_tails(V, top_p, temperature):
+    """A threshold in the tail, where a token's weight is far below the first's but many share the mass: rows without
+    ties, so none of the 64 needs a descent."""
+    rng = np.random.default_rng(int(V * top_p))
+    T = 64
+    x, xd = base.logits_of(rng, T, V, "f32")
+    u, part = rng.random(T), slice(0, 12)
+    check(x[part], xd[part], u[part], top_p=[top_p] * 12, temperature=[temperature] * 12)
+    ud = dev(u.astype(np.float32))
+    own = fastest(xd, ud, top_p=torch.full((T,), top_p, device=DEV), temperature=torch.full((T,), temperature, device=DEV))
+    tied = fastest(torch.zeros((T, V), device=DEV), ud, top_p=torch.full((T,), top_p, device=DEV))
+    print(f"    {own:.1f} us, by descent {tied:.1f}")
+    assert own < 0.6 * tied
