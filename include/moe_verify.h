@@ -411,8 +411,12 @@ int kv4_attend(const moe_kv4_cache *cache, const moe_kv4_rows *rows, const void 
  * p_i = w_i / (sum of the kept).  A draw with a number u in [0, 1) takes the
  * lowest kept index whose running sum in index order exceeds u * sum; a row
  * without tokens gives -1.
- * Weights are summed as integers in units of 2^-45 of the first's weight, so
- * results do not depend on the order of summation. */
+ * Weights are summed as integers in units of 2^-45 of the first's weight (a
+ * token below 2^-46 of it is never drawn), so results do not depend on the
+ * order of summation.  Rows of V > 32768 take two sums from parts joined in
+ * float64 in a fixed order, off by at most V 2^-46 of the sum: the row's
+ * without filters, and the one that top_p is a share of where no top_k is
+ * given. */
 typedef struct {
     const float *temperature; /* [T] device, or NULL: 1 */
     const int32_t *top_k;     /* [T] device, or NULL: off */

@@ -6,6 +6,8 @@
 // values, the last kept index.  Weights w = exp(-(first - l) / temperature)
 // are computed in float64 and summed as integers in units of 2^-45: a sum
 // does not depend on its order, and 2^18 weights of at most 1 fit 63 bits.
+// (Two sums of long rows are joined from the chunks' in float64 instead: the
+// row's in join_kernel and in row_mass.)
 //
 // A row is cut into chunks of 4096 tokens, a workgroup each.  Without
 // filters two launches draw: part_kernel (each chunk's largest value and its
@@ -644,8 +646,10 @@ __global__ __launch_bounds__(kThreads) void part_kernel(SampleArgs a, Work w) {
 }
 
 // The chunks' sums are relative to their own largest values and joined in
-// float64 in chunk order; the draw is made inside its chunk in that chunk's
-// units.  256 rows: 7.5 us.  (Joining in every workgroup of probs_kernel
+// float64 in chunk order, in units of the row's first: off by V 2^-46 of the
+// row's sum at most, by what the units drop.  The draw is made inside its chunk
+// in those units too; a chunk whose tokens have none of them is passed over, as
+// it is with filters.  256 rows: 7.5 us.  (Joining in every workgroup of probs_kernel
 // instead takes that from 47 to 71 us: the draw's registers halve its waves.)
 template <bool F32>
 __global__ __launch_bounds__(kRowThreads) void join_kernel(SampleArgs a, Work w, const float *u, int32_t *token, float *prob) {
@@ -665,7 +669,8 @@ __global__ __launch_bounds__(kRowThreads) void join_kernel(SampleArgs a, Work w,
     if (km) {
         // rows that keep one token: only chunks with the largest value count
         const float top = of_key(kc);
-        const double scale = kc == 0 || (f.one && kc != km) ? 0.0 : f.one ? 1.0 : weight(et, top, st.first, f.invt);
+        const double wc = weight(et, top, st.first, f.invt);
+        const double scale = kc == 0 || (f.one ? kc != km : units(wc) == 0) ? 0.0 : f.one ? 1.0 : wc;
         const double part = (double)sc * scale;
         double incl = part;
 #pragma unroll
@@ -679,13 +684,12 @@ __global__ __launch_bounds__(kRowThreads) void join_kernel(SampleArgs a, Work w,
         const uint64_t some = __ballot(part > 0.0);
         // a number past the last step takes the last token with weight
         const int c = hit ? __ffsll((unsigned long long)hit) - 1 : 63 - __clzll((long long)some);
-        const double inside = fmin((want - __shfl(incl - part, c)) / __shfl(scale, c), 9.0e18);
-        const float topc = __shfl(top, c);
+        const double inside = want - __shfl(incl - part, c);
         st.token = find_in_chunk<kRowThreads, F32>(
             a, t, c, inside > 0.0 ? (uint64_t)inside : 0,
             [&](float v, int) {
-                const uint64_t m = units(weight(et, v, topc, f.invt));
-                return f.one ? (uint64_t)(v == topc) : m;
+                const uint64_t m = units(weight(et, v, st.first, f.invt));
+                return f.one ? (uint64_t)(v == st.first) : m;
             },
             sums, &found);
         st.sum = f.one ? kUnit : total;
@@ -885,7 +889,8 @@ __device__ void plan_row(Bins &h, const Filter &f, const Kind &kind, uint64_t ma
 }
 
 // The row's sum from its chunks' (relative to their own largest values), in
-// units of the first's weight.
+// units of the first's weight; above the sum of all units by V 2^-46 of it at
+// most, by what the units drop.
 __device__ __forceinline__ double row_mass(const ExpTable &et, const Work &w, int row, const Filter &f, unsigned km) {
     const int lane = threadIdx.x & 63;
     const unsigned kc = lane < w.C ? w.kmax[row * w.C + lane] : 0;

@@ -113,3 +113,32 @@ def test_long_tails(V, top_p, temperature):
     tied = fastest(torch.zeros((T, V), device=DEV), ud, top_p=torch.full((T,), top_p, device=DEV))
     print(f"    {own:.1f} us, by descent {tied:.1f}")
     assert own < 0.6 * tied
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [5003, 40009, 150001])
+def test_no_filter_and_filters_that_are_off(V, dtype):
+    """The same draws without filters as with ones that keep everything: tokens below 2^-46 of the first have no
+    units on either path, so u = 0 takes the lowest token that has some."""
+    rng = np.random.default_rng(V)
+    T = 8
+    x = rng.normal(size=(T, V))
+    x[0, :V // 2] = -200                        # whole chunks below
+    x[1, 1:] -= 60                              # all but one token
+    x[2, :5000] = -31.5                         # 2^-45.4 of 1 where the first is 0: some have units, some none
+    x[2, 5000:] = np.minimum(x[2, 5000:], 0)
+    x[2, 0], x[2, V - 1] = -33, 0
+    x[3] = np.where(np.arange(V) % 2, 3.0, -100)
+    x[4] -= 2e-2 * np.arange(V)[::-1]
+    xd = dev(x.astype(np.float32)).to(base.DT[dtype])
+    off = dict(top_k=torch.zeros(T, dtype=torch.int32, device=DEV), top_p=torch.ones(T, device=DEV),
+               min_p=torch.zeros(T, device=DEV))
+    for u in (0.0, 2.0 ** -149, 2.0 ** -60, 0.3, 1 - 2.0 ** -24):
+        ud = torch.full((T,), u, device=DEV)
+        tok, prob, probs = m.sample_tokens(xd, ud, return_probs=True)
+        for names in (["top_k"], ["top_p"], ["min_p"], list(off)):
+            t, p, f = m.sample_tokens(xd, ud, return_probs=True, **{k: off[k] for k in names})
+            assert torch.equal(t, tok), (u, names, t.tolist(), tok.tolist())
+            # float64 sums of the chunks against integers: V 2^-46 of the sum, and a rounding to float32 each
+            assert ((p - prob).abs() <= (2.0 ** -23 + V * 2.0 ** -46) * prob).all()
+            assert ((f - probs).abs() <= (2.0 ** -23 + V * 2.0 ** -46) * probs + 2.0 ** -149).all()
