@@ -459,6 +459,8 @@ int sample_tokens(const void *logits, int64_t stride, int32_t T, int32_t V, int3
  *          u[t] * q(x) < p(x); at the first that is not, the last token is
  *          drawn with u_final[s] from max(p - q, 0) (from p if that is zero
  *          everywhere), after the last draft from p.
+ *          Values of q below 0 count as 0; a draft whose q is NaN is not
+ *          accepted, elsewhere NaN counts as 0.
  *   u      [T] f32, u_final [nseq] f32 in [0, 1) (device; u_final only with
  *          draft_probs, else NULL)
  *   count  [nseq] i32 out: tokens that the sequence gains, accepted drafts

@@ -1721,7 +1721,8 @@ __global__ __launch_bounds__(kRowThreads) void chain_kernel(SampleArgs a, Accept
             const RowState st = w.states[t];
             if (x >= 0 && x < a.V && st.sum > 0.0) {
                 const double p = p_of(st, kUnit / st.sum, value<F32>(row_of<F32>(a, t), x), x);
-                stop = !((double)c.u[t] * (double)c.q[(size_t)t * a.V + x] < p);
+                const double qx = (double)c.q[(size_t)t * a.V + x];
+                stop = !((double)c.u[t] * (qx < 0.0 ? 0.0 : qx) < p);  // NaN stops
             }
         }
         const uint64_t first = __ballot(stop);  // the last row always stops

@@ -76,7 +76,9 @@ def accept_match(drawn, tokens, parent):
 
 def accept_chain(p, q, tokens, u, u_final):
     """One sequence: p [n, V] the target's distributions, q [n, V] the
-    drafter's, tokens [n], u [n].  Returns (gained tokens, path)."""
+    drafter's (values below 0 count as 0), tokens [n], u [n].  Returns (gained
+    tokens, path)."""
+    q = np.where(q < 0, 0.0, q)
     n = len(tokens)
     j = 0
     while j + 1 < n:
