@@ -318,7 +318,9 @@ int expand_drafts(const int32_t *parent, int32_t N, const float *P, const uint32
  * (one byte e), each element is an e2m1 code (0, .5, 1, 1.5, 2, 3, 4, 6 and
  * a sign in bit 3).  The scale of a block is the smallest power of two
  * 2^-100 .. 2^125 with max|x| <= 6 * 2^n, elements are rounded to nearest, ties to
- * the even code, and saturate at 6.
+ * the even code, and saturate at 6.  NaN is stored as 0, an infinity as the
+ * largest value (6 * 2^125, with the block's scale): the cache holds finite
+ * numbers only.
  *   data [num_pages][Hkv][page / 16] tiles of 17 D bytes (device, 16-byte
  *   aligned, kv4_cache_bytes bytes; needs no initialisation).  A tile holds
  *   16 rows i = 0..15 in matrix-core operand order:

@@ -85,6 +85,25 @@ __global__ __launch_bounds__(kThreads) void append_kernel(KvAppendArgs a) {
             x1[2 * i] = __uint_as_float(raw[2 + i] << 16), x1[2 * i + 1] = __uint_as_float(raw[2 + i] & 0xffff0000u);
         }
     }
+    // NaN counts as 0: e2m1 has none, and the conversion would make a large number of it
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) nan |= x0[i] != x0[i] || x1[i] != x1[i];
+    if (nan) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (!F32) {
+                const f32x4 &x = i < 2 ? x0 : x1;
+                const float lo = x[2 * (i & 1)], hi = x[2 * (i & 1) + 1];
+                raw[i] &= (lo == lo ? 0xffffu : 0u) | (hi == hi ? 0xffff0000u : 0u);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x0[i] = x0[i] == x0[i] ? x0[i] : 0.f;
+            x1[i] = x1[i] == x1[i] ? x1[i] : 0.f;
+        }
+    }
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(x0[i]), fabsf(x1[i])));

@@ -16,8 +16,9 @@ E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
 
 def quantise(x):
     """x [..., D] -> (codes uint8 [..., D], scale bytes uint8 [..., D / 32],
-    values float64 [..., D])."""
+    values float64 [..., D]).  NaN counts as 0."""
     x = np.asarray(x, dtype=np.float64)
+    x = np.where(np.isnan(x), 0.0, x)
     b = x.reshape(*x.shape[:-1], -1, 32)
     amax = np.abs(b).max(-1)
     e = np.full(amax.shape, -100)
