@@ -384,7 +384,8 @@ size_t kv4_attend_workspace_bytes(const moe_kv4_cache *cache, const moe_kv4_rows
  *   out[t, h] = sum_p softmax_p(scale * q[t, h] . K[p, h / (Hq / Hkv)]) V[p, ...]
  * over the positions p that t sees: all of its sequence's rows before this
  * call, itself, and its ancestors among the call's rows.  A token that sees
- * nothing (every page outside the pool) gets zeros.
+ * nothing (every page outside the pool) gets zeros.  A head's query that holds
+ * NaN gives NaN, and touches no other head's or token's result.
  *   q [T, Hq, D] in dtype MOE_F32 or MOE_BF16, tokens q_stride elements apart
  *         (16-byte aligned rows); out [T, Hq, D] in dtype, dense
  *   parent (host) [T], read during the call only: parent of each row inside

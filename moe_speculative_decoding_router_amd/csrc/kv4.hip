@@ -26,6 +26,10 @@ __device__ __forceinline__ bf16x8 dequant8(unsigned w, float s) {
     return o.v;
 }
 
+// float32 -> bf16 bits by the hardware's conversion: to nearest, ties to even,
+// and NaN stays NaN whatever its payload.
+__device__ __forceinline__ unsigned bf16_bits(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+
 // Bytes of a row's 17 D / 16 share: a tile holds 16 rows of K, its scales, V and its scales.
 template <int D>
 struct Tile {
@@ -501,7 +505,7 @@ __global__ __launch_bounds__(kThreads, groups(MT, D)) void attend_kernel(KvAtten
                         float v = e < 4 ? p0[e & 3] : p1[e & 3];
 #pragma unroll
                         for (int y = 0; y < NS; ++y) {
-                            const unsigned b = f32_to_bf16_rne(v);
+                            const unsigned b = bf16_bits(v);
                             v -= bf16_to_f32((uint16_t)b);
                             z[y][e >> 1] |= (b ^ flip) << (16 * (e & 1));
                         }
@@ -759,8 +763,8 @@ __global__ __launch_bounds__(kThreads, groups(MT, D)) void attend_kernel(KvAtten
 #pragma unroll
                         for (int y = 0; y < C; y += 4) {
                             u32x2 z;
-                            z[0] = f32_to_bf16_rne(o[mt][y][i] * inv) | ((unsigned)f32_to_bf16_rne(o[mt][y + 1][i] * inv) << 16);
-                            z[1] = f32_to_bf16_rne(o[mt][y + 2][i] * inv) | ((unsigned)f32_to_bf16_rne(o[mt][y + 3][i] * inv) << 16);
+                            z[0] = bf16_bits(o[mt][y][i] * inv) | (bf16_bits(o[mt][y + 1][i] * inv) << 16);
+                            z[1] = bf16_bits(o[mt][y + 2][i] * inv) | (bf16_bits(o[mt][y + 3][i] * inv) << 16);
                             *reinterpret_cast<u32x2 *>(p + y) = z;
                         }
                     }
@@ -846,7 +850,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(KvAttendArgs a) {
         if (F32)
             ((float *)a.out)[to + d] = v * inv;
         else
-            ((uint16_t *)a.out)[to + d] = f32_to_bf16_rne(v * inv);
+            ((uint16_t *)a.out)[to + d] = (uint16_t)bf16_bits(v * inv);
     }
 }
 

@@ -47,3 +47,38 @@ def test_append_nan_and_infinities(D, dtype):
         assert np.isfinite(want).all() and (want[np.isnan(x)] == 0).all()
         assert np.array_equal(got.double().cpu().numpy(), want)
     assert np.array_equal(c.data.cpu().numpy(), data)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens", [[40, 3], [3000, 700]])     # whole units, and units split over workgroups
+def test_attend_nan_and_infinite_queries(D, dtype, lens):
+    """A query that holds NaN, of whatever sign and payload, gives NaN; it and infinite ones touch no other row."""
+    Hkv, G, page, offsets = 2, 8, 16, [0, 3, 5]
+    rng, table, data = base.setup(D + lens[0], D, Hkv, page, lens, offsets)
+    base.any_rows(rng, data, D)
+    T, parent = offsets[-1], [-1, 0, 0, -1, 0]
+    kd, vd = base.rounded(rng, (T, Hkv, D), dtype)[1], base.rounded(rng, (T, Hkv, D), dtype)[1]
+    q, qd = base.rounded(rng, (T, Hkv * G, D), dtype)
+    c, td, ld = base.cache_of(dev(data), D, Hkv, page), dev(table), dev(np.array(lens, dtype=np.int32))
+    m.kv4_append(c, kd, vd, td, ld, offsets)
+    clean = m.kv4_attend(c, qd, td, ld, offsets, parent=parent)
+    base.check_attend(clean, q, c.data.cpu().numpy(), table, lens, offsets, parent, D ** -0.5, dtype)
+    bits = torch.int32 if dtype == "f32" else torch.int16
+    nans = [0x7FC00000, 0x7FFFFFFF, -1, 0x7F800001, 0x7FFF8000, -2 ** 15] if dtype == "f32" else [0x7FC0, 0x7FFF, -1, 0x7F81, -127]
+    none, odd = torch.zeros((T, Hkv * G), dtype=torch.bool), torch.zeros((T, Hkv * G), dtype=torch.bool)
+    for i, b in enumerate(nans):
+        t, h = i % T, (5 * i) % (Hkv * G)
+        qd.view(bits)[t, h, (7 * i) % D] = b
+        none[t, h] = odd[t, h] = True
+    qd.view(bits)[3, 7] = -1                             # memory of 0xff
+    none[3, 7] = odd[3, 7] = True
+    qd[4, 9, 5], qd[0, 13, 2] = float("inf"), -float("inf")
+    odd[4, 9] = odd[0, 13] = True
+    for scale in (None, -0.5):
+        want = clean if scale is None else m.kv4_attend(c, dev(q.astype(np.float32)).to(DT[dtype]), td, ld, offsets, parent=parent, scale=scale)
+        out = m.kv4_attend(c, qd, td, ld, offsets, parent=parent, scale=scale).cpu()
+        assert torch.isnan(out[none]).all(), [i for i, x in enumerate(out[none]) if not torch.isnan(x).all()]
+        # the running maximum moves for all rows of a block together, so the others may round differently
+        base.check_attend(out, q, c.data.cpu().numpy(), table, lens, offsets, parent, D ** -0.5 if scale is None else scale, dtype, ~odd)
+        assert torch.isfinite(want).all()
