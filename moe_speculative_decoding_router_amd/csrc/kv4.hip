@@ -423,8 +423,9 @@ __global__ __launch_bounds__(kThreads, groups(MT, D)) void attend_kernel(KvAtten
     const Units un = units_of(r, a.G, BR, a.nwg, share, all);
     const long long x0 = (long long)blockIdx.x * share;
     long long x = x0, xe = x0 + share < all ? x0 + share : all;
-    // the sign is the queries'; above 0, so that hidden rows' -inf stays what it is
-    const float sl = fmaxf(fabsf(a.scale) * 1.44269504088896341f, 1e-30f);
+    // the sign is the queries'; above 0, so that hidden rows' -inf stays what it is, and by no
+    // more than a subnormal number, which leaves all finite scores at 0
+    const float sl = fmaxf(fabsf(a.scale) * 1.44269504088896341f, 1.4e-45f);
     const unsigned flip = a.scale < 0.f ? 0x8000u : 0u;
     const float inv_g = 1.f / (float)a.G;
 

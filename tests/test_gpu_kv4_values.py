@@ -82,3 +82,19 @@ def test_attend_nan_and_infinite_queries(D, dtype, lens):
         # the running maximum moves for all rows of a block together, so the others may round differently
         base.check_attend(out, q, c.data.cpu().numpy(), table, lens, offsets, parent, D ** -0.5 if scale is None else scale, dtype, ~odd)
         assert torch.isfinite(want).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-33, -1e-33, 1.4e-45, 1e-38])
+def test_attend_scales_next_to_zero(scale, dtype):
+    """Scores are scale * q.k however small the scale and large the products are; 0 weighs all visible rows alike."""
+    D, Hkv, page, lens, offsets = 64, 1, 16, [45], [0, 3]
+    rng, table, data = base.setup(13, D, Hkv, page, lens, offsets)
+    base.fill(rng, data, table, lens, D, Hkv, 1e16)
+    kd, vd = base.rounded(rng, (3, Hkv, D), dtype, 1e16)[1], base.rounded(rng, (3, Hkv, D), dtype)[1]
+    q, qd = base.rounded(rng, (3, 4, D), dtype, 1e16)
+    c, td, ld = base.cache_of(dev(data), D, Hkv, page), dev(table), dev(np.array(lens, dtype=np.int32))
+    m.kv4_append(c, kd, vd, td, ld, offsets)
+    parent, scale = [-1, 0, 0], float(np.float32(scale))
+    out = m.kv4_attend(c, qd, td, ld, offsets, parent=parent, scale=scale)
+    base.check_attend(out, q, c.data.cpu().numpy(), table, lens, offsets, parent, scale, dtype)
