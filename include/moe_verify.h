@@ -369,7 +369,8 @@ size_t kv4_cache_bytes(int32_t num_pages, int32_t page, int32_t Hkv, int32_t D);
  *         len[s] + i (entries outside the sequence's rows are skipped).
  *   k_out, v_out [T, Hkv, D] in dtype (dense), or both NULL: the values that
  *         the codes stand for, for every row of the call; only without path.
- * Positions written twice in one call (a page listed twice) hold either row.
+ * Positions written twice in one call (a page listed twice) hold any mix of the
+ * two rows' codes and scales: finite numbers, but neither row for certain.
  * Limits: 1 <= T <= 2^20.  Errors: EINVAL, ENOTSUP (D, dtype). */
 int kv4_append(const moe_kv4_cache *cache, const moe_kv4_rows *rows, const void *k, const void *v,
                int64_t k_stride, int64_t v_stride, int32_t T, int32_t dtype, const int32_t *path,
