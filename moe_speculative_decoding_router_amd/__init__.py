@@ -786,7 +786,8 @@ def kv4_append(cache: KV4Cache, k, v, table, lengths, offsets, *, path=None, cou
     projection may keep their distance between tokens) into the cache.  The
     call's rows are grouped by sequence: offsets (host) [nseq + 1]; row j of
     sequence s goes to position lengths[s] + j, page table[s].  table [nseq,
-    max_pages] and lengths [nseq] are int32 device tensors.
+    max_pages] and lengths [nseq] are int32 device tensors.  NaN is stored as 0,
+    infinities as the largest value.
 
     path [T], count [nseq] (int32, device; accept_drafts' results): write
     only the accepted rows, row path[offsets[s] + i] to position lengths[s] +

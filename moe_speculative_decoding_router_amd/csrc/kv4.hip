@@ -191,13 +191,25 @@ __global__ __launch_bounds__(kThreads) void append_kernel(KvAppendArgs a) {
 // The maximum is moved only when a score passes it by 2^8, so most steps need
 // no exchange between lanes.
 //
+// For bf16 queries the probabilities are one bf16 term of the second product:
+// each is off by 2^-9 of itself at most, so a result by 2^-9 of sum p |v|, about
+// what rounding it to bf16 costs anyway (the sum l and the accumulators are
+// float32).  Against 64 bits the results are 0.0018 to 0.0023 of their norm off,
+// 0.0017 with a second term, which leaves the result's rounding alone but takes
+// 73.5 us instead of 62 for the long tree below and 27.2 instead of 25.7 for 4 x
+// 5 tokens.  float32 queries and their probabilities are three terms (24 bits).
+//
 // What bounds it: 60 query rows a head over 131086 rows of 8 heads of 128 (143
 // MB) take 63 us (2.3 TB/s, 510 TFLOP/s); a step is 64 matrix and about 390
 // vector instructions (codes to bf16, exponentials, sums), which keep the
 // vector unit busy 57% and the matrix unit 30% of the time.  Few query rows
 // over many cache rows are bound by memory: eight float32 rows a head over 600000
 // rows (660 MB) take 147 us, 4.5 TB/s, where the loads alone take 126.  Short
-// calls are latency: 200 rows take 6 us.  Matrix instructions on the codes
+// calls are latency: 200 rows take 6 us.  D = 256 has one wave a SIMD (its
+// accumulators and operands take 288 registers) and one row tile, so that 64
+// query rows a head read and convert every tile four times: 4 heads over 100000
+// rows (109 MB) take 30.2 us for one row a head, 32.9 for 16 and 74.3 for 64,
+// where 8 heads of 128 take 30.1, 31.4 and 53.6.  Matrix instructions on the codes
 // themselves would need q in 8-bit terms and the probabilities without the
 // rows' own scales, so the codes are converted.
 // ---------------------------------------------------------------------------
@@ -900,7 +912,10 @@ hipError_t launch_kv4_append(const KvAppendArgs &a, hipStream_t s) {
 // cache less often, small ones begin and end a unit sooner: where the tables
 // hold no more than 32 steps a workgroup, blocks of two tiles are faster (64
 // rows a head, D = 128, 4 sequences: of 2000 rows 25.0 us against 32.1, of 8000
-// 31.4 against 37.3; 40 rows a head: of 16000 rows 39.2 against 35.6).
+// 31.4 against 37.3; 40 rows a head: of 16000 rows 39.2 against 35.6).  The
+// lengths are the device's, so the rule goes by the tables' width: a table much
+// wider than its sequences takes the larger blocks (the 4 x 2000 rows in a table
+// of 131072: 24.5 against 20.4, calls on one cache).
 size_t kv4_attend_plan(KvAttendArgs &a, int n_cu) {
     int most = 1;
     for (int s = 0; s < a.r.nseq; ++s) most = max(most, (a.r.off[s + 1] - a.r.off[s]) * a.G);

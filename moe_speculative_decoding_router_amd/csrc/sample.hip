@@ -1348,7 +1348,9 @@ __global__ __launch_bounds__(kRowThreads) void resolve_kernel(SampleArgs a, Work
 // (loads 1.5, largest 2, the sum 6, list 4, order and draw 6) and 33 where the
 // row is flat (narrowing 7, the sum above the list 9 more); with the kernels
 // above, 33 and 39.  The float64 exponentials bound it, 100 cycles of a SIMD
-// for 64 of them.
+// for 64 of them.  A call of 30 allowed tokens among 32000 with top_k 50 takes 20
+// us, of 64 rows whose top_p 0.99 lies in a long tail 35; rows that go through
+// the descent take 95 (top_k) to 140 (top_p).
 // ---------------------------------------------------------------------------
 constexpr int kSmallThreads = 1024;
 constexpr int kSmallRound = 4 * kSmallThreads;  // tokens
@@ -1579,8 +1581,8 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(SampleArgs a, RowS
                         if (x[i] >= low && x[i] <= top) s.l.list[before++] = entry_of(x[i], 4 * (e * NT + tid) + i);
                 }
             __syncthreads();
-            // Ties, or a first k beyond the list; and a narrowing that the exact sums
-            // do not bear out.
+            // Too many equal or close values at the threshold, or a first k beyond the
+            // list; and a narrowing that the exact sums do not bear out.
             const uint64_t least = max((uint64_t)1, (uint64_t)ceil((double)f.topp * (double)p.mass));
             bool slow = n > kSmallList || (kind.by_k ? n < kind.k : p.above_mass >= least);
             if (!slow)
