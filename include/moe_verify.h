@@ -411,7 +411,8 @@ int kv4_attend(const moe_kv4_cache *cache, const moe_kv4_rows *rows, const void 
  *     the least number whose weights sum to >= top_p * (sum of the first
  *       top_k) (off when >= 1),
  *     the number with w_i >= min_p (off when <= 0);
- *   temperature <= 0 keeps the first only.
+ *   temperature <= 0 keeps the first only.  A temperature of NaN is 0, another
+ *   filter of NaN is off.
  * p_i = w_i / (sum of the kept).  A draw with a number u in [0, 1) takes the
  * lowest kept index whose running sum in index order exceeds u * sum; a row
  * without tokens gives -1.

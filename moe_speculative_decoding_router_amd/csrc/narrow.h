@@ -1,9 +1,20 @@
-// Arithmetic of the narrowing in small_kernel (sample.hip): where among equal
-// parts of [low, first] a row's token falls, and what it weighs.  constexpr, so that the same
-// functions run in the kernels and in the host's tests.
+// Arithmetic of the search for a row's threshold (sample.hip): the bins of
+// hist_kernel and gather_kernel, and the narrowing in small_kernel, where among
+// equal parts of [low, first] a row's token falls and what it weighs.
+// constexpr, so that the same functions run in the kernels and in the host's
+// tests.
 #pragma once
 
 namespace moe {
+
+// Bin of a token's distance from the first, in float32: all that is asked of
+// it is that it never falls while the value does.  The last bin holds all that
+// lies beyond: masks of the lowest value are an infinite distance away.
+constexpr int kBins = 2048;
+constexpr int bin_of(float x, float first, float scale) {
+    const float d = (first - x) * scale;
+    return (int)(d < (float)(kBins - 1) ? d : (float)(kBins - 1));
+}
 
 constexpr int kParts = 2048;
 
@@ -18,7 +29,7 @@ constexpr float parts_per_unit(float low, float first) { return (kParts - 0.1f) 
 // whatever lies outside or is no number.
 constexpr int part_at(float first, float x, float per) {
     const float d = (first - x) * per;
-    return d < (float)(kParts - 1) ? (int)d : kParts - 1;
+    return (int)(d < (float)(kParts - 1) ? d : (float)(kParts - 1));
 }
 
 // Weights of a top-p narrowing, float32 numbers relative to the first, are

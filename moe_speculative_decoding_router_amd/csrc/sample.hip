@@ -45,7 +45,6 @@ constexpr int kChunk = 4096;             // tokens
 constexpr int kMaxChunks = 64;           // of a row of 2^18 tokens: a lane each
 constexpr int kHistThreads = 1024;       // of hist_kernel, which takes kHistChunks chunks
 constexpr int kHistChunks = 4;
-constexpr int kBins = 2048;              // the last holds all that lies beyond
 constexpr double kBinsPerNat = 64.0;
 constexpr int kGroups = kChunk / 256;
 constexpr int kList = 8192;              // tokens in the bins of the thresholds
@@ -777,13 +776,7 @@ __device__ __forceinline__ Kind kind_of(const Filter &f, const Work &w, int row,
     return kind_from(f, wave_max_u32(km), wave_sum_int(n), V);
 }
 
-// Bin of a token's distance from the first, in float32: all that is asked of
-// it is that it never falls while the value does.
 __device__ __forceinline__ float bin_scale(double invt) { return (float)fmin(invt * kBinsPerNat, 1e30); }
-
-__device__ __forceinline__ int bin_of(float x, float first, float scale) {
-    return min((int)((first - x) * scale), kBins - 1);
-}
 
 // Which tokens can be left out of the search for a threshold.
 //   top_p: tokens of weight below (1 - top_p) / V of the row's sum hold less

@@ -58,6 +58,24 @@ static void parts() {
     }
 }
 
+// Bins of every distance and temperature, masks of the lowest value among them.
+static void bins() {
+    const float big = std::numeric_limits<float>::max();
+    for (float first : {big, 1e30f, 90.f, 1.f, 0.f, -7.f, -1e38f})
+        for (float scale : {1e30f, 6.4e7f, 64.f, 0.9f, 1e-30f, 0.f}) {
+            int last = 0;
+            std::vector<float> xs = {first, first - 1e-6f * std::fabs(first), first - 0.01f, first - 1.f, first - 31.9f, first - 33.f,
+                                     first - 1e9f, first - 1e30f, -3.3895313892515355e38f, -big};
+            std::sort(xs.begin(), xs.end(), [](float a, float b) { return a > b; });
+            for (float x : xs) {
+                if (!(x <= first)) continue;
+                const int bin = moe::bin_of(x, first, scale);
+                CHECK(bin >= last && bin < moe::kBins, "first %g x %g scale %g bin %d after %d", first, x, scale, bin, last);
+                last = bin;
+            }
+        }
+}
+
 // Running sums of a row's weights, largest first, in units of the narrowing:
 // off by less than the slack from the exact ones, for tails that hold most of
 // the row, rows of one value and thresholds next to 1.
@@ -91,6 +109,7 @@ static void sums() {
 
 int main() {
     parts();
+    bins();
     sums();
     if (failures) return 1;
     std::puts("all checks passed");

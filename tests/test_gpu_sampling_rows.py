@@ -147,3 +147,29 @@ def test_no_filter_and_filters_that_are_off(V, dtype):
             # float64 sums of the chunks against integers: V 2^-46 of the sum, and a rounding to float32 each
             assert ((p - prob).abs() <= (2.0 ** -23 + V * 2.0 ** -46) * prob).all()
             assert ((f - probs).abs() <= (2.0 ** -23 + V * 2.0 ** -46) * probs + 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("V", [5003, 40009])
+def test_infinite_temperatures_and_filters_that_are_no_numbers(V):
+    """An infinite temperature weighs all tokens alike, those an infinite distance from the first too; a temperature
+    of NaN is 0, another filter of NaN is off."""
+    rng = np.random.default_rng(V)
+    T = 6
+    big = 3.4028234663852886e38
+    x = rng.normal(size=(T, V)).astype(np.float32)
+    x[0, [5, V - 9]] = big, -big
+    x[1, 1:] = -big
+    x[2, ::2] = -big
+    x[2, 1] = big
+    x[3, rng.random(V) < 0.9] = -np.inf
+    xd = dev(x)
+    x, u = x.astype(np.float64), rng.random(T)
+    inf, nan = [np.inf] * T, [np.nan] * T
+    for kw in ({}, {"top_k": [V // 3] * T}, {"top_k": [50] * T}, {"top_p": [0.3] * T}, {"min_p": [0.5] * T},
+               {"top_k": [V - 3] * T, "top_p": [0.9] * T, "min_p": [1.0] * T}):
+        check(x, xd, u, temperature=inf, **kw)
+        check(x, xd, u, temperature=nan, **kw)
+    check(x, xd, u, top_p=nan)
+    check(x, xd, u, min_p=nan, top_k=[40] * T)
+    for kw in ({"top_k": [1500] * T}, {"top_p": [0.3] * T}, {"top_p": [0.999] * T}):    # the lowest value as a mask
+        check(x, xd, u, **kw)
