@@ -402,6 +402,93 @@ int kv4_attend(const moe_kv4_cache *cache, const moe_kv4_rows *rows, const void 
                size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
+ * Rows and pages of the 4-bit cache: what prompts need of it.
+ *
+ * Reads rows back as dense K and V, the values that the codes stand for: call
+ * row t = seg_off[s] + j is position len[s] + j of sequence s (the beginning
+ * of a prompt that stands already: len 0), rows without a page are zeros.
+ *   k, v [T, Hkv, D] out in dtype MOE_F32 or MOE_BF16 (exact in both), dense
+ * Limits: 0 <= T <= 2^22.  Errors: EINVAL, ENOTSUP (D, dtype). */
+int kv4_read(const moe_kv4_cache *cache, const moe_kv4_rows *rows, void *k, void *v, int32_t T, int32_t dtype,
+             void *stream);
+
+/* The pages of a pool and who holds them.  A table entry inside [0,
+ * num_pages) holds its page; refs counts the entries that hold each page, and
+ * a page is free while its count is 0 or below.  Sequences may share the pages
+ * of a common beginning.  The calls below keep counts and table in step; all
+ * layers' caches share one pool and differ in their data only, so that the
+ * data is moved by kv4_copy_pages, once for each layer.
+ *   refs  [num_pages] i32 (device), 0 for a new pool
+ *   table [nseq, max_pages] i32 (device), -1 for a new pool; the table of
+ *         moe_kv4_rows for sequences 0 .. nseq - 1, or a table of which the
+ *         caller gathers rows into one
+ *   page  rows of a page, a power of two, 16 .. 4096
+ * Limits: 1 <= num_pages <= 2^24, 1 <= nseq <= 2^16, nseq * max_pages <= 2^30,
+ * max_pages * page below 2^31 - 2^22.
+ * Lists name sequences by their row of the table (device, n <=
+ * MOE_MAX_SEGMENTS entries); one that is outside [0, nseq) names none. */
+typedef struct {
+    int32_t *refs, *table;
+    int32_t num_pages, page, nseq, max_pages;
+} moe_kv4_pool;
+
+/* Takes pages for the first rows[i] rows of sequence seq[i]: the entries from
+ * its first one without a page on get the lowest free pages.  Entries of the
+ * list are served in order, each whole or not at all.
+ *   ok [n] i32 out: 1 if the sequence holds pages for its rows now; 0 if too
+ *      few pages are free, or the table's row is too short, or seq[i] names no
+ *      sequence or one that an earlier entry names */
+int kv4_reserve(const moe_kv4_pool *pool, const int32_t *seq, const int32_t *rows, int32_t n, int32_t *ok, void *stream);
+
+/* Makes sequence dst[i] hold the first rows[i] rows of sequence src[i]: whole
+ * pages are shared, a page that is filled in part gets the lowest free page, into
+ * which its data has to be copied before either sequence writes.  What dst[i]
+ * held before is let go first.
+ *   pairs [n, 2] i32 out: (page, fresh page) for kv4_copy_pages; (-1, -1) where
+ *         nothing is to be copied
+ *   ok    [n] i32 out: 1 done.  0 if no page was free (dst[i] then holds
+ *         nothing), or nothing was done: a name outside [0, nseq), rows[i] above
+ *         a table's row, a dst[i] that an earlier entry names too, or that any
+ *         entry names as its source. */
+int kv4_fork(const moe_kv4_pool *pool, const int32_t *src, const int32_t *dst, const int32_t *rows, int32_t n,
+             int32_t *pairs, int32_t *ok, void *stream);
+
+/* Lets go the pages of sequence seq[i] behind its first keep[i] rows (0: all
+ * of them); their entries become -1.  A sequence named twice keeps the fewer. */
+int kv4_release(const moe_kv4_pool *pool, const int32_t *seq, const int32_t *keep, int32_t n, void *stream);
+
+/* Moves used pages to the pool's front: the i-th lowest free page takes the
+ * i-th highest used one while it lies below it, at most max_moves of them.
+ * Counts and table follow; the data has to be copied before the caches are
+ * used again.  With as many moves as it takes, the used pages are 0 .. U - 1.
+ *   pairs [max_moves, 2] i32 out: (from, to) for kv4_copy_pages, then (-1, -1);
+ *         no page is among both
+ *   ws    4-byte aligned, kv4_compact_workspace_bytes bytes, no initialisation
+ * Limits: 1 <= max_moves <= 2^24. */
+size_t kv4_compact_workspace_bytes(const moe_kv4_pool *pool, int32_t max_moves);
+int kv4_compact(const moe_kv4_pool *pool, int32_t max_moves, int32_t *pairs, void *ws, size_t ws_bytes, void *stream);
+
+/* Copies page pairs[i][0] of a cache to page pairs[i][1], for i < n; pairs with
+ * an entry outside [0, num_pages), or of one page twice, copy nothing.  A page that is
+ * written by two pairs, or read by one and written by another, holds any mix
+ * of them.
+ *   pairs [n, 2] i32 (device).  Limits: 0 <= n <= 2^24. */
+int kv4_copy_pages(const moe_kv4_cache *cache, const int32_t *pairs, int32_t n, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Prompts: any number of tokens a call, where moe_verify_layer takes 64.
+ *
+ * The experts of each token from its router logits [T, E] float32, rows
+ * `stride` elements apart: the first k by (logit desc, index asc), NaN counts
+ * as -inf and +inf as the largest float; gate weights are the softmax over
+ * them (0 where even the first is -inf).
+ *   topk_idx [T, k] i32, topk_w [T, k] f32 out, as moe_aux has them
+ * Limits: 0 <= T <= 2^24, 1 <= E <= MOE_MAX_EXPERTS, 1 <= k <= min(E,
+ * MOE_MAX_TOPK). */
+int route_tokens(const float *logits, int64_t stride, int32_t T, int32_t E, int32_t k, int32_t *topk_idx,
+                 float *topk_w, void *stream);
+
+/* ------------------------------------------------------------------------
  * Drawing and accepting draft tokens.  Both use the filtered distribution of
  * a row of logits l [V], defined in 64 bits:
  *   the tokens with l > -inf (NaN counts as -inf, +inf as the largest float)

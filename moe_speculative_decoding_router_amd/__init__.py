@@ -21,6 +21,13 @@ Entry points (same names as the C ABI in include/moe_verify.h):
   sample_tokens(logits, u, temperature, top_k, top_p, min_p, return_probs=False) -> (token, prob, probs)
   accept_drafts(logits, tokens, offsets, u, parent=None, draft_probs=None, u_final=None, ...)
                                       -> (out, path, count)
+  kv4_read(cache, table, start, offsets, dtype=torch.bfloat16) -> (k, v)
+  kv4_reserve(refs, table, page, seq, rows) -> ok
+  kv4_fork(refs, table, page, src, dst, rows) -> (pairs, ok)
+  kv4_release(refs, table, page, seq, keep)
+  kv4_compact(refs, table, max_moves=None)  -> pairs
+  kv4_copy_pages(cache, pairs)
+  route_tokens(logits, k)             -> (topk_idx, topk_w)
 """
 from __future__ import annotations
 
@@ -42,7 +49,9 @@ STAGE_NAMES = ("router", "route", "gate_up", "down", "combine")
 EXPORTED = ("moe_pack_weights", "moe_verify_workspace_bytes", "moe_verify_layer", "union_stats",
             "select_drafts", "select_drafts_static", "expand_drafts", "union_stats_segments", "gate_depths",
             "moe_stream_read", "moe_last_error", "moe_verify_layer_noalloc", "kv4_cache_bytes", "kv4_append",
-            "kv4_attend_workspace_bytes", "kv4_attend", "sample_workspace_bytes", "sample_tokens", "accept_drafts")
+            "kv4_attend_workspace_bytes", "kv4_attend", "sample_workspace_bytes", "sample_tokens", "accept_drafts",
+            "kv4_read", "kv4_reserve", "kv4_fork", "kv4_release", "kv4_compact_workspace_bytes", "kv4_compact",
+            "kv4_copy_pages", "route_tokens")
 
 _vp, _i32, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float
 _i64, _size = ctypes.c_int64, ctypes.c_size_t
@@ -70,6 +79,10 @@ class _KvCache(ctypes.Structure):
 
 class _KvRows(ctypes.Structure):
     _fields_ = [("table", _vp), ("max_pages", _i32), ("len", _vp), ("nseq", _i32), ("seg_off", _vp)]
+
+
+class _KvPool(ctypes.Structure):
+    _fields_ = [("refs", _vp), ("table", _vp), ("num_pages", _i32), ("page", _i32), ("nseq", _i32), ("max_pages", _i32)]
 
 
 class _Sampling(ctypes.Structure):
@@ -127,6 +140,23 @@ def lib() -> ctypes.CDLL:
         L.accept_drafts.argtypes = [_vp, _i64, _i32, _i32, _i32, fp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                     _vp, _size, _vp]
         L.accept_drafts.restype = ctypes.c_int
+        pp = ctypes.POINTER(_KvPool)
+        L.kv4_read.argtypes = [cp, rp, _vp, _vp, _i32, _i32, _vp]
+        L.kv4_read.restype = ctypes.c_int
+        L.kv4_reserve.argtypes = [pp, _vp, _vp, _i32, _vp, _vp]
+        L.kv4_reserve.restype = ctypes.c_int
+        L.kv4_fork.argtypes = [pp, _vp, _vp, _vp, _i32, _vp, _vp, _vp]
+        L.kv4_fork.restype = ctypes.c_int
+        L.kv4_release.argtypes = [pp, _vp, _vp, _i32, _vp]
+        L.kv4_release.restype = ctypes.c_int
+        L.kv4_compact_workspace_bytes.argtypes = [pp, _i32]
+        L.kv4_compact_workspace_bytes.restype = _size
+        L.kv4_compact.argtypes = [pp, _i32, _vp, _vp, _size, _vp]
+        L.kv4_compact.restype = ctypes.c_int
+        L.kv4_copy_pages.argtypes = [cp, _vp, _i32, _vp]
+        L.kv4_copy_pages.restype = ctypes.c_int
+        L.route_tokens.argtypes = [_vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp]
+        L.route_tokens.restype = ctypes.c_int
         L.moe_last_error.argtypes = []
         L.moe_last_error.restype = ctypes.c_char_p
         _lib = L
@@ -921,3 +951,144 @@ def accept_drafts(logits, tokens, offsets, u, *, parent=None, draft_probs=None, 
           ctypes.addressof(off), None if par is None else ctypes.addressof(par), _ptr(draft_probs), u.data_ptr(), _ptr(u_final),
           out.data_ptr(), path.data_ptr(), count.data_ptr(), ws.data_ptr(), ws.numel())
     return out, path, count
+
+
+# ---------------------------------------------------------------------------
+# Prompts: rows and pages of the cache, experts of many tokens
+# ---------------------------------------------------------------------------
+def kv4_read(cache: KV4Cache, table, start, offsets, *, dtype=None, out=None, stream=None):
+    """Rows of the cache as dense (k, v) [T, Hkv, D], the values that the
+    codes stand for: row t = offsets[s] + j is position start[s] + j of
+    sequence s; rows without a page are zeros.  table [nseq, max_pages] and
+    start [nseq] are int32 device tensors, offsets (host) [nseq + 1]; dtype
+    float32 or bfloat16 (the default).  out: a pair of dense tensors to write
+    to (their dtype counts)."""
+    import torch
+    dev = cache.data.device
+    c = cache._c(dev)
+    r, _ = _kv_rows(table, start, offsets, dev)
+    T = r._keep[len(r._keep) - 1]
+    shape = (T, cache.Hkv, cache.D)
+    owned = []
+    if T < 0:
+        raise ValueError("offsets must run from 0 and not decrease")
+    if out is None:
+        dtype = torch.bfloat16 if dtype is None else dtype
+        owned = [torch.empty(shape, dtype=dtype, device=dev) for _ in range(2)]
+        k, v = owned
+    else:
+        k, v = out
+        if dtype is not None and k.dtype != dtype:
+            raise ValueError(f"out has dtype {k.dtype}, dtype is {dtype}")
+        dtype = k.dtype
+        _dense(k, "out[0]", dtype, shape, dev)
+        _dense(v, "out[1]", dtype, shape, dev)
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"dtype must be float32 or bfloat16, got {dtype}")
+    _call(lib().kv4_read, dev, stream, owned, ctypes.byref(c), ctypes.byref(r), k.data_ptr(), v.data_ptr(), T,
+          MOE_F32 if dtype is torch.float32 else MOE_BF16)
+    return k, v
+
+
+def _pool(refs, table, page: int):
+    import torch
+    dev = getattr(refs, "device", None)
+    if getattr(refs, "dtype", None) is not torch.int32 or len(refs.shape) != 1 or not refs.is_cuda or not refs.is_contiguous():
+        raise ValueError("refs must be a contiguous int32 [num_pages] device tensor")
+    if (getattr(table, "dtype", None) is not torch.int32 or table.device != dev or len(table.shape) != 2
+            or not table.is_contiguous()):
+        raise ValueError(f"table must be a contiguous int32 [nseq, max_pages] tensor on {dev}")
+    return _KvPool(refs.data_ptr(), table.data_ptr(), refs.shape[0], page, table.shape[0], table.shape[1]), dev
+
+
+def _list(dev, **lists):
+    """Length of the int32 device lists, all of one length."""
+    import torch
+    n = None
+    for name, t in lists.items():
+        if getattr(t, "dtype", None) is not torch.int32 or len(t.shape) != 1:
+            raise ValueError(f"{name} must be an int32 [n] tensor on {dev}")
+        n = t.shape[0] if n is None else n
+        _dense(t, name, torch.int32, (n,), dev)
+    return n
+
+
+def kv4_reserve(refs, table, page: int, seq, rows, *, stream=None):
+    """Take pages for the first rows[i] rows of sequence seq[i] (a row of
+    table), the lowest free ones, each entry of the lists whole or not at all.
+    refs [num_pages] and table [nseq, max_pages] are int32 device tensors that
+    the call changes (zeros and -1 for a new pool); seq and rows [n] int32
+    device tensors, n at most 64.  Returns ok [n] int32."""
+    import torch
+    p, dev = _pool(refs, table, page)
+    n = _list(dev, seq=seq, rows=rows)
+    ok = torch.empty(n, dtype=torch.int32, device=dev)
+    _call(lib().kv4_reserve, dev, stream, [ok], ctypes.byref(p), seq.data_ptr(), rows.data_ptr(), n, ok.data_ptr())
+    return ok
+
+
+def kv4_fork(refs, table, page: int, src, dst, rows, *, stream=None):
+    """Make sequence dst[i] hold the first rows[i] rows of sequence src[i]:
+    whole pages are shared, one that is filled in part is replaced by a fresh
+    page.  Returns (pairs [n, 2], ok [n]) int32: the pages to copy in each
+    layer's cache (kv4_copy_pages) and whether the entry was done."""
+    import torch
+    p, dev = _pool(refs, table, page)
+    n = _list(dev, src=src, dst=dst, rows=rows)
+    pairs = torch.empty((n, 2), dtype=torch.int32, device=dev)
+    ok = torch.empty(n, dtype=torch.int32, device=dev)
+    _call(lib().kv4_fork, dev, stream, [pairs, ok], ctypes.byref(p), src.data_ptr(), dst.data_ptr(), rows.data_ptr(), n,
+          pairs.data_ptr(), ok.data_ptr())
+    return pairs, ok
+
+
+def kv4_release(refs, table, page: int, seq, keep, *, stream=None) -> None:
+    """Let go the pages of sequence seq[i] behind its first keep[i] rows."""
+    p, dev = _pool(refs, table, page)
+    n = _list(dev, seq=seq, keep=keep)
+    _call(lib().kv4_release, dev, stream, [], ctypes.byref(p), seq.data_ptr(), keep.data_ptr(), n)
+
+
+def kv4_compact(refs, table, max_moves: Optional[int] = None, *, workspace=None, stream=None):
+    """Move the pool's used pages to its front, at most max_moves of them
+    (None: half the pool, which is always enough).  refs and table follow;
+    returns pairs [max_moves, 2] int32 for kv4_copy_pages."""
+    import torch
+    p, dev = _pool(refs, table, 16)
+    most = max(1, refs.shape[0] // 2) if max_moves is None else max_moves
+    owned = []
+    ws = _workspace(lib().kv4_compact_workspace_bytes(ctypes.byref(p), most), "workspace", dev, workspace, owned)
+    pairs = torch.empty((most, 2), dtype=torch.int32, device=dev)
+    owned.append(pairs)
+    _call(lib().kv4_compact, dev, stream, owned, ctypes.byref(p), most, pairs.data_ptr(), ws.data_ptr(), ws.numel())
+    return pairs
+
+
+def kv4_copy_pages(cache: KV4Cache, pairs, *, stream=None) -> None:
+    """Copy page pairs[i][0] of the cache to page pairs[i][1] (int32 [n, 2]
+    device tensor); pairs outside the pool copy nothing."""
+    import torch
+    dev = cache.data.device
+    c = cache._c(dev)
+    n = pairs.shape[0] if hasattr(pairs, "shape") and len(pairs.shape) else 0
+    _dense(pairs, "pairs", torch.int32, (n, 2), dev)
+    _call(lib().kv4_copy_pages, dev, stream, [], ctypes.byref(c), pairs.data_ptr(), n)
+
+
+def route_tokens(logits, k: int, *, stream=None):
+    """The k experts of each token from its router logits [T, E] float32 (rows
+    may be further apart), by (logit desc, index asc), and their gate weights,
+    the softmax over them.  Returns (topk_idx [T, k] int32, topk_w [T, k]
+    float32)."""
+    import torch
+    dtype, stride = _rows_dtype(logits, "logits", 2)
+    if dtype != MOE_F32:
+        raise ValueError("logits must be float32")
+    dev = logits.device
+    T, E = logits.shape
+    if not 1 <= k <= E:
+        raise ValueError(f"k={k} outside [1, E={E}]")
+    idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+    w = torch.empty((T, k), dtype=torch.float32, device=dev)
+    _call(lib().route_tokens, dev, stream, [idx, w], logits.data_ptr(), stride, T, E, k, idx.data_ptr(), w.data_ptr())
+    return idx, w

@@ -1,40 +1,18 @@
 // The 4-bit K/V cache: quantisation of rows into pages, and the attention of
 // the verified tokens over it.  Layout and formulas in include/moe_verify.h.
 #include "common.h"
+#include "kv4.h"
 #include "serve.h"
 
 namespace moe {
 namespace {
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-
-// 2^(e - 127) of a scale byte.
-__device__ __forceinline__ float scale_of(unsigned e) { return __uint_as_float(e << 23); }
-
-__device__ __forceinline__ bf16x8 dequant8(unsigned w, float s) {
-    union {
-        bf16x2 h[4];
-        bf16x8 v;
-    } o;
-    o.h[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
-    o.h[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1);
-    o.h[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2);
-    o.h[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3);
-    return o.v;
-}
 
 // float32 -> bf16 bits by the hardware's conversion: to nearest, ties to even,
 // and NaN stays NaN whatever its payload.
 __device__ __forceinline__ unsigned bf16_bits(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
-
-// Bytes of a row's 17 D / 16 share: a tile holds 16 rows of K, its scales, V and its scales.
-template <int D>
-struct Tile {
-    static constexpr int kK = 0, kKs = 8 * D, kV = 17 * D / 2, kVs = 33 * D / 2, kBytes = 17 * D;
-};
 
 // ---------------------------------------------------------------------------
 // Append.  One lane holds 8 consecutive elements of a row, so 4 lanes share a
@@ -141,11 +119,11 @@ __global__ __launch_bounds__(kThreads) void append_kernel(KvAppendArgs a) {
         const size_t o = ((size_t)t * a.r.Hkv + h) * D + l * 8;
         void *dst = isv ? a.v_out : a.k_out;
         if constexpr (F32) {
-            const f32x2 y0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, sc, 0), y1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, sc, 1);
-            const f32x2 y2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, sc, 2), y3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, sc, 3);
             f32x4 *p = reinterpret_cast<f32x4 *>((float *)dst + o);
-            p[0] = f32x4{y0[0], y0[1], y1[0], y1[1]};
-            p[1] = f32x4{y2[0], y2[1], y3[0], y3[1]};
+            f32x4 y0, y1;
+            dequant8_f32(word, sc, y0, y1);
+            p[0] = y0;
+            p[1] = y1;
         } else {
             *reinterpret_cast<bf16x8 *>((uint16_t *)dst + o) = dequant8(word, sc);
         }

@@ -1,0 +1,458 @@
+// Pages of the 4-bit K/V cache: rows read back as dense K and V, and the page
+// tables' bookkeeping (pages taken, shared, let go, moved together, copied).
+// Layout and semantics in include/moe_verify.h.
+#include "common.h"
+#include "kv4.h"
+#include "prompt.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+
+// ---------------------------------------------------------------------------
+// Read.  The inverse of append: a lane holds 8 consecutive elements of a row
+// (4 code bytes in, 16 or 32 bytes out), a wave 512 / D consecutive rows of
+// one head, kReadAhead times over so that its loads are under way together.
+// K and V are the grid's z.
+// ---------------------------------------------------------------------------
+constexpr int kReadAhead = 4;
+
+template <int D, bool F32>
+__global__ __launch_bounds__(kThreads) void read_kernel(KvReadArgs a) {
+    constexpr int LPR = D / 8, RPW = 64 / LPR, W = D / 32;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int h = blockIdx.y;
+    const bool isv = blockIdx.z != 0;
+    const int l = lane % LPR;
+    const int t0 = (blockIdx.x * (kThreads / 64) + wave) * RPW * kReadAhead + lane / LPR;
+    unsigned word[kReadAhead], sc[kReadAhead];
+#pragma unroll
+    for (int u = 0; u < kReadAhead; ++u) {
+        const int t = t0 + u * RPW;
+        word[u] = 0;  // code 0 of any scale: rows without a page are zeros
+        sc[u] = 127;
+        if (t >= a.T) continue;
+        int s = 0;
+        while (t >= a.r.off[s + 1]) ++s;
+        const int64_t pos = (int64_t)max(a.r.len[s], 0) + (t - a.r.off[s]);
+        const int64_t slot = pos >> a.r.page_shift;
+        if (slot >= a.r.max_pages) continue;
+        const int pid = a.r.table[(size_t)s * a.r.max_pages + slot];
+        if (pid < 0 || pid >= a.r.num_pages) continue;
+        const int in = (int)pos & ((1 << a.r.page_shift) - 1), i = in & 15;
+        const uint8_t *tile =
+            a.r.data + ((((size_t)pid * a.r.Hkv + h) << (a.r.page_shift - 4)) + (in >> 4)) * Tile<D>::kBytes;
+        if (!isv) {
+            word[u] = *reinterpret_cast<const unsigned *>(tile + Tile<D>::kK + i * (D / 2) + l * 4);
+        } else {
+            const uint8_t *v = tile + Tile<D>::kV + (64 * (i >> 2) + (i & 3)) * W;
+            if (D == 64) {
+                word[u] = *reinterpret_cast<const uint16_t *>(v + (2 * l) * 4 * W) |
+                          (unsigned)*reinterpret_cast<const uint16_t *>(v + (2 * l + 1) * 4 * W) << 16;
+            } else if (D == 128) {
+                word[u] = *reinterpret_cast<const unsigned *>(v + l * 4 * W);
+            } else {
+                word[u] = *reinterpret_cast<const unsigned *>(v + (l >> 1) * 4 * W + (l & 1) * 4);
+            }
+        }
+        sc[u] = tile[(isv ? Tile<D>::kVs : Tile<D>::kKs) + 16 * (l >> 2) + i];
+    }
+#pragma unroll
+    for (int u = 0; u < kReadAhead; ++u) {
+        const int t = t0 + u * RPW;
+        if (t >= a.T) continue;
+        const size_t o = ((size_t)t * a.r.Hkv + h) * D + l * 8;
+        const float s = scale_of(sc[u]);
+        void *dst = isv ? a.v : a.k;
+        if constexpr (F32) {
+            f32x4 y0, y1;
+            dequant8_f32(word[u], s, y0, y1);
+            f32x4 *p = reinterpret_cast<f32x4 *>((float *)dst + o);
+            p[0] = y0;
+            p[1] = y1;
+        } else {
+            *reinterpret_cast<bf16x8 *>((uint16_t *)dst + o) = dequant8(word[u], s);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Page bookkeeping.  Lists of at most 64 sequences: one workgroup, whose
+// accesses to the counts bypass its L1 (agent scope), since its own atomics
+// change them in between.  Everything is integers and chosen by rank, so
+// results do not depend on the order in which atomics arrive.
+// ---------------------------------------------------------------------------
+constexpr int kBookThreads = 1024;
+constexpr int kScan = 8;  // counts of a thread at a time in the search for free pages
+
+__device__ __forceinline__ int count_of(const int32_t *refs, int p) {
+    return __hip_atomic_load(refs + p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+struct Take {  // what the list's entries need, in LDS
+    int need[kMaxSegments];   // fresh pages
+    int start[kMaxSegments];  // rank of the first of them among the pages taken, -1: not served
+    long long at[kMaxSegments];  // table index of the first
+    int total, found;
+    int wave[kBookThreads / 64];
+};
+
+// Number of free pages before this thread's run of the chunk at `base`, and
+// the mask of its free ones.
+__device__ int free_before(const PoolArgs &a, int base, Take &t, unsigned &mask, int &all) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    mask = 0;
+    const int p0 = base + threadIdx.x * kScan;
+    int v[kScan];
+#pragma unroll
+    for (int i = 0; i < kScan; ++i) v[i] = p0 + i < a.num_pages ? count_of(a.refs, p0 + i) : 1;
+#pragma unroll
+    for (int i = 0; i < kScan; ++i) mask |= (unsigned)(v[i] <= 0) << i;
+    const int mine = __popc(mask), incl = wave_incl_scan(mine);
+    __syncthreads();  // the last chunk's sums are read
+    if (lane == 63) t.wave[wave] = incl;
+    __syncthreads();
+    int before = incl - mine;
+    all = 0;
+    for (int w = 0; w < kBookThreads / 64; ++w) {
+        const int x = t.wave[w];
+        if (w < wave) before += x;
+        all += x;
+    }
+    return before;
+}
+
+// Gives entry i of the list its need[i] lowest free pages, the entries in
+// order, each whole or not at all; writes them to table[at[i]...] with a count
+// of 1 and sets start[i] (-1: not enough pages).
+__device__ void take_pages(const PoolArgs &a, Take &t) {
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        long long sum = 0;
+        for (int i = 0; i < a.n; ++i) sum += t.need[i];
+        t.total = (int)(sum < a.num_pages ? sum : a.num_pages);
+    }
+    __syncthreads();
+    // how many are free, up to the number that is needed
+    unsigned mask;
+    int all, found = 0, end = 0;
+    for (int base = 0; base < a.num_pages && found < t.total; base += kBookThreads * kScan) {
+        free_before(a, base, t, mask, all);
+        found += all;
+        end = base + kBookThreads * kScan;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int used = 0;
+        for (int i = 0; i < a.n; ++i) {
+            const bool fits = t.need[i] <= found - used;
+            t.start[i] = fits ? used : -1;
+            if (fits) used += t.need[i];
+        }
+        t.total = used;
+    }
+    __syncthreads();
+    int before = 0;
+    for (int base = 0; base < end && before < t.total; base += kBookThreads * kScan) {
+        int rank = before + free_before(a, base, t, mask, all);
+        for (int i = 0; i < kScan; ++i) {
+            if (!((mask >> i) & 1)) continue;
+            if (rank < t.total) {
+                int e = 0;  // the entry whose run holds this rank
+                for (int j = 0; j < a.n; ++j)
+                    if (t.start[j] >= 0 && t.need[j] > 0 && t.start[j] <= rank) e = j;
+                const int p = base + threadIdx.x * kScan + i;
+                a.table[t.at[e] + (rank - t.start[e])] = p;
+                a.refs[p] = 1;
+                t.found = p;
+            }
+            ++rank;
+        }
+        before += all;
+        __syncthreads();
+    }
+    __syncthreads();
+}
+
+__global__ __launch_bounds__(kBookThreads) void reserve_kernel(PoolArgs a) {
+    __shared__ Take t;
+    __shared__ int seq[kMaxSegments], want[kMaxSegments], have[kMaxSegments];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (threadIdx.x < a.n) {
+        const int i = threadIdx.x, rows = a.rows[i];
+        seq[i] = a.dst[i];
+        const int64_t pages = ((int64_t)max(rows, 0) + (1 << a.page_shift) - 1) >> a.page_shift;
+        want[i] = pages <= a.max_pages && seq[i] >= 0 && seq[i] < a.nseq ? (int)pages : -1;
+    }
+    __syncthreads();
+    if (threadIdx.x < a.n)
+        for (int j = 0; j < (int)threadIdx.x; ++j)
+            if (seq[j] == seq[threadIdx.x]) want[threadIdx.x] = -1;
+    __syncthreads();
+    for (int i = wave; i < a.n; i += kBookThreads / 64) {
+        int run = 0;  // leading entries that name a page
+        if (want[i] > 0) {
+            const int32_t *row = a.table + (size_t)seq[i] * a.max_pages;
+            for (; run < want[i]; run += 64) {
+                const int p = run + lane < want[i] ? row[run + lane] : -1;
+                const uint64_t bad = __ballot(p < 0 || p >= a.num_pages);
+                if (bad) {
+                    run += __ffsll((unsigned long long)bad) - 1;
+                    break;
+                }
+            }
+        }
+        if (lane == 0) {
+            have[i] = run;
+            t.need[i] = want[i] > run ? want[i] - run : 0;
+            t.at[i] = (long long)(want[i] < 0 ? 0 : seq[i]) * a.max_pages + run;
+        }
+    }
+    take_pages(a, t);
+    if (threadIdx.x < a.n) a.ok[threadIdx.x] = want[threadIdx.x] >= 0 && t.start[threadIdx.x] >= 0;
+}
+
+__global__ __launch_bounds__(kBookThreads) void fork_kernel(PoolArgs a) {
+    __shared__ Take t;
+    __shared__ int src[kMaxSegments], dst[kMaxSegments], full[kMaxSegments], last[kMaxSegments], valid[kMaxSegments];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    if (tid < a.n) {
+        const int rows = a.rows[tid], page = 1 << a.page_shift;
+        src[tid] = a.src[tid];
+        dst[tid] = a.dst[tid];
+        full[tid] = max(rows, 0) >> a.page_shift;
+        last[tid] = max(rows, 0) & (page - 1) ? 0 : -1;  // whether a page is filled in part
+        const int64_t pages = ((int64_t)max(rows, 0) + page - 1) >> a.page_shift;
+        valid[tid] = pages <= a.max_pages && src[tid] >= 0 && src[tid] < a.nseq && dst[tid] >= 0 && dst[tid] < a.nseq;
+    }
+    __syncthreads();
+    if (tid < a.n) {
+        int v = valid[tid];
+        for (int j = 0; j < a.n; ++j) v &= src[j] != dst[tid] && (j >= tid || dst[j] != dst[tid]);
+        valid[tid] = v;
+    }
+    __syncthreads();
+    // the former pages of the slots that are filled are let go, the shared ones counted
+    for (int i = wave; i < a.n; i += kBookThreads / 64) {
+        int part = -1;
+        if (valid[i]) {
+            int32_t *to = a.table + (size_t)dst[i] * a.max_pages;
+            const int32_t *from = a.table + (size_t)src[i] * a.max_pages;
+            for (int j = lane; j < a.max_pages; j += 64) {
+                const int old = to[j], p = from[j];
+                if (old >= 0 && old < a.num_pages) atomicSub(a.refs + old, 1);
+                const bool live = p >= 0 && p < a.num_pages, share = live && j < full[i];
+                if (share) atomicAdd(a.refs + p, 1);
+                to[j] = share ? p : -1;
+            }
+            if (last[i] == 0) {
+                const int p = from[full[i]];
+                part = p >= 0 && p < a.num_pages ? p : -1;
+            }
+        }
+        if (lane == 0) {
+            last[i] = part;
+            t.need[i] = part >= 0;
+            t.at[i] = (long long)(valid[i] ? dst[i] : 0) * a.max_pages + full[i];
+        }
+    }
+    __threadfence();
+    take_pages(a, t);
+    for (int i = wave; i < a.n; i += kBookThreads / 64) {
+        if (!valid[i] || t.start[i] >= 0) continue;  // no page was left for this one: its slot stays empty
+        int32_t *to = a.table + (size_t)dst[i] * a.max_pages;
+        for (int j = lane; j < full[i]; j += 64) {
+            const int p = to[j];
+            if (p >= 0 && p < a.num_pages) atomicSub(a.refs + p, 1);
+            to[j] = -1;
+        }
+    }
+    if (tid < a.n) {
+        const bool ok = valid[tid] && t.start[tid] >= 0;
+        const bool copy = ok && last[tid] >= 0;
+        a.pairs[2 * tid] = copy ? last[tid] : -1;
+        a.pairs[2 * tid + 1] = copy ? a.table[t.at[tid]] : -1;
+        a.ok[tid] = ok;
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void release_kernel(PoolArgs a) {
+    const int i = blockIdx.y, s = a.dst[i];
+    if (s < 0 || s >= a.nseq) return;
+    const int64_t keep = ((int64_t)max(a.rows[i], 0) + (1 << a.page_shift) - 1) >> a.page_shift;
+    int32_t *row = a.table + (size_t)s * a.max_pages;
+    for (int64_t j = keep + blockIdx.x * kThreads + threadIdx.x; j < a.max_pages; j += (int64_t)gridDim.x * kThreads) {
+        // a sequence listed twice: only one of the two takes the entry
+        const int p = atomicExch(row + j, -1);
+        if (p >= 0 && p < a.num_pages) atomicSub(a.refs + p, 1);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Compaction.  The i-th lowest free page takes the i-th highest used one
+// while it lies below it: the fewest moves that leave the used pages together
+// at the front, and no page is both read and written.  Three launches: used
+// pages of each chunk; ranks; pairs, counts and tables.
+// ---------------------------------------------------------------------------
+constexpr int kChunk = kThreads * 16;  // pages of a workgroup
+
+__global__ __launch_bounds__(kThreads) void count_kernel(CompactArgs a) {
+    __shared__ int part[kThreads / 64];
+    int n = 0;
+    for (int i = 0; i < kChunk / kThreads; ++i) {
+        const int p = blockIdx.x * kChunk + i * kThreads + threadIdx.x;
+        n += p < a.num_pages && a.refs[p] > 0;
+    }
+    n = wave_sum_int(n);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = n;
+    __syncthreads();
+    if (threadIdx.x == 0) a.chunk[blockIdx.x] = part[0] + part[1] + part[2] + part[3];
+}
+
+__global__ __launch_bounds__(kThreads) void rank_kernel(CompactArgs a) {
+    __shared__ int part[2][kThreads / 64], run[kThreads / 64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int before = 0, all = 0;
+    for (int c = threadIdx.x; c < a.chunks; c += kThreads) {
+        const int n = a.chunk[c];
+        all += n;
+        before += c < (int)blockIdx.x ? n : 0;
+    }
+    all = wave_sum_int(all);
+    before = wave_sum_int(before);
+    if (lane == 0) part[0][wave] = all, part[1][wave] = before;
+    __syncthreads();
+    all = part[0][0] + part[0][1] + part[0][2] + part[0][3];
+    before = part[1][0] + part[1][1] + part[1][2] + part[1][3];
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.chunk[a.chunks] = all;
+    for (int i = 0; i < kChunk / kThreads; ++i) {
+        const int p = blockIdx.x * kChunk + i * kThreads + threadIdx.x;
+        const bool used = p < a.num_pages && a.refs[p] > 0;
+        const int incl = wave_incl_scan(used);
+        if (lane == 63) run[wave] = incl;
+        __syncthreads();
+        int u = before + incl - used;  // used pages below p
+        for (int w = 0; w < kThreads / 64; ++w) {
+            if (w < wave) u += run[w];
+            before += run[w];
+        }
+        __syncthreads();
+        if (p >= a.num_pages) continue;
+        const int rank = used ? all - 1 - u : p - u;  // from the top, or from the bottom
+        a.rank[p] = used ? rank : -1;
+        if (rank < a.most) (used ? a.high : a.low)[rank] = p;
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void move_kernel(CompactArgs a) {
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int used = a.chunk[a.chunks];
+    const int most = min(a.most, min(used, a.num_pages - used));
+    if (i < a.max_moves) {
+        int from = -1, to = -1;
+        if (i < most && a.low[i] < a.high[i]) {
+            from = a.high[i];
+            to = a.low[i];
+            a.refs[to] = a.refs[from];
+            a.refs[from] = 0;
+        }
+        a.pairs[2 * i] = from;
+        a.pairs[2 * i + 1] = to;
+    }
+    if (i < (int64_t)a.nseq * a.max_pages) {
+        const int p = a.table[i];
+        if (p >= 0 && p < a.num_pages) {
+            const int r = a.rank[p];
+            if (r >= 0 && r < most && a.low[r] < p) a.table[i] = a.low[r];
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Copy.  A workgroup copies 16 KB of a page, four 16-byte loads a thread
+// under way together.
+// ---------------------------------------------------------------------------
+constexpr int kPiece = 4 * kThreads * 16;
+
+__global__ __launch_bounds__(kThreads) void copy_kernel(CopyArgs a) {
+    const int64_t all = (int64_t)a.n * a.pieces;
+    for (int64_t w = blockIdx.x; w < all; w += gridDim.x) {
+        const int i = (int)(w / a.pieces);
+        const size_t in = (size_t)(w - (int64_t)i * a.pieces) * kPiece;
+        const int from = a.pairs[2 * (size_t)i], to = a.pairs[2 * (size_t)i + 1];
+        if (from < 0 || from >= a.num_pages || to < 0 || to >= a.num_pages || from == to) continue;
+        const uint8_t *s = a.data + (size_t)from * a.page_bytes;
+        uint8_t *d = a.data + (size_t)to * a.page_bytes;
+        u32x4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const size_t at = in + (j * kThreads + threadIdx.x) * 16;
+            if (at < a.page_bytes) v[j] = *reinterpret_cast<const u32x4 *>(s + at);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const size_t at = in + (j * kThreads + threadIdx.x) * 16;
+            if (at < a.page_bytes) *reinterpret_cast<u32x4 *>(d + at) = v[j];
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_kv4_read(const KvReadArgs &a, hipStream_t s) {
+    const int rows = kThreads / 64 * (512 / a.r.D) * kReadAhead;
+    const dim3 grid((a.T + rows - 1) / rows, a.r.Hkv, 2);
+    void (*k)(KvReadArgs) = nullptr;
+    if (a.r.D == 64) k = a.f32 ? read_kernel<64, true> : read_kernel<64, false>;
+    else if (a.r.D == 128) k = a.f32 ? read_kernel<128, true> : read_kernel<128, false>;
+    else k = a.f32 ? read_kernel<256, true> : read_kernel<256, false>;
+    hipLaunchKernelGGL(k, grid, dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_reserve(const PoolArgs &a, hipStream_t s) {
+    hipLaunchKernelGGL(reserve_kernel, dim3(1), dim3(kBookThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_fork(const PoolArgs &a, hipStream_t s) {
+    hipLaunchKernelGGL(fork_kernel, dim3(1), dim3(kBookThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_release(const PoolArgs &a, hipStream_t s) {
+    const int x = (a.max_pages + 4 * kThreads - 1) / (4 * kThreads);
+    hipLaunchKernelGGL(release_kernel, dim3(x < 256 ? x : 256, a.n), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+// Workspace: used pages of each chunk and of all, the lowest free and the
+// highest used pages, the used pages' ranks.
+size_t compact_ws_bytes(int num_pages, int max_moves) {
+    const int most = max_moves < num_pages / 2 ? max_moves : num_pages / 2;
+    return 4 * ((size_t)(num_pages + kChunk - 1) / kChunk + 1 + 2 * (size_t)most + num_pages);
+}
+
+hipError_t launch_compact(CompactArgs a, int32_t *ws, hipStream_t s) {
+    a.most = a.max_moves < a.num_pages / 2 ? a.max_moves : a.num_pages / 2;
+    a.chunks = (a.num_pages + kChunk - 1) / kChunk;
+    a.chunk = ws;
+    a.low = a.chunk + a.chunks + 1;
+    a.high = a.low + a.most;
+    a.rank = a.high + a.most;
+    hipLaunchKernelGGL(count_kernel, dim3(a.chunks), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL(rank_kernel, dim3(a.chunks), dim3(kThreads), 0, s, a);
+    const int64_t n = (int64_t)a.nseq * a.max_pages > a.max_moves ? (int64_t)a.nseq * a.max_pages : a.max_moves;
+    hipLaunchKernelGGL(move_kernel, dim3((unsigned)((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_copy_pages(CopyArgs a, hipStream_t s) {
+    a.pieces = (int)((a.page_bytes + kPiece - 1) / kPiece);
+    const int64_t all = (int64_t)a.n * a.pieces;
+    hipLaunchKernelGGL(copy_kernel, dim3((unsigned)(all < 16384 ? all : 16384)), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,164 @@
+// Host side of the operators for prompts: argument validation and launches.
+// No allocation, no synchronisation, no per-call state.
+#include "prompt.h"
+
+#include <cmath>
+
+#include "checks.h"
+
+namespace {
+
+using namespace moe;
+
+int check_pool(const moe_kv4_pool *p, PoolArgs *a) {
+    if (!p) return fail(MOE_EINVAL, "pool is NULL");
+    if (!p->refs || !p->table) return fail(MOE_EINVAL, "refs and table must be non-NULL");
+    if (p->num_pages < 1 || p->num_pages > (1 << 24)) return fail(MOE_EINVAL, "num_pages=%d outside [1, 2^24]", p->num_pages);
+    if (p->page < 16 || p->page > 4096 || (p->page & (p->page - 1)) != 0)
+        return fail(MOE_EINVAL, "page=%d must be a power of two, 16 .. 4096", p->page);
+    if (p->nseq < 1 || p->nseq > (1 << 16)) return fail(MOE_EINVAL, "nseq=%d outside [1, 2^16]", p->nseq);
+    if (p->max_pages < 1 || (int64_t)p->max_pages * p->page > (int64_t)INT32_MAX - (1 << 22))
+        return fail(MOE_EINVAL, "max_pages=%d must be positive, and max_pages * page below 2^31 - 2^22", p->max_pages);
+    if ((int64_t)p->nseq * p->max_pages > (1 << 30)) return fail(MOE_EINVAL, "nseq * max_pages above 2^30");
+    if (misaligned(p->refs, 4) || misaligned(p->table, 4)) return fail(MOE_EINVAL, "refs and table must be 4-byte aligned");
+    a->refs = p->refs;
+    a->table = p->table;
+    a->num_pages = p->num_pages;
+    a->page_shift = __builtin_ctz((unsigned)p->page);
+    a->nseq = p->nseq;
+    a->max_pages = p->max_pages;
+    return MOE_OK;
+}
+
+int check_list(int n) {
+    if (n < 0 || n > kMaxSegments) return fail(MOE_EINVAL, "n=%d outside [0, %d]", n, kMaxSegments);
+    return MOE_OK;
+}
+
+int check_moves(int max_moves) {
+    if (max_moves < 1 || max_moves > (1 << 24)) return fail(MOE_EINVAL, "max_moves=%d outside [1, 2^24]", max_moves);
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int kv4_read(const moe_kv4_cache *cache, const moe_kv4_rows *rows, void *k, void *v, int32_t T, int32_t dtype,
+             void *stream) {
+    if (T < 0 || T > (1 << 22)) return fail(MOE_EINVAL, "T=%d outside [0, 2^22]", T);
+    KvReadArgs a{};
+    int rc = check_rows(cache, rows, T, &a.r);
+    if (rc == MOE_OK) rc = check_row_pointers(a.r);
+    if (rc == MOE_OK) rc = check_dtype(dtype);
+    if (rc != MOE_OK) return rc;
+    if (T == 0) return MOE_OK;
+    if (!k || !v) return fail(MOE_EINVAL, "k and v must be non-NULL");
+    if (misaligned(k, 16) || misaligned(v, 16)) return fail(MOE_EINVAL, "k and v must be 16-byte aligned");
+    a.k = k;
+    a.v = v;
+    a.T = T;
+    a.f32 = dtype == MOE_F32;
+    return launched(launch_kv4_read(a, static_cast<hipStream_t>(stream)));
+}
+
+int kv4_reserve(const moe_kv4_pool *pool, const int32_t *seq, const int32_t *rows, int32_t n, int32_t *ok, void *stream) {
+    PoolArgs a{};
+    int rc = check_pool(pool, &a);
+    if (rc == MOE_OK) rc = check_list(n);
+    if (rc != MOE_OK) return rc;
+    if (n == 0) return MOE_OK;
+    if (!seq || !rows || !ok) return fail(MOE_EINVAL, "seq, rows and ok must be non-NULL");
+    a.n = n;
+    a.dst = seq;
+    a.rows = rows;
+    a.ok = ok;
+    return launched(launch_reserve(a, static_cast<hipStream_t>(stream)));
+}
+
+int kv4_fork(const moe_kv4_pool *pool, const int32_t *src, const int32_t *dst, const int32_t *rows, int32_t n,
+             int32_t *pairs, int32_t *ok, void *stream) {
+    PoolArgs a{};
+    int rc = check_pool(pool, &a);
+    if (rc == MOE_OK) rc = check_list(n);
+    if (rc != MOE_OK) return rc;
+    if (n == 0) return MOE_OK;
+    if (!src || !dst || !rows || !pairs || !ok) return fail(MOE_EINVAL, "src, dst, rows, pairs and ok must be non-NULL");
+    a.n = n;
+    a.src = src;
+    a.dst = dst;
+    a.rows = rows;
+    a.pairs = pairs;
+    a.ok = ok;
+    return launched(launch_fork(a, static_cast<hipStream_t>(stream)));
+}
+
+int kv4_release(const moe_kv4_pool *pool, const int32_t *seq, const int32_t *keep, int32_t n, void *stream) {
+    PoolArgs a{};
+    int rc = check_pool(pool, &a);
+    if (rc == MOE_OK) rc = check_list(n);
+    if (rc != MOE_OK) return rc;
+    if (n == 0) return MOE_OK;
+    if (!seq || !keep) return fail(MOE_EINVAL, "seq and keep must be non-NULL");
+    a.n = n;
+    a.dst = seq;
+    a.rows = keep;
+    return launched(launch_release(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t kv4_compact_workspace_bytes(const moe_kv4_pool *pool, int32_t max_moves) {
+    PoolArgs a{};
+    if (check_pool(pool, &a) != MOE_OK || check_moves(max_moves) != MOE_OK) return 0;
+    return compact_ws_bytes(a.num_pages, max_moves);
+}
+
+int kv4_compact(const moe_kv4_pool *pool, int32_t max_moves, int32_t *pairs, void *ws, size_t ws_bytes, void *stream) {
+    PoolArgs a{};
+    int rc = check_pool(pool, &a);
+    if (rc == MOE_OK) rc = check_moves(max_moves);
+    if (rc != MOE_OK) return rc;
+    if (!pairs || !ws) return fail(MOE_EINVAL, "pairs and the workspace must be non-NULL");
+    if (misaligned(ws, 4)) return fail(MOE_EINVAL, "the workspace must be 4-byte aligned");
+    const size_t need = compact_ws_bytes(a.num_pages, max_moves);
+    if (ws_bytes < need) return fail(MOE_EWORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+    CompactArgs c{};
+    c.refs = a.refs;
+    c.table = a.table;
+    c.num_pages = a.num_pages;
+    c.nseq = a.nseq;
+    c.max_pages = a.max_pages;
+    c.max_moves = max_moves;
+    c.pairs = pairs;
+    return launched(launch_compact(c, static_cast<int32_t *>(ws), static_cast<hipStream_t>(stream)));
+}
+
+int kv4_copy_pages(const moe_kv4_cache *cache, const int32_t *pairs, int32_t n, void *stream) {
+    if (!cache) return fail(MOE_EINVAL, "cache is NULL");
+    const int rc = check_cache_sizes(cache->num_pages, cache->page, cache->Hkv, cache->D);
+    if (rc != MOE_OK) return rc;
+    if (n < 0 || n > (1 << 24)) return fail(MOE_EINVAL, "n=%d outside [0, 2^24]", n);
+    if (!cache->data) return fail(MOE_EINVAL, "cache data must be non-NULL");
+    if (misaligned(cache->data, 16)) return fail(MOE_EINVAL, "cache data must be 16-byte aligned");
+    if (n == 0) return MOE_OK;
+    if (!pairs) return fail(MOE_EINVAL, "pairs is NULL");
+    CopyArgs a{};
+    a.data = static_cast<uint8_t *>(cache->data);
+    a.page_bytes = (size_t)cache->Hkv * (cache->page / 16) * 17 * cache->D;
+    a.pairs = pairs;
+    a.num_pages = cache->num_pages;
+    a.n = n;
+    return launched(launch_copy_pages(a, static_cast<hipStream_t>(stream)));
+}
+
+int route_tokens(const float *logits, int64_t stride, int32_t T, int32_t E, int32_t k, int32_t *topk_idx, float *topk_w,
+                 void *stream) {
+    if (T < 0 || T > (1 << 24)) return fail(MOE_EINVAL, "T=%d outside [0, 2^24]", T);
+    if (E < 1 || E > MOE_MAX_EXPERTS) return fail(MOE_EINVAL, "E=%d outside [1, %d]", E, MOE_MAX_EXPERTS);
+    if (k < 1 || k > E || k > MOE_MAX_TOPK) return fail(MOE_EINVAL, "k=%d outside [1, min(E, %d)]", k, MOE_MAX_TOPK);
+    if (stride < E) return fail(MOE_EINVAL, "stride=%lld is below E=%d", (long long)stride, E);
+    if (T == 0) return MOE_OK;
+    if (!logits || !topk_idx || !topk_w) return fail(MOE_EINVAL, "logits, topk_idx and topk_w must be non-NULL");
+    return launched(launch_route_tokens(logits, stride, T, E, k, topk_idx, topk_w, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
