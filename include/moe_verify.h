@@ -477,8 +477,36 @@ int kv4_copy_pages(const moe_kv4_cache *cache, const int32_t *pairs, int32_t n, 
 
 /* ------------------------------------------------------------------------
  * Prompts: any number of tokens a call, where moe_verify_layer takes 64.
- *
- * The experts of each token from its router logits [T, E] float32, rows
+ */
+
+/* Attention of prompts: causal, over dense K and V of sequences packed one
+ * behind the other.
+ *   out[t, h] = sum_p softmax_p(scale * q[t, h] . k[p, h / (Hq / Hkv)]) v[p, ...]
+ * Row j of a sequence with n query rows and m keys sees its first
+ * j + 1 + (m - n) keys: with m = n a whole prompt, with m > n its next piece,
+ * behind m - n rows that stand already (kv4_read has them); with m < n the first
+ * n - m rows see nothing and get zeros.
+ *   q [T, Hq, D], k, v [Tk, Hkv, D] in dtype MOE_F32 or MOE_BF16, tokens
+ *         q_stride / k_stride / v_stride elements apart (slices of a fused
+ *         projection), 16-byte aligned rows; out [T, Hq, D] in dtype, dense
+ *   q_off, k_off (host) [nseq + 1], 0 = off[0] <= ... <= off[nseq] = T (Tk),
+ *         read during the call only; 1 <= nseq <= MOE_MAX_SEGMENTS
+ *   ws    256-byte aligned, prompt_attend_workspace_bytes bytes, no
+ *         initialisation; may be NULL where that is 0
+ * Sums and softmax statistics are float32.  bf16: probabilities enter the
+ * second product rounded to bf16.  float32: all operands enter the products as
+ * three bf16 terms (24 bits).  Rows of one sequence do not touch another's
+ * results; a k or v that is no finite number may make any result of its
+ * sequence and head NaN.
+ * Limits: 0 <= T, Tk <= 2^22, D 64, 128 or 256, Hq a multiple of Hkv, at most
+ * 8192, strides up to 2^24 elements. */
+size_t prompt_attend_workspace_bytes(int32_t nseq, const int32_t *q_off, const int32_t *k_off, int32_t Hq, int32_t Hkv,
+                                     int32_t D, int32_t dtype);
+int prompt_attend(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                  int32_t nseq, const int32_t *q_off, const int32_t *k_off, int32_t Hq, int32_t Hkv, int32_t D,
+                  int32_t dtype, float scale, void *out, void *ws, size_t ws_bytes, void *stream);
+
+/* The experts of each token from its router logits [T, E] float32, rows
  * `stride` elements apart: the first k by (logit desc, index asc), NaN counts
  * as -inf and +inf as the largest float; gate weights are the softmax over
  * them (0 where even the first is -inf).

@@ -27,6 +27,7 @@ Entry points (same names as the C ABI in include/moe_verify.h):
   kv4_release(refs, table, page, seq, keep)
   kv4_compact(refs, table, max_moves=None)  -> pairs
   kv4_copy_pages(cache, pairs)
+  prompt_attend(q, k, v, offsets, k_offsets=None, scale=None) -> out
   route_tokens(logits, k)             -> (topk_idx, topk_w)
 """
 from __future__ import annotations
@@ -51,7 +52,7 @@ EXPORTED = ("moe_pack_weights", "moe_verify_workspace_bytes", "moe_verify_layer"
             "moe_stream_read", "moe_last_error", "moe_verify_layer_noalloc", "kv4_cache_bytes", "kv4_append",
             "kv4_attend_workspace_bytes", "kv4_attend", "sample_workspace_bytes", "sample_tokens", "accept_drafts",
             "kv4_read", "kv4_reserve", "kv4_fork", "kv4_release", "kv4_compact_workspace_bytes", "kv4_compact",
-            "kv4_copy_pages", "route_tokens")
+            "kv4_copy_pages", "prompt_attend_workspace_bytes", "prompt_attend", "route_tokens")
 
 _vp, _i32, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float
 _i64, _size = ctypes.c_int64, ctypes.c_size_t
@@ -155,6 +156,11 @@ def lib() -> ctypes.CDLL:
         L.kv4_compact.restype = ctypes.c_int
         L.kv4_copy_pages.argtypes = [cp, _vp, _i32, _vp]
         L.kv4_copy_pages.restype = ctypes.c_int
+        L.prompt_attend_workspace_bytes.argtypes = [_i32, _vp, _vp, _i32, _i32, _i32, _i32]
+        L.prompt_attend_workspace_bytes.restype = _size
+        L.prompt_attend.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _f32, _vp, _vp,
+                                    _size, _vp]
+        L.prompt_attend.restype = ctypes.c_int
         L.route_tokens.argtypes = [_vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp]
         L.route_tokens.restype = ctypes.c_int
         L.moe_last_error.argtypes = []
@@ -1073,6 +1079,48 @@ def kv4_copy_pages(cache: KV4Cache, pairs, *, stream=None) -> None:
     n = pairs.shape[0] if hasattr(pairs, "shape") and len(pairs.shape) else 0
     _dense(pairs, "pairs", torch.int32, (n, 2), dev)
     _call(lib().kv4_copy_pages, dev, stream, [], ctypes.byref(c), pairs.data_ptr(), n)
+
+
+def prompt_attend(q, k, v, offsets, k_offsets=None, *, scale: Optional[float] = None, out=None, workspace=None, stream=None):
+    """Causal attention of prompts: q [T, Hq, D] over k, v [Tk, Hkv, D]
+    (float32 or bfloat16, all of one type; slices of a fused projection may
+    keep their distance between tokens), sequences packed one behind the other:
+    offsets (host) [nseq + 1] of the query rows, k_offsets of the keys (None:
+    the same).  Row j of a sequence with n rows and m keys sees its first
+    j + 1 + (m - n) keys; a row that sees none gets zeros.  scale: default
+    D ** -0.5.  Returns out [T, Hq, D] in q's type.  workspace: a uint8 device
+    tensor of prompt_attend_workspace_bytes, one per stream; None allocates."""
+    import torch
+    dtype, qs = _rows_dtype(q, "q", 3)
+    kt, ks = _rows_dtype(k, "k", 3)
+    vt, vs = _rows_dtype(v, "v", 3)
+    dev, shape = q.device, q.shape
+    T, Hq, D = shape
+    Tk, Hkv = k.shape[0], k.shape[1]
+    if kt != dtype or vt != dtype or k.device != dev or v.device != dev or k.shape[2] != D or v.shape != k.shape:
+        raise ValueError("k and v must be [Tk, Hkv, D] tensors of q's type, head size and device")
+    off = _int_array(offsets)
+    n = len(off) - 1
+    koff = off if k_offsets is None else _int_array(k_offsets, n + 1, "k_offsets")
+    if n < 1 or off[n] != T or koff[n] != Tk:
+        raise ValueError(f"offsets must run from 0 to T={T}, k_offsets to Tk={Tk}")
+    L, owned = lib(), []
+    at, kat = ctypes.addressof(off), ctypes.addressof(koff)
+    need = L.prompt_attend_workspace_bytes(n, at, kat, Hq, Hkv, D, dtype)
+    if workspace is None:
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            owned.append(workspace)
+    else:
+        _check_tensor(workspace, "workspace", ("uint8",), numel=need, device=dev, at_least=True)
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=dev)
+        owned.append(out)
+    else:
+        _dense(out, "out", q.dtype, shape, dev)
+    _call(L.prompt_attend, dev, stream, owned, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, n, at, kat, Hq, Hkv, D, dtype,
+          D ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel())
+    return out
 
 
 def route_tokens(logits, k: int, *, stream=None):

@@ -30,6 +30,34 @@ int check_pool(const moe_kv4_pool *p, PoolArgs *a) {
     return MOE_OK;
 }
 
+// Validates what prompt_attend and its workspace query share and plans the launch.
+int plan_prompt(int nseq, const int32_t *q_off, const int32_t *k_off, int Hq, int Hkv, int D, int dtype, PromptArgs *a,
+                size_t *need) {
+    if (nseq < 1 || nseq > kMaxSegments) return fail(MOE_EINVAL, "nseq=%d outside [1, %d]", nseq, kMaxSegments);
+    if (!q_off || !k_off) return fail(MOE_EINVAL, "q_off and k_off must be non-NULL");
+    for (int i = 0; i < 2; ++i) {
+        const int32_t *off = i ? k_off : q_off;
+        const int T = off[nseq];
+        if (T < 0 || T > (1 << 22)) return fail(MOE_EINVAL, "%s ends at %d, outside [0, 2^22]", i ? "k_off" : "q_off", T);
+        const int rc = check_offsets(T, nseq, off, i ? a->k_off : a->q_off);
+        if (rc != MOE_OK) return rc;
+    }
+    const int rc = check_dtype(dtype);
+    if (rc != MOE_OK) return rc;
+    if (Hkv < 1 || Hkv > 1024) return fail(MOE_EINVAL, "Hkv=%d outside [1, 1024]", Hkv);
+    if (Hq < 1 || Hq > 8192 || Hq % Hkv != 0)
+        return fail(MOE_EINVAL, "Hq=%d must be a positive multiple of Hkv=%d, at most 8192", Hq, Hkv);
+    if (D != 64 && D != 128 && D != 256) return fail(MOE_ENOTSUP, "D=%d: head sizes 64, 128 and 256 are built", D);
+    a->nseq = nseq;
+    a->Hq = Hq;
+    a->Hkv = Hkv;
+    a->G = Hq / Hkv;
+    a->D = D;
+    a->f32 = dtype == MOE_F32;
+    *need = prompt_plan(*a, device_cu_count());
+    return MOE_OK;
+}
+
 int check_list(int n) {
     if (n < 0 || n > kMaxSegments) return fail(MOE_EINVAL, "n=%d outside [0, %d]", n, kMaxSegments);
     return MOE_OK;
@@ -148,6 +176,45 @@ int kv4_copy_pages(const moe_kv4_cache *cache, const int32_t *pairs, int32_t n, 
     a.num_pages = cache->num_pages;
     a.n = n;
     return launched(launch_copy_pages(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t prompt_attend_workspace_bytes(int32_t nseq, const int32_t *q_off, const int32_t *k_off, int32_t Hq, int32_t Hkv,
+                                     int32_t D, int32_t dtype) {
+    PromptArgs a{};
+    size_t need = 0;
+    return plan_prompt(nseq, q_off, k_off, Hq, Hkv, D, dtype, &a, &need) == MOE_OK ? need : 0;
+}
+
+int prompt_attend(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                  int32_t nseq, const int32_t *q_off, const int32_t *k_off, int32_t Hq, int32_t Hkv, int32_t D,
+                  int32_t dtype, float scale, void *out, void *ws, size_t ws_bytes, void *stream) {
+    PromptArgs a{};
+    size_t need = 0;
+    int rc = plan_prompt(nseq, q_off, k_off, Hq, Hkv, D, dtype, &a, &need);
+    if (rc != MOE_OK) return rc;
+    const size_t esz = a.f32 ? 4 : 2;
+    if ((rc = check_stride("q_stride", q_stride, (int64_t)Hq * D, esz)) != MOE_OK) return rc;
+    if ((rc = check_stride("k_stride", k_stride, (int64_t)Hkv * D, esz)) != MOE_OK) return rc;
+    if ((rc = check_stride("v_stride", v_stride, (int64_t)Hkv * D, esz)) != MOE_OK) return rc;
+    if (k_stride > (1 << 24) || v_stride > (1 << 24)) return fail(MOE_ENOTSUP, "strides of k and v above 2^24 elements");
+    if (!std::isfinite(scale)) return fail(MOE_EINVAL, "scale must be finite");
+    if (a.q_off[nseq] == 0) return MOE_OK;
+    if (!q || !out) return fail(MOE_EINVAL, "q and out must be non-NULL");
+    if ((!k || !v) && a.k_off[nseq] > 0) return fail(MOE_EINVAL, "k and v must be non-NULL");
+    if (!ws && need > 0) return fail(MOE_EINVAL, "workspace is NULL");
+    if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(out, 16) || misaligned(ws, 256))
+        return fail(MOE_EINVAL, "q, k, v and out must be 16-byte, the workspace 256-byte aligned");
+    if (ws_bytes < need) return fail(MOE_EWORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.qs = q_stride;
+    a.ks = k_stride;
+    a.vs = v_stride;
+    a.out = out;
+    a.ws = ws;
+    a.scale = scale;
+    return launched(launch_prompt(a, static_cast<hipStream_t>(stream)));
 }
 
 int route_tokens(const float *logits, int64_t stride, int32_t T, int32_t E, int32_t k, int32_t *topk_idx, float *topk_w,

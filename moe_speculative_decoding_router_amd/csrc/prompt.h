@@ -62,6 +62,7 @@ struct PromptArgs {
     int parts;              // shares of a unit's keys
     int units;              // row blocks of all sequences and heads
     int blocks[kMaxSegments + 1];  // row blocks before each sequence
+    size_t part_at;  // of the shares in the workspace
 };
 // Fills the plan; returns the workspace bytes.
 size_t prompt_plan(PromptArgs &a, int n_cu);
