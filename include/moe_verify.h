@@ -516,6 +516,28 @@ int prompt_attend(const void *q, const void *k, const void *v, int64_t q_stride,
 int route_tokens(const float *logits, int64_t stride, int32_t T, int32_t E, int32_t k, int32_t *topk_idx,
                  float *topk_w, void *stream);
 
+/* The experts' products over T tokens, from choices that are made already
+ * (route_tokens', or any other):
+ *   y[t] = sum_j topk_w[t][j] FFN_{topk_idx[t][j]}(x_t) (+ shared expert)
+ * with the layer of moe_verify_layer (bf16 or fp8 weights, packed; Wr is not
+ * read).  Tokens are grouped by expert, whose weights are read once for a tile of
+ * up to 256 of them.
+ *   x     [T, H] in dtype MOE_F32 or MOE_BF16, tokens x_stride elements apart,
+ *         16-byte aligned rows
+ *   topk_idx, topk_w [T, k] i32 / f32 (device); an entry outside [0, E) names
+ *         no expert and counts for nothing; an expert named twice counts twice
+ *   y     [T, H] out in dtype, dense; may be x itself
+ *   ws    256-byte aligned, moe_experts_workspace_bytes bytes, no initialisation
+ * Sums are float32.  bf16: activations, hidden activations and each expert's output
+ * are bf16.  float32: activations and hidden activations enter the products as three
+ * bf16 terms (24 bits), outputs are float32.  An fp8 block scale of 0 or below 2^-126 counts as
+ * 2^-127.  Results do not depend on the order in which a call's workgroups run.
+ * Limits: 0 <= T <= 2^20, 1 <= k <= min(E, MOE_MAX_TOPK), E <= MOE_MAX_EXPERTS; bf16: H a multiple of 64 and I of
+ * 32; fp8: H, I multiples of 128.  Errors: EINVAL, ENOTSUP (float32 weights), EWORKSPACE. */
+size_t moe_experts_workspace_bytes(const moe_layer *layer, int32_t T, int32_t dtype);
+int moe_experts(const moe_layer *layer, const void *x, int64_t x_stride, int32_t T, int32_t dtype,
+                const int32_t *topk_idx, const float *topk_w, void *y, void *ws, size_t ws_bytes, void *stream);
+
 /* ------------------------------------------------------------------------
  * Drawing and accepting draft tokens.  Both use the filtered distribution of
  * a row of logits l [V], defined in 64 bits:

@@ -29,6 +29,7 @@ Entry points (same names as the C ABI in include/moe_verify.h):
   kv4_copy_pages(cache, pairs)
   prompt_attend(q, k, v, offsets, k_offsets=None, scale=None) -> out
   route_tokens(logits, k)             -> (topk_idx, topk_w)
+  experts(x, layer, topk_idx, topk_w) -> y
 """
 from __future__ import annotations
 
@@ -52,7 +53,8 @@ EXPORTED = ("moe_pack_weights", "moe_verify_workspace_bytes", "moe_verify_layer"
             "moe_stream_read", "moe_last_error", "moe_verify_layer_noalloc", "kv4_cache_bytes", "kv4_append",
             "kv4_attend_workspace_bytes", "kv4_attend", "sample_workspace_bytes", "sample_tokens", "accept_drafts",
             "kv4_read", "kv4_reserve", "kv4_fork", "kv4_release", "kv4_compact_workspace_bytes", "kv4_compact",
-            "kv4_copy_pages", "prompt_attend_workspace_bytes", "prompt_attend", "route_tokens")
+            "kv4_copy_pages", "prompt_attend_workspace_bytes", "prompt_attend", "route_tokens",
+            "moe_experts_workspace_bytes", "moe_experts")
 
 _vp, _i32, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float
 _i64, _size = ctypes.c_int64, ctypes.c_size_t
@@ -163,6 +165,10 @@ def lib() -> ctypes.CDLL:
         L.prompt_attend.restype = ctypes.c_int
         L.route_tokens.argtypes = [_vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp]
         L.route_tokens.restype = ctypes.c_int
+        L.moe_experts_workspace_bytes.argtypes = [ctypes.POINTER(_Layer), _i32, _i32]
+        L.moe_experts_workspace_bytes.restype = _size
+        L.moe_experts.argtypes = [ctypes.POINTER(_Layer), _vp, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _size, _vp]
+        L.moe_experts.restype = ctypes.c_int
         L.moe_last_error.argtypes = []
         L.moe_last_error.restype = ctypes.c_char_p
         _lib = L
@@ -1140,3 +1146,32 @@ def route_tokens(logits, k: int, *, stream=None):
     w = torch.empty((T, k), dtype=torch.float32, device=dev)
     _call(lib().route_tokens, dev, stream, [idx, w], logits.data_ptr(), stride, T, E, k, idx.data_ptr(), w.data_ptr())
     return idx, w
+
+
+def experts(x, layer: LayerWeights, topk_idx, topk_w, *, out=None, workspace=None, stream=None):
+    """The experts' products over any number of tokens x [T, H] (float32 or
+    bfloat16, rows may be further apart): y[t] = sum_j topk_w[t, j]
+    FFN_{topk_idx[t, j]}(x[t]), plus the shared expert's, for choices that are made
+    already (topk_idx [T, k] int32, entries outside [0, E) count for nothing;
+    topk_w [T, k] float32; route_tokens makes them from router logits).
+    layer: bf16 or fp8 weights, packed.  Returns y [T, H] in x's type.
+    workspace: a uint8 device tensor of moe_experts_workspace_bytes, one per
+    stream; None allocates."""
+    import torch
+    dtype, xs = _rows_dtype(x, "x", 2)
+    dev, (T, H) = x.device, x.shape
+    if H != layer.H:
+        raise ValueError(f"x must be [T, {layer.H}]")
+    layer.validate(dev)
+    _dense(topk_idx, "topk_idx", torch.int32, (T, layer.k), dev)
+    _dense(topk_w, "topk_w", torch.float32, (T, layer.k), dev)
+    L, owned = layer._c(), []
+    ws = _workspace(lib().moe_experts_workspace_bytes(ctypes.byref(L), T, dtype), "workspace", dev, workspace, owned)
+    if out is None:
+        out = torch.empty((T, H), dtype=x.dtype, device=dev)
+        owned.append(out)
+    else:
+        _dense(out, "out", x.dtype, (T, H), dev)
+    _call(lib().moe_experts, dev, stream, owned, ctypes.byref(L), x.data_ptr(), xs, T, dtype, topk_idx.data_ptr(), topk_w.data_ptr(),
+          out.data_ptr(), ws.data_ptr(), ws.numel())
+    return out

@@ -24,6 +24,11 @@ __device__ __forceinline__ void dma16(const void *base, unsigned offset, unsigne
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(offset), "s"(base) : "memory");
 }
 
+// The same from an address of each lane's own.
+__device__ __forceinline__ void dma16v(const void *from, unsigned at) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(from) : "memory");
+}
+
 // Waits until at most N of the wave's loads are under way.
 template <int N>
 __device__ __forceinline__ void dma_wait() {

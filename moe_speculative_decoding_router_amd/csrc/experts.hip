@@ -1,6 +1,7 @@
 // The experts of prompts: the choice of each token's experts from its router
 // logits, and the experts' products over any number of tokens.
 #include "common.h"
+#include "dma.h"
 #include "prompt.h"
 
 namespace moe {
@@ -74,7 +75,493 @@ __global__ __launch_bounds__(kRouteThreads) void route_tokens_kernel(const float
     }
 }
 
+// ---------------------------------------------------------------------------
+// The experts' products.  The (token, rank) pairs are grouped by expert (rows
+// of the products); gate-up makes the hidden activations of every row, down
+// their outputs, combine the tokens' weighted sums in rank order.
+// ---------------------------------------------------------------------------
+constexpr int kListThreads = 256;
+constexpr int kMinChunk = 4096;  // pairs of a workgroup at least
+constexpr int kMaxChunks = 256;
+
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
+
+// The workspace, and what every kernel of a call needs.
+struct Plan {
+    ExpertArgs a;
+    int pairs, rows;     // T k, and with the shared expert's
+    int chunk, chunks;   // pairs of a workgroup of the list kernels
+    int tn;              // rows of a product tile
+    int Ip;              // elements of a hidden row
+    int *counts;         // [chunks][E]
+    int *first;          // [E + 2] first row of each expert (E: the shared one)
+    int *tile;           // [E + 2] product tiles before each expert
+    int *row_token;      // [rows]
+    int *row_of;         // [pairs] row of each pair, -1 for entries that name no expert
+    __bf16 *x;           // [3][T][H] terms of float32 activations
+    __bf16 *h;           // [NT][rows][Ip] hidden activations
+    void *out;           // [rows][H] outputs
+};
+
+__global__ __launch_bounds__(kListThreads) void count_pairs_kernel(Plan p) {
+    __shared__ int n[kMaxExperts];
+    for (int e = threadIdx.x; e < p.a.E; e += kListThreads) n[e] = 0;
+    __syncthreads();
+    const int64_t end = min((int64_t)(blockIdx.x + 1) * p.chunk, (int64_t)p.pairs);
+    for (int64_t i = (int64_t)blockIdx.x * p.chunk + threadIdx.x; i < end; i += kListThreads) {
+        const int e = p.a.idx[i];
+        if (e >= 0 && e < p.a.E) atomicAdd(&n[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.a.E; e += kListThreads) p.counts[(size_t)blockIdx.x * p.a.E + e] = n[e];
+}
+
+// Places the pairs.  A row's products do not depend on where it lies in its
+// expert's list, so the order in which the atomics hand out places is free.
+__global__ __launch_bounds__(kListThreads) void place_pairs_kernel(Plan p) {
+    __shared__ int at[kMaxExperts], all[kMaxExperts], sum[2];
+    const int E = p.a.E, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    for (int e = tid; e < E; e += kListThreads) {
+        int before = 0, n = 0;
+        if (p.chunks > 1) {
+            for (int c = 0; c < p.chunks; ++c) {
+                const int v = p.counts[(size_t)c * E + e];
+                before += c < (int)blockIdx.x ? v : 0;
+                n += v;
+            }
+        }
+        at[e] = before;
+        all[e] = n;
+    }
+    __syncthreads();
+    const int64_t begin = (int64_t)blockIdx.x * p.chunk, end = min(begin + p.chunk, (int64_t)p.pairs);
+    if (p.chunks == 1) {
+        for (int64_t i = tid; i < end; i += kListThreads) {
+            const int e = p.a.idx[i];
+            if (e >= 0 && e < E) atomicAdd(&all[e], 1);
+        }
+        __syncthreads();
+    }
+    if (wave == 0) {  // first rows and tiles of the experts, 64 at a time
+        int rows = 0, tiles = 0;
+        for (int e0 = 0; e0 < E; e0 += 64) {
+            const int e = e0 + lane, n = e < E ? all[e] : 0, t = (n + p.tn - 1) / p.tn;
+            const int ri = wave_incl_scan(n), ti = wave_incl_scan(t);
+            if (e < E) {
+                at[e] += rows + ri - n;
+                if (blockIdx.x == 0) p.first[e] = rows + ri - n, p.tile[e] = tiles + ti - t;
+            }
+            rows += __builtin_amdgcn_readlane(ri, 63);
+            tiles += __builtin_amdgcn_readlane(ti, 63);
+        }
+        if (lane == 0) {
+            sum[0] = rows;
+            if (blockIdx.x == 0) {
+                const int own = p.a.shared ? p.a.T : 0;
+                p.first[E] = rows, p.tile[E] = tiles;
+                p.first[E + 1] = rows + own, p.tile[E + 1] = tiles + (own + p.tn - 1) / p.tn;
+            }
+        }
+    }
+    __syncthreads();
+    for (int64_t i = begin + tid; i < end; i += kListThreads) {
+        const int e = p.a.idx[i];
+        int r = -1;
+        if (e >= 0 && e < E) {
+            r = atomicAdd(&at[e], 1);
+            p.row_token[r] = (int)(i / p.a.k);
+        }
+        p.row_of[i] = r;
+    }
+    if (p.a.shared)
+        for (int64_t t = (int64_t)blockIdx.x * kListThreads + tid; t < p.a.T; t += (int64_t)gridDim.x * kListThreads)
+            p.row_token[sum[0] + t] = (int)t;
+}
+
+// float32 activations as three planes of bf16 terms.
+__global__ __launch_bounds__(kListThreads) void split_x_kernel(Plan p) {
+    const int64_t i = ((int64_t)blockIdx.x * kListThreads + threadIdx.x) * 4, n = (int64_t)p.a.T * p.a.H;
+    if (i >= n) return;
+    const int64_t t = i / p.a.H;
+    f32x4 v = *reinterpret_cast<const f32x4 *>((const float *)p.a.x + t * p.a.xs + (i - t * p.a.H));
+#pragma unroll
+    for (int y = 0; y < 3; ++y) {
+        bf16x4 z;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[e] = (__bf16)v[e], v[e] -= (float)z[e];
+        *reinterpret_cast<bf16x4 *>(p.x + y * n + i) = z;
+    }
+}
+
+// Rows of a tile lie in LDS as 8 chunks of 16 bytes (64 k), chunk c of row r at
+// c ^ swizzle(r), so that 16 lanes that read one chunk of 16 rows meet no bank twice.
+__device__ __forceinline__ int swizzle(int r) { return ((r >> 1) ^ ((r & 1) << 2)) & 7; }
+
+// 8 e4m3 codes as bf16, times the power of two `scale`: exact (4 significant bits).
+__device__ __forceinline__ bf16x8 decode8(unsigned lo, unsigned hi, float scale) {
+    union {
+        bf16x2v h[4];
+        bf16x8 v;
+    } o;
+    o.h[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+    o.h[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+    o.h[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+    o.h[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+    return o.v;
+}
+
+// A block scale as a power of two and a factor in [1, 2) with its sign (1 for 0).
+struct Scale {
+    float power, factor;
+};
+__device__ __forceinline__ Scale parts_of(float s) {
+    const unsigned u = __float_as_uint(s), e = u & 0x7f800000u;
+    return {__uint_as_float(e), e ? __uint_as_float((u & 0x807fffffu) | 0x3f800000u) : 1.f};
+}
+
+// Shape of a product tile: TM weight rows by TN activation rows, WM x WN waves,
+// NS buffers of 64 k; FP8 weights, NT activation terms.
+template <bool GU, bool FP8_, int NT_, int TM_, int TN_, int WM_, int WN_, int NS_, int PER_CU_>
+struct Shape {
+    static constexpr bool kGateUp = GU, FP8 = FP8_;
+    static constexpr int NT = NT_, TM = TM_, TN = TN_, WM = WM_, WN = WN_, NS = NS_, PER_CU = PER_CU_;
+    static constexpr int kThreads = 64 * WM * WN, kWaves = WM * WN;
+    static constexpr int A = TM * (FP8 ? 64 : 128), B = NT * TN * 128;  // bytes of a buffer
+    static constexpr int PA = A / 1024 / kWaves, PB = TN * 128 / 1024 / kWaves;  // loads of a wave (B: a term)
+    static constexpr int kLoads = PA + PB * NT;
+    static constexpr int MT = TM / WM / 16, NC = TN / WN / 16;  // 16 x 16 tiles of a wave
+    static constexpr int kLds = NS * (A + B);
+    static_assert(A % (1024 * kWaves) == 0 && (TN * 128) % (1024 * kWaves) == 0 && (NS - 2) * kLoads < 63 && kLds <= 163840, "");
+};
+
+template <typename S>
+__global__ __launch_bounds__(S::kThreads, S::PER_CU * S::kWaves / 4) void product_kernel(Plan p) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // [NS][A, B]
+    __shared__ int found;
+    constexpr bool GU = S::kGateUp, FP8 = S::FP8;
+    constexpr int NT = S::NT, MT = S::MT, NC = S::NC, NS = S::NS;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / S::WN, wn = wave % S::WN, g = lane >> 4, c = lane & 15;
+    const int E = p.a.E, K = GU ? p.a.H : p.a.I, M = GU ? 2 * p.a.I : p.a.H;
+    const int mblocks = (M + S::TM - 1) / S::TM;
+
+    // ---- the workgroup's tile: each XCD takes a run of neighbours, an expert's row blocks
+    // one after the other and all its tiles beside each other ----
+    const int64_t items = (int64_t)p.tile[E + 1] * mblocks, run = (items + 7) >> 3;
+    const int64_t item = (blockIdx.x & 7) * run + (blockIdx.x >> 3);
+    if ((int64_t)(blockIdx.x >> 3) >= run || item >= items) return;
+    for (int e = threadIdx.x; e <= E; e += S::kThreads)
+        if (item >= (int64_t)p.tile[e] * mblocks && item < (int64_t)p.tile[e + 1] * mblocks) found = e;
+    __syncthreads();
+    const int e = __builtin_amdgcn_readfirstlane(found);
+    const int t0 = p.tile[e], nt = p.tile[e + 1] - t0;
+    const int in = (int)(item - (int64_t)t0 * mblocks), mb = in / nt, tile = in - mb * nt;
+    const int row0 = p.first[e] + tile * S::TN, rows = min(S::TN, p.first[e + 1] - row0);
+    const bool own = e == E;  // the shared expert
+
+    // ---- loads: weights in pieces of 1 KB (16 rows x 32 or 64 k), activations of 8 rows x 64 k ----
+    const int rts = M / 16, nkt = K / (FP8 ? 64 : 32), steps = (K + 63) / 64;
+    const uint8_t *W = (const uint8_t *)(GU ? (own ? p.a.Wsh_gu : p.a.W_gu) : (own ? p.a.Wsh_d : p.a.W_d)) +
+                       (own ? 0 : (size_t)e * M * K * (FP8 ? 1 : 2));
+    const unsigned lds0 = lds_address(lds);
+    const __bf16 *brow[S::PB];
+    size_t plane = 0;
+#pragma unroll
+    for (int j = 0; j < S::PB; ++j) {
+        const int r = (wave * S::PB + j) * 8 + (lane >> 3);
+        const int row = row0 + min(r, rows - 1);  // rows behind the last are copies of it
+        if constexpr (GU) {
+            const size_t t = p.row_token[row];
+            brow[j] = NT > 1 ? p.x + t * p.a.H : (const __bf16 *)p.a.x + t * p.a.xs;
+            plane = (size_t)p.a.T * p.a.H;
+        } else {
+            brow[j] = p.h + (size_t)row * p.Ip;
+            plane = (size_t)p.rows * p.Ip;
+        }
+        brow[j] += ((lane & 7) ^ swizzle(r)) * 8;
+    }
+    auto issue = [&](int step, int buf) {
+        const unsigned at = lds0 + buf * (S::A + S::B);
+#pragma unroll
+        for (int j = 0; j < S::PA; ++j) {
+            // piece of the buffer: row tile, then its k tiles
+            const int piece = wave * S::PA + j, rt = FP8 ? piece : piece >> 1, kt = FP8 ? step : min(2 * step + (piece & 1), nkt - 1);
+            const int grt = min(mb * (S::TM / 16) + rt, rts - 1);
+            const size_t kb = GU ? (size_t)grt * nkt + kt : ((size_t)(grt >> 2) * nkt + kt) * 4 + (grt & 3);
+            dma16(W + kb * 1024, lane * 16, at + piece * 1024);
+        }
+#pragma unroll
+        for (int j = 0; j < S::PB; ++j)
+#pragma unroll
+            for (int y = 0; y < NT; ++y)
+                dma16v(brow[j] + y * plane + step * 64, at + S::A + y * (S::TN * 128) + (wave * S::PB + j) * 1024);
+    };
+
+    f32x4 acc[MT][NC];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NC; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    // fp8: scales of the block rows that this lane's operand rows and its result rows are in
+    const float *sc = nullptr;
+    size_t up = 0;  // from the gate rows' scales to the up rows'
+    if constexpr (FP8) {
+        const float *s = GU ? (own ? p.a.ssh_gu : p.a.s_gu) : (own ? p.a.ssh_d : p.a.s_d);
+        const int kbs = K / 128;
+        const int block = GU ? mb * (S::TM / 2) / 128 : min((mb * S::TM + wm * (S::TM / S::WM)) / 128, M / 128 - 1);
+        sc = s + (own ? 0 : (size_t)e * (M / 128) * kbs) + (size_t)block * kbs;
+        up = (size_t)(p.a.I / 128) * kbs;
+    }
+    float operand = 1.f, factor = 1.f;
+
+    auto compute = [&](int step, int buf) {
+        const uint8_t *A = lds + buf * (S::A + S::B), *B = A + S::A;
+        if constexpr (FP8) {
+            if ((step & 1) == 0) {  // a new block: its power of two goes into the codes, its factor into the sums
+                const Scale x = parts_of(sc[step >> 1]);
+                const Scale y = GU ? parts_of(sc[up + (step >> 1)]) : x;
+                operand = GU && c >= 8 ? y.power : x.power;
+                const float f = GU && lane >= 32 ? y.factor : x.factor;
+                if (step > 0) {
+                    const float ratio = factor / f;
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int j = 0; j < NC; ++j) acc[i][j] *= ratio;
+                }
+                factor = f;
+            }
+        }
+        u32x4 code[MT];
+        if constexpr (FP8) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i) code[i] = *reinterpret_cast<const u32x4 *>(A + (wm * MT + i) * 1024 + lane * 16);
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            if (!FP8 && !GU && 2 * step + s >= nkt) break;  // the last 32 k of an odd number
+            const int ch = FP8 ? 2 * g + s : 4 * s + g;
+            bf16x8 b[NT][NC], a[MT];
+#pragma unroll
+            for (int y = 0; y < NT; ++y)
+#pragma unroll
+                for (int j = 0; j < NC; ++j) {
+                    const int r = (wn * NC + j) * 16 + c;
+                    b[y][j] = *reinterpret_cast<const bf16x8 *>(B + y * (S::TN * 128) + r * 128 + ((ch ^ swizzle(c)) << 4));
+                }
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                if constexpr (FP8) a[i] = decode8(code[i][2 * s], code[i][2 * s + 1], operand);
+                else a[i] = *reinterpret_cast<const bf16x8 *>(A + ((wm * MT + i) * 2 + s) * 1024 + lane * 16);
+            }
+#pragma unroll
+            for (int y = NT - 1; y >= 0; --y)  // the smaller terms first
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < NC; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[y][j], acc[i][j], 0, 0, 0);
+        }
+    };
+
+#pragma unroll
+    for (int i = 0; i < NS - 1; ++i)
+        if (i < steps) issue(i, i);
+    int buf = 0, put = NS - 1;
+    for (int st = 0; st < steps; ++st) {
+        if (st + NS - 2 < steps) dma_wait<(NS - 2) * S::kLoads>();  // of the buffers behind this one
+        else dma_wait<0>();
+        dma_barrier();  // this buffer is there, and the one before was read by all
+        if (st + NS - 1 < steps) issue(st + NS - 1, put);
+        compute(st, buf);
+        buf = buf + 1 == NS ? 0 : buf + 1;
+        put = put + 1 == NS ? 0 : put + 1;
+    }
+
+    // ---- results: lane (g, c) holds weight rows 4 g .. 4 g + 3 of its tiles for activation row c ----
+    if constexpr (FP8) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NC; ++j) acc[i][j] *= factor;
+    }
+    const int rt0 = mb * (S::TM / 16) + wm * MT;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+        const int r = (wn * NC + j) * 16 + c;
+        if constexpr (GU) {
+            // a row tile is 8 gate rows (lanes below 32) and the same 8 up rows; two tiles exchange
+            // halves, so that every lane holds both of one element
+#pragma unroll
+            for (int i = 0; i < MT; i += 2) {
+                float hid[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const unsigned a0 = __float_as_uint(acc[i][j][x]), a1 = __float_as_uint(acc[MT > 1 ? i + 1 : i][j][x]);
+                    const auto sw = __builtin_amdgcn_permlane32_swap(a0, a1, false, false);
+                    const float gate = __uint_as_float(sw[0]), u = __uint_as_float(sw[1]);
+                    hid[x] = gate / (1.f + __expf(-gate)) * u;
+                }
+                const int rt = rt0 + i + (lane >> 5);
+                if (r < rows && rt < rts && (MT > 1 || lane < 32)) {
+                    __bf16 *to = p.h + (size_t)(row0 + r) * p.Ip + rt * 8 + 4 * (g & 1);
+#pragma unroll
+                    for (int y = 0; y < NT; ++y) {
+                        bf16x4 z;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) z[x] = (__bf16)hid[x], hid[x] -= (float)z[x];
+                        *reinterpret_cast<bf16x4 *>(to + (size_t)y * p.rows * p.Ip) = z;
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                if (r >= rows || rt0 + i >= rts) continue;
+                const size_t at = (size_t)(row0 + r) * p.a.H + (rt0 + i) * 16 + 4 * g;
+                if constexpr (NT > 1) {
+                    *reinterpret_cast<f32x4 *>((float *)p.out + at) = acc[i][j];
+                } else {
+                    const bf16x4 z = {(__bf16)acc[i][j][0], (__bf16)acc[i][j][1], (__bf16)acc[i][j][2], (__bf16)acc[i][j][3]};
+                    *reinterpret_cast<bf16x4 *>((__bf16 *)p.out + at) = z;
+                }
+            }
+        }
+    }
+}
+
+// y[t] = sum of the token's rows in rank order, times their weights, and of the
+// shared expert's.  8 elements a thread.
+template <bool F32>
+__global__ __launch_bounds__(kListThreads) void combine_rows_kernel(Plan p) {
+    const int t = blockIdx.x, H = p.a.H;
+    const int own = p.a.shared ? p.first[p.a.E] + t : -1;
+    for (int i = (blockIdx.y * kListThreads + threadIdx.x) * 8; i < H; i += gridDim.y * kListThreads * 8) {
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = 0.f;
+        auto add = [&](int row, float w) {
+            if constexpr (F32) {
+                const f32x4 *v = reinterpret_cast<const f32x4 *>((const float *)p.out + (size_t)row * H + i);
+                const f32x4 a = v[0], b = v[1];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = fmaf(w, a[e], y[e]), y[4 + e] = fmaf(w, b[e], y[4 + e]);
+            } else {
+                const bf16x8 v = *reinterpret_cast<const bf16x8 *>((const __bf16 *)p.out + (size_t)row * H + i);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = fmaf(w, (float)v[e], y[e]);
+            }
+        };
+        for (int j = 0; j < p.a.k; ++j) {
+            const int row = p.row_of[(size_t)t * p.a.k + j];
+            if (row >= 0) add(row, p.a.w[(size_t)t * p.a.k + j]);
+        }
+        if (own >= 0) add(own, 1.f);
+        if constexpr (F32) {
+            f32x4 *d = reinterpret_cast<f32x4 *>((float *)p.a.y + (size_t)t * H + i);
+            d[0] = f32x4{y[0], y[1], y[2], y[3]};
+            d[1] = f32x4{y[4], y[5], y[6], y[7]};
+        } else {
+            bf16x8 z;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = (__bf16)y[e];
+            *reinterpret_cast<bf16x8 *>((__bf16 *)p.a.y + (size_t)t * H + i) = z;
+        }
+    }
+}
+
+template <typename S>
+hipError_t launch_product(const Plan &p, hipStream_t s) {
+    if (S::kLds > 65536) {
+        const hipError_t e = allow_lds<product_kernel<S>>(S::kLds);
+        if (e != hipSuccess) return e;
+    }
+    const int64_t M = S::kGateUp ? 2 * p.a.I : p.a.H, mblocks = (M + S::TM - 1) / S::TM;
+    // tiles at most: every used expert's last one is filled in part
+    const int64_t used = p.a.E < p.pairs ? p.a.E : p.pairs;
+    const int64_t tiles = p.pairs / S::TN + used + (p.a.shared ? (p.a.T + S::TN - 1) / S::TN : 0);
+    const int64_t grid = (tiles * mblocks + 7) / 8 * 8;
+    hipLaunchKernelGGL(product_kernel<S>, dim3((unsigned)grid), dim3(S::kThreads), S::kLds, s, p);
+    return hipGetLastError();
+}
+
+template <bool FP8, int NT, int TM, int TN, int WM, int WN, int NS, int PER_CU>
+hipError_t launch_both(const Plan &p, hipStream_t s) {
+    const hipError_t e = launch_product<Shape<true, FP8, NT, TM, TN, WM, WN, NS, PER_CU>>(p, s);
+    if (e != hipSuccess) return e;
+    return launch_product<Shape<false, FP8, NT, TM, TN, WM, WN, NS, PER_CU>>(p, s);
+}
+
+template <bool FP8>
+hipError_t launch_products(const Plan &p, hipStream_t s) {
+    if (p.a.f32) {
+        if (p.tn == 32) return launch_both<FP8, 3, 64, 32, 4, 1, 3, 1>(p, s);
+        return launch_both<FP8, 3, 128, 128, 2, 4, 2, 1>(p, s);
+    }
+    if (p.tn == 32) return launch_both<FP8, 1, 64, 32, 4, 1, 4, 2>(p, s);
+    if (p.tn == 128) return launch_both<FP8, 1, 256, 128, 4, 2, 3, 1>(p, s);
+    return launch_both<FP8, 1, 256, 256, 2, 4, 2, 1>(p, s);
+}
+
+// Rows of a product tile, by the rows that an expert has on average.
+int tile_rows(const ExpertArgs &a) {
+    const int64_t avg = (int64_t)a.T * a.k / a.E;
+    if (a.f32) return avg <= 48 ? 32 : 128;
+    return avg <= 48 ? 32 : avg <= 256 ? 128 : 256;
+}
+
+size_t lay_out(const ExpertArgs &a, uint8_t *ws, Plan *p) {
+    Plan q{};
+    q.a = a;
+    q.pairs = a.T * a.k;
+    q.rows = q.pairs + (a.shared ? a.T : 0);
+    q.chunk = (q.pairs + kMaxChunks - 1) / kMaxChunks;
+    if (q.chunk < kMinChunk) q.chunk = kMinChunk;
+    q.chunks = (q.pairs + q.chunk - 1) / q.chunk;
+    q.tn = tile_rows(a);
+    q.Ip = (a.I + 63) / 64 * 64;
+    const int NT = a.f32 ? 3 : 1;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        uint8_t *at = ws + off;
+        off += (bytes + 255) & ~(size_t)255;
+        return at;
+    };
+    q.counts = (int *)take((size_t)q.chunks * a.E * 4);
+    q.first = (int *)take((a.E + 2) * 4);
+    q.tile = (int *)take((a.E + 2) * 4);
+    q.row_token = (int *)take((size_t)q.rows * 4);
+    q.row_of = (int *)take((size_t)q.pairs * 4);
+    q.x = (__bf16 *)take(a.f32 ? (size_t)a.T * a.H * 6 : 0);
+    q.h = (__bf16 *)take((size_t)NT * q.rows * q.Ip * 2);
+    q.out = take((size_t)q.rows * a.H * (a.f32 ? 4 : 2));
+    if (p) *p = q;
+    return off;
+}
+
 }  // namespace
+
+size_t experts_ws_bytes(const ExpertArgs &a) { return lay_out(a, nullptr, nullptr); }
+
+hipError_t launch_experts(const ExpertArgs &a, hipStream_t s) {
+    Plan p;
+    lay_out(a, (uint8_t *)a.ws, &p);
+    if (p.chunks > 1) hipLaunchKernelGGL(count_pairs_kernel, dim3(p.chunks), dim3(kListThreads), 0, s, p);
+    hipLaunchKernelGGL(place_pairs_kernel, dim3(p.chunks), dim3(kListThreads), 0, s, p);
+    if (a.f32) {
+        const int64_t n = ((int64_t)a.T * a.H / 4 + kListThreads - 1) / kListThreads;
+        hipLaunchKernelGGL(split_x_kernel, dim3((unsigned)n), dim3(kListThreads), 0, s, p);
+    }
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess) e = a.fp8 ? launch_products<true>(p, s) : launch_products<false>(p, s);
+    if (e != hipSuccess) return e;
+    const dim3 grid(a.T, (a.H + kListThreads * 8 - 1) / (kListThreads * 8));
+    if (a.f32) hipLaunchKernelGGL(combine_rows_kernel<true>, grid, dim3(kListThreads), 0, s, p);
+    else hipLaunchKernelGGL(combine_rows_kernel<false>, grid, dim3(kListThreads), 0, s, p);
+    return hipGetLastError();
+}
 
 hipError_t launch_route_tokens(const float *logits, int64_t stride, int T, int E, int k, int32_t *idx, float *w,
                                hipStream_t s) {

@@ -58,6 +58,33 @@ int plan_prompt(int nseq, const int32_t *q_off, const int32_t *k_off, int Hq, in
     return MOE_OK;
 }
 
+// Validates what moe_experts and its workspace query share.
+int check_experts(const moe_layer *L, int T, int dtype, ExpertArgs *a) {
+    size_t need = 0;
+    int rc = verify_needs(L, 1, nullptr, &need);  // the layer's own checks
+    if (rc == MOE_OK) rc = check_dtype(dtype);
+    if (rc != MOE_OK) return rc;
+    if (L->wdtype == MOE_F32) return fail(MOE_ENOTSUP, "float32 weights: bf16 and fp8 are built");
+    if (T < 0 || T > (1 << 20)) return fail(MOE_EINVAL, "T=%d outside [0, 2^20]", T);
+    a->T = T;
+    a->H = L->H;
+    a->I = L->I;
+    a->E = L->E;
+    a->k = L->k;
+    a->fp8 = L->wdtype == MOE_FP8_E4M3;
+    a->f32 = dtype == MOE_F32;
+    a->shared = L->Wsh_gu != nullptr;
+    a->W_gu = L->W_gu;
+    a->W_d = L->W_d;
+    a->Wsh_gu = L->Wsh_gu;
+    a->Wsh_d = L->Wsh_d;
+    a->s_gu = L->s_gu;
+    a->s_d = L->s_d;
+    a->ssh_gu = L->ssh_gu;
+    a->ssh_d = L->ssh_d;
+    return MOE_OK;
+}
+
 int check_list(int n) {
     if (n < 0 || n > kMaxSegments) return fail(MOE_EINVAL, "n=%d outside [0, %d]", n, kMaxSegments);
     return MOE_OK;
@@ -226,6 +253,34 @@ int route_tokens(const float *logits, int64_t stride, int32_t T, int32_t E, int3
     if (T == 0) return MOE_OK;
     if (!logits || !topk_idx || !topk_w) return fail(MOE_EINVAL, "logits, topk_idx and topk_w must be non-NULL");
     return launched(launch_route_tokens(logits, stride, T, E, k, topk_idx, topk_w, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_experts_workspace_bytes(const moe_layer *layer, int32_t T, int32_t dtype) {
+    ExpertArgs a{};
+    return check_experts(layer, T, dtype, &a) == MOE_OK ? experts_ws_bytes(a) : 0;
+}
+
+int moe_experts(const moe_layer *layer, const void *x, int64_t x_stride, int32_t T, int32_t dtype,
+                const int32_t *topk_idx, const float *topk_w, void *y, void *ws, size_t ws_bytes, void *stream) {
+    ExpertArgs a{};
+    int rc = check_experts(layer, T, dtype, &a);
+    if (rc != MOE_OK) return rc;
+    if ((rc = check_stride("x_stride", x_stride, a.H, a.f32 ? 4 : 2)) != MOE_OK) return rc;
+    if (T == 0) return MOE_OK;
+    if (!x || !topk_idx || !topk_w || !y || !ws) return fail(MOE_EINVAL, "x, topk_idx, topk_w, y and the workspace must be non-NULL");
+    if (misaligned(x, 16) || misaligned(y, 16) || misaligned(ws, 256))
+        return fail(MOE_EINVAL, "x and y must be 16-byte, the workspace 256-byte aligned");
+    if (misaligned(a.W_gu, 16) || misaligned(a.W_d, 16) || misaligned(a.Wsh_gu, 16) || misaligned(a.Wsh_d, 16))
+        return fail(MOE_EINVAL, "weights must be 16-byte aligned");
+    const size_t need = experts_ws_bytes(a);
+    if (ws_bytes < need) return fail(MOE_EWORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+    a.x = x;
+    a.xs = x_stride;
+    a.idx = topk_idx;
+    a.w = topk_w;
+    a.y = y;
+    a.ws = ws;
+    return launched(launch_experts(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -85,6 +85,6 @@ struct ExpertArgs {
     void *ws;
 };
 size_t experts_ws_bytes(const ExpertArgs &a);
-hipError_t launch_experts(const ExpertArgs &a, int n_cu, hipStream_t s);
+hipError_t launch_experts(const ExpertArgs &a, hipStream_t s);
 
 }  // namespace moe
