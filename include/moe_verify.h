@@ -528,9 +528,9 @@ int route_tokens(const float *logits, int64_t stride, int32_t T, int32_t E, int3
  *         no expert and counts for nothing; an expert named twice counts twice
  *   y     [T, H] out in dtype, dense; may be x itself
  *   ws    256-byte aligned, moe_experts_workspace_bytes bytes, no initialisation
- * Sums are float32.  bf16: activations, hidden activations and each expert's output
- * are bf16.  float32: activations and hidden activations enter the products as three
- * bf16 terms (24 bits), outputs are float32.  An fp8 block scale of 0 or below 2^-126 counts as
+ * Sums and each expert's outputs are float32.  bf16: hidden activations enter
+ * the second product rounded to bf16.  float32: activations and hidden
+ * activations enter the products as three bf16 terms (24 bits).  An fp8 block scale of 0 or below 2^-126 counts as
  * 2^-127.  Results do not depend on the order in which a call's workgroups run.
  * Limits: 0 <= T <= 2^20, 1 <= k <= min(E, MOE_MAX_TOPK), E <= MOE_MAX_EXPERTS; bf16: H a multiple of 64 and I of
  * 32; fp8: H, I multiples of 128.  Errors: EINVAL, ENOTSUP (float32 weights), EWORKSPACE. */

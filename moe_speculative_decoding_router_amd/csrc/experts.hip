@@ -101,7 +101,7 @@ struct Plan {
     int *row_of;         // [pairs] row of each pair, -1 for entries that name no expert
     __bf16 *x;           // [3][T][H] terms of float32 activations
     __bf16 *h;           // [NT][rows][Ip] hidden activations
-    void *out;           // [rows][H] outputs
+    float *out;          // [rows][H] outputs
 };
 
 __global__ __launch_bounds__(kListThreads) void count_pairs_kernel(Plan p) {
@@ -421,12 +421,7 @@ __global__ __launch_bounds__(S::kThreads, S::PER_CU * S::kWaves / 4) void produc
             for (int i = 0; i < MT; ++i) {
                 if (r >= rows || rt0 + i >= rts) continue;
                 const size_t at = (size_t)(row0 + r) * p.a.H + (rt0 + i) * 16 + 4 * g;
-                if constexpr (NT > 1) {
-                    *reinterpret_cast<f32x4 *>((float *)p.out + at) = acc[i][j];
-                } else {
-                    const bf16x4 z = {(__bf16)acc[i][j][0], (__bf16)acc[i][j][1], (__bf16)acc[i][j][2], (__bf16)acc[i][j][3]};
-                    *reinterpret_cast<bf16x4 *>((__bf16 *)p.out + at) = z;
-                }
+                *reinterpret_cast<f32x4 *>(p.out + at) = acc[i][j];
             }
         }
     }
@@ -443,16 +438,10 @@ __global__ __launch_bounds__(kListThreads) void combine_rows_kernel(Plan p) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = 0.f;
         auto add = [&](int row, float w) {
-            if constexpr (F32) {
-                const f32x4 *v = reinterpret_cast<const f32x4 *>((const float *)p.out + (size_t)row * H + i);
-                const f32x4 a = v[0], b = v[1];
+            const f32x4 *v = reinterpret_cast<const f32x4 *>(p.out + (size_t)row * H + i);
+            const f32x4 a = v[0], b = v[1];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = fmaf(w, a[e], y[e]), y[4 + e] = fmaf(w, b[e], y[4 + e]);
-            } else {
-                const bf16x8 v = *reinterpret_cast<const bf16x8 *>((const __bf16 *)p.out + (size_t)row * H + i);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = fmaf(w, (float)v[e], y[e]);
-            }
+            for (int e = 0; e < 4; ++e) y[e] = fmaf(w, a[e], y[e]), y[4 + e] = fmaf(w, b[e], y[4 + e]);
         };
         for (int j = 0; j < p.a.k; ++j) {
             const int row = p.row_of[(size_t)t * p.a.k + j];
@@ -536,7 +525,7 @@ size_t lay_out(const ExpertArgs &a, uint8_t *ws, Plan *p) {
     q.row_of = (int *)take((size_t)q.pairs * 4);
     q.x = (__bf16 *)take(a.f32 ? (size_t)a.T * a.H * 6 : 0);
     q.h = (__bf16 *)take((size_t)NT * q.rows * q.Ip * 2);
-    q.out = take((size_t)q.rows * a.H * (a.f32 ? 4 : 2));
+    q.out = (float *)take((size_t)q.rows * a.H * 4);
     if (p) *p = q;
     return off;
 }
