@@ -221,163 +221,177 @@ __device__ __forceinline__ Scale parts_of(float s) {
 }
 
 // Shape of a product tile: TM weight rows by TN activation rows, WM x WN waves,
-// NS buffers of 64 k; FP8 weights, NT activation terms.
-template <bool GU, bool FP8_, int NT_, int TM_, int TN_, int WM_, int WN_, int NS_, int PER_CU_>
+// FP8 weights, NT activation terms.  A wave's columns are 16 of every 16 WN
+// activation rows, so that a tile with few rows costs all waves less; the loop
+// is compiled for each number JN of such steps, with as many buffers of 64 k as
+// LDS holds.
+template <bool GU, bool FP8_, int NT_, int TM_, int TN_, int WM_, int WN_, int LDS_>
 struct Shape {
     static constexpr bool kGateUp = GU, FP8 = FP8_;
-    static constexpr int NT = NT_, TM = TM_, TN = TN_, WM = WM_, WN = WN_, NS = NS_, PER_CU = PER_CU_;
-    static constexpr int kThreads = 64 * WM * WN, kWaves = WM * WN;
-    static constexpr int A = TM * (FP8 ? 64 : 128), B = NT * TN * 128;  // bytes of a buffer
-    static constexpr int PA = A / 1024 / kWaves, PB = TN * 128 / 1024 / kWaves;  // loads of a wave (B: a term)
-    static constexpr int kLoads = PA + PB * NT;
-    static constexpr int MT = TM / WM / 16, NC = TN / WN / 16;  // 16 x 16 tiles of a wave
-    static constexpr int kLds = NS * (A + B);
-    static_assert(A % (1024 * kWaves) == 0 && (TN * 128) % (1024 * kWaves) == 0 && (NS - 2) * kLoads < 63 && kLds <= 163840, "");
+    static constexpr int NT = NT_, TM = TM_, TN = TN_, WM = WM_, WN = WN_, kLds = LDS_;
+    static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+    static constexpr int kStep = 16 * WN;  // activation rows of a step
+    static constexpr int A = TM * (FP8 ? 64 : 128);  // bytes of a buffer
+    static constexpr int PA = A / 1024 / kWaves;     // loads of a wave
+    static constexpr int MT = TM / WM / 16, NC = TN / kStep;  // 16 x 16 tiles of a wave
+    // loads of a wave for an activation term, 8 rows each: every wave has as many, so that
+    // their counts tell which buffers are there
+    static constexpr int PB(int jn) { return (jn * kStep + 8 * kWaves - 1) / (8 * kWaves); }
+    static constexpr int B(int jn) { return NT * PB(jn) * kWaves * 1024; }
+    static constexpr int NS(int jn) {
+        const int n = LDS_ / (A + B(jn));
+        return n > 4 ? 4 : n;
+    }
+    static_assert(A % (1024 * kWaves) == 0 && NS(NC) >= 2 && LDS_ <= 163328, "");
 };
 
-template <typename S>
-__global__ __launch_bounds__(S::kThreads, S::PER_CU * S::kWaves / 4) void product_kernel(Plan p) {
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // [NS][A, B]
-    __shared__ int found;
+// What a workgroup works on.
+struct Job {
+    const uint8_t *W;
+    const float *sc, *sc_up;  // fp8: scales of the result rows (gate-up: of the gate rows and the up rows)
+    int mb, row0, rows, M, K;
+};
+
+// A wave's operands of one step of 32 k.
+template <typename S, int JN>
+struct Frags {
+    typedef unsigned u32xa __attribute__((ext_vector_type(S::FP8 ? 2 : 4)));
+    u32xa a[S::MT];
+    bf16x8 b[S::NT][JN];
+};
+
+template <typename S, int JN>
+__device__ __forceinline__ void multiply(const Plan &p, const Job &job, uint8_t *lds) {
     constexpr bool GU = S::kGateUp, FP8 = S::FP8;
-    constexpr int NT = S::NT, MT = S::MT, NC = S::NC, NS = S::NS;
+    constexpr int NT = S::NT, MT = S::MT, NS = S::NS(JN), PA = S::PA, PB = S::PB(JN), kLoads = PA + PB * NT;
+    constexpr int kPlane = PB * S::kWaves * 1024, kBuffer = S::A + NT * kPlane;
+    static_assert((NS - 2) * kLoads < 63, "");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / S::WN, wn = wave % S::WN, g = lane >> 4, c = lane & 15;
-    const int E = p.a.E, K = GU ? p.a.H : p.a.I, M = GU ? 2 * p.a.I : p.a.H;
-    const int mblocks = (M + S::TM - 1) / S::TM;
-
-    // ---- the workgroup's tile: each XCD takes a run of neighbours, an expert's row blocks
-    // one after the other and all its tiles beside each other ----
-    const int64_t items = (int64_t)p.tile[E + 1] * mblocks, run = (items + 7) >> 3;
-    const int64_t item = (blockIdx.x & 7) * run + (blockIdx.x >> 3);
-    if ((int64_t)(blockIdx.x >> 3) >= run || item >= items) return;
-    for (int e = threadIdx.x; e <= E; e += S::kThreads)
-        if (item >= (int64_t)p.tile[e] * mblocks && item < (int64_t)p.tile[e + 1] * mblocks) found = e;
-    __syncthreads();
-    const int e = __builtin_amdgcn_readfirstlane(found);
-    const int t0 = p.tile[e], nt = p.tile[e + 1] - t0;
-    const int in = (int)(item - (int64_t)t0 * mblocks), mb = in / nt, tile = in - mb * nt;
-    const int row0 = p.first[e] + tile * S::TN, rows = min(S::TN, p.first[e + 1] - row0);
-    const bool own = e == E;  // the shared expert
+    const int K = job.K;
 
     // ---- loads: weights in pieces of 1 KB (16 rows x 32 or 64 k), activations of 8 rows x 64 k ----
-    const int rts = M / 16, nkt = K / (FP8 ? 64 : 32), steps = (K + 63) / 64;
-    const uint8_t *W = (const uint8_t *)(GU ? (own ? p.a.Wsh_gu : p.a.W_gu) : (own ? p.a.Wsh_d : p.a.W_d)) +
-                       (own ? 0 : (size_t)e * M * K * (FP8 ? 1 : 2));
+    const int rts = job.M / 16, nkt = K / (FP8 ? 64 : 32), steps = (K + 63) / 64;
     const unsigned lds0 = lds_address(lds);
-    const __bf16 *brow[S::PB];
-    size_t plane = 0;
+    const __bf16 *brow[PB];
+    const size_t plane = GU ? (size_t)p.a.T * p.a.H : (size_t)p.rows * p.Ip;
 #pragma unroll
-    for (int j = 0; j < S::PB; ++j) {
-        const int r = (wave * S::PB + j) * 8 + (lane >> 3);
-        const int row = row0 + min(r, rows - 1);  // rows behind the last are copies of it
+    for (int j = 0; j < PB; ++j) {
+        const int r = (j * S::kWaves + wave) * 8 + (lane >> 3);
+        const int row = job.row0 + min(r, job.rows - 1);  // rows behind the last are copies of it
         if constexpr (GU) {
             const size_t t = p.row_token[row];
             brow[j] = NT > 1 ? p.x + t * p.a.H : (const __bf16 *)p.a.x + t * p.a.xs;
-            plane = (size_t)p.a.T * p.a.H;
         } else {
             brow[j] = p.h + (size_t)row * p.Ip;
-            plane = (size_t)p.rows * p.Ip;
         }
         brow[j] += ((lane & 7) ^ swizzle(r)) * 8;
     }
     auto issue = [&](int step, int buf) {
-        const unsigned at = lds0 + buf * (S::A + S::B);
+        const unsigned at = lds0 + buf * kBuffer;
 #pragma unroll
-        for (int j = 0; j < S::PA; ++j) {
+        for (int j = 0; j < PA; ++j) {
             // piece of the buffer: row tile, then its k tiles
-            const int piece = wave * S::PA + j, rt = FP8 ? piece : piece >> 1, kt = FP8 ? step : min(2 * step + (piece & 1), nkt - 1);
-            const int grt = min(mb * (S::TM / 16) + rt, rts - 1);
+            const int piece = wave * PA + j, rt = FP8 ? piece : piece >> 1, kt = FP8 ? step : min(2 * step + (piece & 1), nkt - 1);
+            const int grt = min(job.mb * (S::TM / 16) + rt, rts - 1);
             const size_t kb = GU ? (size_t)grt * nkt + kt : ((size_t)(grt >> 2) * nkt + kt) * 4 + (grt & 3);
-            dma16(W + kb * 1024, lane * 16, at + piece * 1024);
+            dma16(job.W + kb * 1024, lane * 16, at + piece * 1024);
         }
 #pragma unroll
-        for (int j = 0; j < S::PB; ++j)
+        for (int j = 0; j < PB; ++j)
 #pragma unroll
             for (int y = 0; y < NT; ++y)
-                dma16v(brow[j] + y * plane + step * 64, at + S::A + y * (S::TN * 128) + (wave * S::PB + j) * 1024);
+                dma16v(brow[j] + y * plane + step * 64, at + S::A + y * kPlane + (j * S::kWaves + wave) * 1024);
     };
 
-    f32x4 acc[MT][NC];
+    f32x4 acc[MT][JN];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < NC; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < JN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    // fp8: scales of the block rows that this lane's operand rows and its result rows are in
-    const float *sc = nullptr;
-    size_t up = 0;  // from the gate rows' scales to the up rows'
-    if constexpr (FP8) {
-        const float *s = GU ? (own ? p.a.ssh_gu : p.a.s_gu) : (own ? p.a.ssh_d : p.a.s_d);
-        const int kbs = K / 128;
-        const int block = GU ? mb * (S::TM / 2) / 128 : min((mb * S::TM + wm * (S::TM / S::WM)) / 128, M / 128 - 1);
-        sc = s + (own ? 0 : (size_t)e * (M / 128) * kbs) + (size_t)block * kbs;
-        up = (size_t)(p.a.I / 128) * kbs;
-    }
+    typedef Frags<S, JN> F;
+    auto read = [&](F &f, int buf, int s) {
+        const uint8_t *A = lds + buf * kBuffer, *B = A + S::A;
+        const int ch = FP8 ? 2 * g + s : 4 * s + g;
+#pragma unroll
+        for (int y = 0; y < NT; ++y)
+#pragma unroll
+            for (int j = 0; j < JN; ++j)
+                f.b[y][j] = *reinterpret_cast<const bf16x8 *>(B + y * kPlane + ((j * S::WN + wn) * 16 + c) * 128 + ((ch ^ swizzle(c)) << 4));
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const uint8_t *at = FP8 ? A + (wm * MT + i) * 1024 + lane * 16 + 8 * s : A + ((wm * MT + i) * 2 + s) * 1024 + lane * 16;
+            f.a[i] = *reinterpret_cast<const typename F::u32xa *>(at);
+        }
+    };
     float operand = 1.f, factor = 1.f;
+    auto product = [&](const F &f) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            bf16x8 a;
+            if constexpr (FP8) a = decode8(f.a[i][0], f.a[i][1], operand);
+            else a = __builtin_bit_cast(bf16x8, f.a[i]);
+#pragma unroll
+            for (int y = NT - 1; y >= 0; --y)  // the smaller terms first
+#pragma unroll
+                for (int j = 0; j < JN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, f.b[y][j], acc[i][j], 0, 0, 0);
+        }
+    };
+    // the reads of the next step among the products of this one
+    auto mix = [&]() {
+        constexpr int reads = MT + NT * JN, products = MT * NT * JN, each = products / reads > 0 ? products / reads : 1;
+#pragma unroll
+        for (int i = 0; i < reads; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x8, each, 0);
+        }
+        if (products > reads * each) __builtin_amdgcn_sched_group_barrier(0x8, products - reads * each, 0);
+    };
 
-    auto compute = [&](int step, int buf) {
-        const uint8_t *A = lds + buf * (S::A + S::B), *B = A + S::A;
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+        if (i < steps) issue(i, i);
+    if (NS - 1 < steps) dma_wait<(NS - 1) * kLoads>();
+    else dma_wait<0>();
+    dma_barrier();
+    F f0, f1;
+    read(f0, 0, 0);
+    int buf = 0;
+    for (int st = 0; st < steps; ++st) {
         if constexpr (FP8) {
-            if ((step & 1) == 0) {  // a new block: its power of two goes into the codes, its factor into the sums
-                const Scale x = parts_of(sc[step >> 1]);
-                const Scale y = GU ? parts_of(sc[up + (step >> 1)]) : x;
+            if ((st & 1) == 0) {  // a new block: its power of two goes into the codes, its factor into the sums
+                const Scale x = parts_of(job.sc[st >> 1]);
+                const Scale y = GU ? parts_of(job.sc_up[st >> 1]) : x;
                 operand = GU && c >= 8 ? y.power : x.power;
                 const float f = GU && lane >= 32 ? y.factor : x.factor;
-                if (step > 0) {
+                if (st > 0) {
                     const float ratio = factor / f;
 #pragma unroll
                     for (int i = 0; i < MT; ++i)
 #pragma unroll
-                        for (int j = 0; j < NC; ++j) acc[i][j] *= ratio;
+                        for (int j = 0; j < JN; ++j) acc[i][j] *= ratio;
                 }
                 factor = f;
             }
         }
-        u32x4 code[MT];
-        if constexpr (FP8) {
-#pragma unroll
-            for (int i = 0; i < MT; ++i) code[i] = *reinterpret_cast<const u32x4 *>(A + (wm * MT + i) * 1024 + lane * 16);
+        read(f1, buf, 1);
+        product(f0);
+        mix();
+        const int next = buf + 1 == NS ? 0 : buf + 1;
+        if (st + 1 < steps) {
+            // the next buffer is there, and this one was read by all
+            if (st + NS - 1 < steps) dma_wait<(NS - 2) * kLoads>();
+            else dma_wait<0>();
+            dma_barrier();
+            if (st + NS < steps) issue(st + NS, buf);
+            read(f0, next, 0);
         }
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            if (!FP8 && !GU && 2 * step + s >= nkt) break;  // the last 32 k of an odd number
-            const int ch = FP8 ? 2 * g + s : 4 * s + g;
-            bf16x8 b[NT][NC], a[MT];
-#pragma unroll
-            for (int y = 0; y < NT; ++y)
-#pragma unroll
-                for (int j = 0; j < NC; ++j) {
-                    const int r = (wn * NC + j) * 16 + c;
-                    b[y][j] = *reinterpret_cast<const bf16x8 *>(B + y * (S::TN * 128) + r * 128 + ((ch ^ swizzle(c)) << 4));
-                }
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                if constexpr (FP8) a[i] = decode8(code[i][2 * s], code[i][2 * s + 1], operand);
-                else a[i] = *reinterpret_cast<const bf16x8 *>(A + ((wm * MT + i) * 2 + s) * 1024 + lane * 16);
-            }
-#pragma unroll
-            for (int y = NT - 1; y >= 0; --y)  // the smaller terms first
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int j = 0; j < NC; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[y][j], acc[i][j], 0, 0, 0);
+        if (FP8 || GU || 2 * st + 1 < nkt) {  // else the last 32 k of an odd number
+            product(f1);
+            mix();
         }
-    };
-
-#pragma unroll
-    for (int i = 0; i < NS - 1; ++i)
-        if (i < steps) issue(i, i);
-    int buf = 0, put = NS - 1;
-    for (int st = 0; st < steps; ++st) {
-        if (st + NS - 2 < steps) dma_wait<(NS - 2) * S::kLoads>();  // of the buffers behind this one
-        else dma_wait<0>();
-        dma_barrier();  // this buffer is there, and the one before was read by all
-        if (st + NS - 1 < steps) issue(st + NS - 1, put);
-        compute(st, buf);
-        buf = buf + 1 == NS ? 0 : buf + 1;
-        put = put + 1 == NS ? 0 : put + 1;
+        buf = next;
     }
 
     // ---- results: lane (g, c) holds weight rows 4 g .. 4 g + 3 of its tiles for activation row c ----
@@ -385,12 +399,12 @@ __global__ __launch_bounds__(S::kThreads, S::PER_CU * S::kWaves / 4) void produc
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int j = 0; j < NC; ++j) acc[i][j] *= factor;
+            for (int j = 0; j < JN; ++j) acc[i][j] *= factor;
     }
-    const int rt0 = mb * (S::TM / 16) + wm * MT;
+    const int rt0 = job.mb * (S::TM / 16) + wm * MT;
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-        const int r = (wn * NC + j) * 16 + c;
+    for (int j = 0; j < JN; ++j) {
+        const int r = (j * S::WN + wn) * 16 + c;
         if constexpr (GU) {
             // a row tile is 8 gate rows (lanes below 32) and the same 8 up rows; two tiles exchange
             // halves, so that every lane holds both of one element
@@ -405,8 +419,8 @@ __global__ __launch_bounds__(S::kThreads, S::PER_CU * S::kWaves / 4) void produc
                     hid[x] = gate / (1.f + __expf(-gate)) * u;
                 }
                 const int rt = rt0 + i + (lane >> 5);
-                if (r < rows && rt < rts && (MT > 1 || lane < 32)) {
-                    __bf16 *to = p.h + (size_t)(row0 + r) * p.Ip + rt * 8 + 4 * (g & 1);
+                if (r < job.rows && rt < rts && (MT > 1 || lane < 32)) {
+                    __bf16 *to = p.h + (size_t)(job.row0 + r) * p.Ip + rt * 8 + 4 * (g & 1);
 #pragma unroll
                     for (int y = 0; y < NT; ++y) {
                         bf16x4 z;
@@ -419,12 +433,58 @@ __global__ __launch_bounds__(S::kThreads, S::PER_CU * S::kWaves / 4) void produc
         } else {
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
-                if (r >= rows || rt0 + i >= rts) continue;
-                const size_t at = (size_t)(row0 + r) * p.a.H + (rt0 + i) * 16 + 4 * g;
-                *reinterpret_cast<f32x4 *>(p.out + at) = acc[i][j];
+                if (r >= job.rows || rt0 + i >= rts) continue;
+                *reinterpret_cast<f32x4 *>(p.out + (size_t)(job.row0 + r) * p.a.H + (rt0 + i) * 16 + 4 * g) = acc[i][j];
             }
         }
     }
+}
+
+template <typename S>
+__global__ __launch_bounds__(S::kThreads, 2) void product_kernel(Plan p) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // [NS][A, B]
+    __shared__ int found;
+    constexpr bool GU = S::kGateUp, FP8 = S::FP8;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int E = p.a.E;
+    Job job;
+    job.K = GU ? p.a.H : p.a.I;
+    job.M = GU ? 2 * p.a.I : p.a.H;
+    const int mblocks = (job.M + S::TM - 1) / S::TM;
+
+    // ---- the workgroup's tile: each XCD takes a run of neighbours, an expert's row blocks
+    // one after the other and all its tiles beside each other ----
+    const int64_t items = (int64_t)p.tile[E + 1] * mblocks, run = (items + 7) >> 3;
+    const int64_t item = (blockIdx.x & 7) * run + (blockIdx.x >> 3);
+    if ((int64_t)(blockIdx.x >> 3) >= run || item >= items) return;
+    for (int e = threadIdx.x; e <= E; e += S::kThreads)
+        if (item >= (int64_t)p.tile[e] * mblocks && item < (int64_t)p.tile[e + 1] * mblocks) found = e;
+    __syncthreads();
+    const int e = __builtin_amdgcn_readfirstlane(found);
+    const int t0 = p.tile[e], nt = p.tile[e + 1] - t0;
+    const int in = (int)(item - (int64_t)t0 * mblocks), tile = in % nt;
+    job.mb = in / nt;
+    job.row0 = p.first[e] + tile * S::TN;
+    job.rows = min(S::TN, p.first[e + 1] - job.row0);
+    const bool own = e == E;  // the shared expert
+    job.W = (const uint8_t *)(GU ? (own ? p.a.Wsh_gu : p.a.W_gu) : (own ? p.a.Wsh_d : p.a.W_d)) +
+            (own ? 0 : (size_t)e * job.M * job.K * (FP8 ? 1 : 2));
+    if constexpr (FP8) {  // a wave's weight rows lie in one block of 128, gate and up rows in one each
+        const float *s = GU ? (own ? p.a.ssh_gu : p.a.s_gu) : (own ? p.a.ssh_d : p.a.s_d);
+        const int kbs = job.K / 128;
+        const int block = GU ? job.mb * (S::TM / 2) / 128 : min((job.mb * S::TM + wave / S::WN * (S::TM / S::WM)) / 128, job.M / 128 - 1);
+        job.sc = s + (own ? 0 : (size_t)e * (job.M / 128) * kbs) + (size_t)block * kbs;
+        job.sc_up = job.sc + (size_t)(p.a.I / 128) * kbs;
+    }
+    const int jn = (job.rows + S::kStep - 1) / S::kStep;
+    if constexpr (S::NC >= 4) {
+        if (jn == 4) return multiply<S, 4>(p, job, lds);
+        if (jn == 3) return multiply<S, 3>(p, job, lds);
+    }
+    if constexpr (S::NC >= 2) {
+        if (jn == 2) return multiply<S, 2>(p, job, lds);
+    }
+    multiply<S, 1>(p, job, lds);
 }
 
 // y[t] = sum of the token's rows in rank order, times their weights, and of the
@@ -476,29 +536,27 @@ hipError_t launch_product(const Plan &p, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <bool FP8, int NT, int TM, int TN, int WM, int WN, int NS, int PER_CU>
+template <bool FP8, int NT, int TM, int TN, int WM, int WN, int LDS>
 hipError_t launch_both(const Plan &p, hipStream_t s) {
-    const hipError_t e = launch_product<Shape<true, FP8, NT, TM, TN, WM, WN, NS, PER_CU>>(p, s);
+    const hipError_t e = launch_product<Shape<true, FP8, NT, TM, TN, WM, WN, LDS>>(p, s);
     if (e != hipSuccess) return e;
-    return launch_product<Shape<false, FP8, NT, TM, TN, WM, WN, NS, PER_CU>>(p, s);
+    return launch_product<Shape<false, FP8, NT, TM, TN, WM, WN, LDS>>(p, s);
 }
 
 template <bool FP8>
 hipError_t launch_products(const Plan &p, hipStream_t s) {
     if (p.a.f32) {
-        if (p.tn == 32) return launch_both<FP8, 3, 64, 32, 4, 1, 3, 1>(p, s);
-        return launch_both<FP8, 3, 128, 128, 2, 4, 2, 1>(p, s);
+        if (p.tn == 32) return launch_both<FP8, 3, 64, 32, 4, 1, 81664>(p, s);
+        return launch_both<FP8, 3, 128, 128, 2, 4, 163328>(p, s);
     }
-    if (p.tn == 32) return launch_both<FP8, 1, 64, 32, 4, 1, 4, 2>(p, s);
-    if (p.tn == 128) return launch_both<FP8, 1, 256, 128, 4, 2, 3, 1>(p, s);
-    return launch_both<FP8, 1, 256, 256, 2, 4, 2, 1>(p, s);
+    if (p.tn == 32) return launch_both<FP8, 1, 64, 32, 4, 1, 81664>(p, s);
+    return launch_both<FP8, 1, 256, 256, 2, 4, 163328>(p, s);
 }
 
 // Rows of a product tile, by the rows that an expert has on average.
 int tile_rows(const ExpertArgs &a) {
     const int64_t avg = (int64_t)a.T * a.k / a.E;
-    if (a.f32) return avg <= 48 ? 32 : 128;
-    return avg <= 48 ? 32 : avg <= 256 ? 128 : 256;
+    return avg <= 48 ? 32 : a.f32 ? 128 : 256;
 }
 
 size_t lay_out(const ExpertArgs &a, uint8_t *ws, Plan *p) {
