@@ -4,6 +4,8 @@
 #include "dma.h"
 #include "prompt.h"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
@@ -287,21 +289,19 @@ __device__ __forceinline__ void multiply(const Plan &p, const Job &job, uint8_t 
         }
         brow[j] += ((lane & 7) ^ swizzle(r)) * 8;
     }
-    auto issue = [&](int step, int buf) {
+    // load i of a wave's kLoads
+    auto load = [&](int i, int step, int buf) {
         const unsigned at = lds0 + buf * kBuffer;
-#pragma unroll
-        for (int j = 0; j < PA; ++j) {
+        if (i < PA) {
             // piece of the buffer: row tile, then its k tiles
-            const int piece = wave * PA + j, rt = FP8 ? piece : piece >> 1, kt = FP8 ? step : min(2 * step + (piece & 1), nkt - 1);
+            const int piece = wave * PA + i, rt = FP8 ? piece : piece >> 1, kt = FP8 ? step : min(2 * step + (piece & 1), nkt - 1);
             const int grt = min(job.mb * (S::TM / 16) + rt, rts - 1);
             const size_t kb = GU ? (size_t)grt * nkt + kt : ((size_t)(grt >> 2) * nkt + kt) * 4 + (grt & 3);
             dma16(job.W + kb * 1024, lane * 16, at + piece * 1024);
+        } else {
+            const int j = (i - PA) / NT, y = (i - PA) % NT;
+            dma16v(brow[j] + y * plane + step * 64, at + S::A + y * kPlane + (j * S::kWaves + wave) * 1024);
         }
-#pragma unroll
-        for (int j = 0; j < PB; ++j)
-#pragma unroll
-            for (int y = 0; y < NT; ++y)
-                dma16v(brow[j] + y * plane + step * 64, at + S::A + y * kPlane + (j * S::kWaves + wave) * 1024);
     };
 
     f32x4 acc[MT][JN];
@@ -310,25 +310,39 @@ __device__ __forceinline__ void multiply(const Plan &p, const Job &job, uint8_t 
 #pragma unroll
         for (int j = 0; j < JN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+    // read i of a step's kReads: the activations first, every product needs them
     typedef Frags<S, JN> F;
-    auto read = [&](F &f, int buf, int s) {
+    constexpr int kReads = NT * JN + MT;
+    auto read = [&](F &f, int i, int buf, int s) {
         const uint8_t *A = lds + buf * kBuffer, *B = A + S::A;
-        const int ch = FP8 ? 2 * g + s : 4 * s + g;
-#pragma unroll
-        for (int y = 0; y < NT; ++y)
-#pragma unroll
-            for (int j = 0; j < JN; ++j)
-                f.b[y][j] = *reinterpret_cast<const bf16x8 *>(B + y * kPlane + ((j * S::WN + wn) * 16 + c) * 128 + ((ch ^ swizzle(c)) << 4));
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const uint8_t *at = FP8 ? A + (wm * MT + i) * 1024 + lane * 16 + 8 * s : A + ((wm * MT + i) * 2 + s) * 1024 + lane * 16;
-            f.a[i] = *reinterpret_cast<const typename F::u32xa *>(at);
+        if (i < NT * JN) {
+            const int y = NT - 1 - i / JN, j = i % JN, ch = FP8 ? 2 * g + s : 4 * s + g;
+            f.b[y][j] = *reinterpret_cast<const bf16x8 *>(B + y * kPlane + ((j * S::WN + wn) * 16 + c) * 128 + ((ch ^ swizzle(c)) << 4));
+        } else {
+            const int m = wm * MT + i - NT * JN;
+            const uint8_t *at = FP8 ? A + m * 1024 + lane * 16 + 8 * s : A + (m * 2 + s) * 1024 + lane * 16;
+            f.a[i - NT * JN] = *reinterpret_cast<const typename F::u32xa *>(at);
         }
     };
-    float operand = 1.f, factor = 1.f;
-    auto product = [&](const F &f) {
+    // The products of one step of 32 k, row tile by row tile; between them the reads of the next step
+    // (`with`, if READ) and the loads of the buffer that has become free (if LOAD), in this order.
+    float operand = 1.f, factor = 1.f, ratio = 1.f;
+    auto products = [&](const F &f, F &with, int at_buf, int at_s, int at_step, int free_buf, auto READ, auto LOAD, auto SCALE) {
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
+            if constexpr (LOAD.value) {
+#pragma unroll
+                for (int x = i * kLoads / MT; x < (i + 1) * kLoads / MT; ++x) load(x, at_step, free_buf);
+            }
+            if constexpr (READ.value) {  // done with the last but one row tile
+                constexpr int n = MT > 1 ? MT - 1 : 1;
+#pragma unroll
+                for (int x = min(i * kReads / n, kReads); x < min((i + 1) * kReads / n, kReads); ++x) read(with, x, at_buf, at_s);
+            }
+            if constexpr (SCALE.value) {
+#pragma unroll
+                for (int j = 0; j < JN; ++j) acc[i][j] *= ratio;
+            }
             bf16x8 a;
             if constexpr (FP8) a = decode8(f.a[i][0], f.a[i][1], operand);
             else a = __builtin_bit_cast(bf16x8, f.a[i]);
@@ -336,63 +350,69 @@ __device__ __forceinline__ void multiply(const Plan &p, const Job &job, uint8_t 
             for (int y = NT - 1; y >= 0; --y)  // the smaller terms first
 #pragma unroll
                 for (int j = 0; j < JN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, f.b[y][j], acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
-    // the reads of the next step among the products of this one
-    auto mix = [&]() {
-        constexpr int reads = MT + NT * JN, products = MT * NT * JN, each = products / reads > 0 ? products / reads : 1;
-#pragma unroll
-        for (int i = 0; i < reads; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x8, each, 0);
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
+    // fp8: a new block of 128 k: its power of two goes into the codes, its factor into the sums.
+    // A lane holds the scales of every 64th block; they are waited for where they are
+    // loaded, since a wait where they are used would be for the buffers' loads as well.
+    float scale_x = 0.f, scale_y = 0.f;
+    auto rescale = [&](int st) {
+        if constexpr (FP8) {
+            const int block = st >> 1;
+            if ((block & 63) == 0) {
+                const int at = min(block + lane, K / 128 - 1);
+                scale_x = job.sc[at];
+                if (GU) scale_y = job.sc_up[at];
+                asm volatile("" : "+v"(scale_x), "+v"(scale_y));
+            }
+            const Scale x = parts_of(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale_x), block & 63)));
+            const Scale y = GU ? parts_of(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale_y), block & 63))) : x;
+            operand = GU && c >= 8 ? y.power : x.power;
+            const float f = GU && lane >= 32 ? y.factor : x.factor;
+            ratio = factor / f;
+            factor = f;
         }
-        if (products > reads * each) __builtin_amdgcn_sched_group_barrier(0x8, products - reads * each, 0);
     };
 
+    // Buffers behind the last step hold copies of it, so that all waits count the same loads.
 #pragma unroll
     for (int i = 0; i < NS; ++i)
-        if (i < steps) issue(i, i);
-    if (NS - 1 < steps) dma_wait<(NS - 1) * kLoads>();
-    else dma_wait<0>();
+#pragma unroll
+        for (int x = 0; x < kLoads; ++x) load(x, min(i, steps - 1), i);
+    dma_wait<(NS - 1) * kLoads>();
     dma_barrier();
     F f0, f1;
-    read(f0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kReads; ++i) read(f0, i, 0, 0);
     int buf = 0;
-    for (int st = 0; st < steps; ++st) {
-        if constexpr (FP8) {
-            if ((st & 1) == 0) {  // a new block: its power of two goes into the codes, its factor into the sums
-                const Scale x = parts_of(job.sc[st >> 1]);
-                const Scale y = GU ? parts_of(job.sc_up[st >> 1]) : x;
-                operand = GU && c >= 8 ? y.power : x.power;
-                const float f = GU && lane >= 32 ? y.factor : x.factor;
-                if (st > 0) {
-                    const float ratio = factor / f;
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-#pragma unroll
-                        for (int j = 0; j < JN; ++j) acc[i][j] *= ratio;
-                }
-                factor = f;
-            }
-        }
-        read(f1, buf, 1);
-        product(f0);
-        mix();
+    auto step = [&](int st, auto SCALE) {
+        products(f0, f1, buf, 1, 0, 0, yes, no, SCALE);
         const int next = buf + 1 == NS ? 0 : buf + 1;
-        if (st + 1 < steps) {
-            // the next buffer is there, and this one was read by all
-            if (st + NS - 1 < steps) dma_wait<(NS - 2) * kLoads>();
-            else dma_wait<0>();
-            dma_barrier();
-            if (st + NS < steps) issue(st + NS, buf);
-            read(f0, next, 0);
-        }
-        if (FP8 || GU || 2 * st + 1 < nkt) {  // else the last 32 k of an odd number
-            product(f1);
-            mix();
-        }
+        dma_wait<(NS - 2) * kLoads>();  // the next buffer is there,
+        dma_barrier();                  // and this one was read by all
+        products(f1, f0, next, 0, min(st + NS, steps - 1), buf, yes, yes, no);
         buf = next;
+    };
+    if constexpr (FP8) {  // an even number of steps
+        int st = 0;
+        for (; st + 2 < steps; st += 2) {
+            rescale(st);
+            step(st, yes);
+            step(st + 1, no);
+        }
+        rescale(st);
+        step(st, yes);
+        products(f0, f1, buf, 1, 0, 0, yes, no, no);
+        products(f1, f0, 0, 0, 0, 0, no, no, no);
+    } else {
+        for (int st = 0; st + 1 < steps; ++st) step(st, no);
+        products(f0, f1, buf, 1, 0, 0, yes, no, no);
+        if (GU || nkt % 2 == 0) products(f1, f0, 0, 0, 0, 0, no, no, no);  // else the last 32 k of an odd number
     }
+    dma_wait<0>();
 
     // ---- results: lane (g, c) holds weight rows 4 g .. 4 g + 3 of its tiles for activation row c ----
     if constexpr (FP8) {
