@@ -240,11 +240,14 @@ struct Shape {
     // their counts tell which buffers are there
     static constexpr int PB(int jn) { return (jn * kStep + 8 * kWaves - 1) / (8 * kWaves); }
     static constexpr int B(int jn) { return NT * PB(jn) * kWaves * 1024; }
-    static constexpr int NS(int jn) {
+    // Buffers of activations and of weights: up to four of both, and one more of
+    // the weights, which come from further away, where LDS still holds it.
+    static constexpr int NB(int jn) {
         const int n = LDS_ / (A + B(jn));
         return n > 4 ? 4 : n;
     }
-    static_assert(A % (1024 * kWaves) == 0 && NS(NC) >= 2 && LDS_ <= 163328, "");
+    static constexpr int NA(int jn) { return NB(jn) < 4 && NB(jn) * (A + B(jn)) + A <= LDS_ ? NB(jn) + 1 : NB(jn); }
+    static_assert(A % (1024 * kWaves) == 0 && NB(NC) >= 2 && LDS_ <= 163840, "");
 };
 
 // What a workgroup works on.
@@ -265,9 +268,9 @@ struct Frags {
 template <typename S, int JN>
 __device__ __forceinline__ void multiply(const Plan &p, const Job &job, uint8_t *lds) {
     constexpr bool GU = S::kGateUp, FP8 = S::FP8;
-    constexpr int NT = S::NT, MT = S::MT, NS = S::NS(JN), PA = S::PA, PB = S::PB(JN), kLoads = PA + PB * NT;
-    constexpr int kPlane = PB * S::kWaves * 1024, kBuffer = S::A + NT * kPlane;
-    static_assert((NS - 2) * kLoads < 63, "");
+    constexpr int NT = S::NT, MT = S::MT, NA = S::NA(JN), NB = S::NB(JN), PA = S::PA, PB = S::PB(JN), kLoads = PA + PB * NT;
+    constexpr int kPlane = PB * S::kWaves * 1024, kB0 = NA * S::A;  // the activations' buffers lie behind the weights'
+    static_assert((NB - 1) * PB * NT + (NA - 1) * PA < 63, "");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / S::WN, wn = wave % S::WN, g = lane >> 4, c = lane & 15;
     const int K = job.K;
@@ -289,18 +292,18 @@ __device__ __forceinline__ void multiply(const Plan &p, const Job &job, uint8_t 
         }
         brow[j] += ((lane & 7) ^ swizzle(r)) * 8;
     }
-    // load i of a wave's kLoads
-    auto load = [&](int i, int step, int buf) {
-        const unsigned at = lds0 + buf * kBuffer;
-        if (i < PA) {
+    // load i of a wave's kLoads: the activations of a step, then the weights of a step
+    auto load = [&](int i, int step_b, int buf_b, int step_a, int buf_a) {
+        if (i >= PB * NT) {
             // piece of the buffer: row tile, then its k tiles
-            const int piece = wave * PA + i, rt = FP8 ? piece : piece >> 1, kt = FP8 ? step : min(2 * step + (piece & 1), nkt - 1);
+            const int piece = wave * PA + i - PB * NT, rt = FP8 ? piece : piece >> 1;
+            const int kt = FP8 ? step_a : min(2 * step_a + (piece & 1), nkt - 1);
             const int grt = min(job.mb * (S::TM / 16) + rt, rts - 1);
             const size_t kb = GU ? (size_t)grt * nkt + kt : ((size_t)(grt >> 2) * nkt + kt) * 4 + (grt & 3);
-            dma16(job.W + kb * 1024, lane * 16, at + piece * 1024);
+            dma16(job.W + kb * 1024, lane * 16, lds0 + buf_a * S::A + piece * 1024);
         } else {
-            const int j = (i - PA) / NT, y = (i - PA) % NT;
-            dma16v(brow[j] + y * plane + step * 64, at + S::A + y * kPlane + (j * S::kWaves + wave) * 1024);
+            const int j = i / NT, y = i % NT;
+            dma16v(brow[j] + y * plane + step_b * 64, lds0 + kB0 + buf_b * (NT * kPlane) + y * kPlane + (j * S::kWaves + wave) * 1024);
         }
     };
 
@@ -313,8 +316,8 @@ __device__ __forceinline__ void multiply(const Plan &p, const Job &job, uint8_t 
     // read i of a step's kReads: the activations first, every product needs them
     typedef Frags<S, JN> F;
     constexpr int kReads = NT * JN + MT;
-    auto read = [&](F &f, int i, int buf, int s) {
-        const uint8_t *A = lds + buf * kBuffer, *B = A + S::A;
+    auto read = [&](F &f, int i, int buf_a, int buf_b, int s) {
+        const uint8_t *A = lds + buf_a * S::A, *B = lds + kB0 + buf_b * (NT * kPlane);
         if (i < NT * JN) {
             const int y = NT - 1 - i / JN, j = i % JN, ch = FP8 ? 2 * g + s : 4 * s + g;
             f.b[y][j] = *reinterpret_cast<const bf16x8 *>(B + y * kPlane + ((j * S::WN + wn) * 16 + c) * 128 + ((ch ^ swizzle(c)) << 4));
@@ -327,17 +330,18 @@ __device__ __forceinline__ void multiply(const Plan &p, const Job &job, uint8_t 
     // The products of one step of 32 k, row tile by row tile; between them the reads of the next step
     // (`with`, if READ) and the loads of the buffer that has become free (if LOAD), in this order.
     float operand = 1.f, factor = 1.f, ratio = 1.f;
-    auto products = [&](const F &f, F &with, int at_buf, int at_s, int at_step, int free_buf, auto READ, auto LOAD, auto SCALE) {
+    int ba = 0, bb = 0;  // the buffers in use
+    auto products = [&](const F &f, F &with, int at_a, int at_b, int at_s, int st, auto READ, auto LOAD, auto SCALE) {
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
             if constexpr (LOAD.value) {
 #pragma unroll
-                for (int x = i * kLoads / MT; x < (i + 1) * kLoads / MT; ++x) load(x, at_step, free_buf);
+                for (int x = i * kLoads / MT; x < (i + 1) * kLoads / MT; ++x) load(x, min(st + NB, steps - 1), bb, min(st + NA, steps - 1), ba);
             }
             if constexpr (READ.value) {  // done with the last but one row tile
                 constexpr int n = MT > 1 ? MT - 1 : 1;
 #pragma unroll
-                for (int x = min(i * kReads / n, kReads); x < min((i + 1) * kReads / n, kReads); ++x) read(with, x, at_buf, at_s);
+                for (int x = min(i * kReads / n, kReads); x < min((i + 1) * kReads / n, kReads); ++x) read(with, x, at_a, at_b, at_s);
             }
             if constexpr (SCALE.value) {
 #pragma unroll
@@ -379,22 +383,22 @@ __device__ __forceinline__ void multiply(const Plan &p, const Job &job, uint8_t 
 
     // Buffers behind the last step hold copies of it, so that all waits count the same loads.
 #pragma unroll
-    for (int i = 0; i < NS; ++i)
+    for (int i = 0; i < NA; ++i)
 #pragma unroll
-        for (int x = 0; x < kLoads; ++x) load(x, min(i, steps - 1), i);
-    dma_wait<(NS - 1) * kLoads>();
+        for (int x = i < NB ? 0 : PB * NT; x < kLoads; ++x) load(x, min(i, steps - 1), i, min(i, steps - 1), i);
+    dma_wait<(NB - 1) * PB * NT + (NA - 1) * PA>();
     dma_barrier();
     F f0, f1;
 #pragma unroll
-    for (int i = 0; i < kReads; ++i) read(f0, i, 0, 0);
-    int buf = 0;
+    for (int i = 0; i < kReads; ++i) read(f0, i, 0, 0, 0);
     auto step = [&](int st, auto SCALE) {
-        products(f0, f1, buf, 1, 0, 0, yes, no, SCALE);
-        const int next = buf + 1 == NS ? 0 : buf + 1;
-        dma_wait<(NS - 2) * kLoads>();  // the next buffer is there,
-        dma_barrier();                  // and this one was read by all
-        products(f1, f0, next, 0, min(st + NS, steps - 1), buf, yes, yes, no);
-        buf = next;
+        products(f0, f1, ba, bb, 1, 0, yes, no, SCALE);
+        const int na = ba + 1 == NA ? 0 : ba + 1, nb = bb + 1 == NB ? 0 : bb + 1;
+        dma_wait<(NB - 2) * kLoads + (NA > NB ? PA : 0)>();  // the next buffers are there,
+        dma_barrier();                                       // and these were read by all
+        products(f1, f0, na, nb, 0, st, yes, yes, no);
+        ba = na;
+        bb = nb;
     };
     if constexpr (FP8) {  // an even number of steps
         int st = 0;
@@ -405,11 +409,11 @@ __device__ __forceinline__ void multiply(const Plan &p, const Job &job, uint8_t 
         }
         rescale(st);
         step(st, yes);
-        products(f0, f1, buf, 1, 0, 0, yes, no, no);
+        products(f0, f1, ba, bb, 1, 0, yes, no, no);
         products(f1, f0, 0, 0, 0, 0, no, no, no);
     } else {
         for (int st = 0; st + 1 < steps; ++st) step(st, no);
-        products(f0, f1, buf, 1, 0, 0, yes, no, no);
+        products(f0, f1, ba, bb, 1, 0, yes, no, no);
         if (GU || nkt % 2 == 0) products(f1, f0, 0, 0, 0, 0, no, no, no);  // else the last 32 k of an odd number
     }
     dma_wait<0>();
@@ -436,7 +440,7 @@ __device__ __forceinline__ void multiply(const Plan &p, const Job &job, uint8_t 
                     const unsigned a0 = __float_as_uint(acc[i][j][x]), a1 = __float_as_uint(acc[MT > 1 ? i + 1 : i][j][x]);
                     const auto sw = __builtin_amdgcn_permlane32_swap(a0, a1, false, false);
                     const float gate = __uint_as_float(sw[0]), u = __uint_as_float(sw[1]);
-                    hid[x] = gate / (1.f + __expf(-gate)) * u;
+                    hid[x] = gate * __builtin_amdgcn_rcpf(1.f + __expf(-gate)) * u;
                 }
                 const int rt = rt0 + i + (lane >> 5);
                 if (r < job.rows && rt < rts && (MT > 1 || lane < 32)) {
@@ -462,8 +466,7 @@ __device__ __forceinline__ void multiply(const Plan &p, const Job &job, uint8_t 
 
 template <typename S>
 __global__ __launch_bounds__(S::kThreads, 2) void product_kernel(Plan p) {
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // [NS][A, B]
-    __shared__ int found;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // [NA][A], [NB][B]
     constexpr bool GU = S::kGateUp, FP8 = S::FP8;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int E = p.a.E;
@@ -477,10 +480,12 @@ __global__ __launch_bounds__(S::kThreads, 2) void product_kernel(Plan p) {
     const int64_t items = (int64_t)p.tile[E + 1] * mblocks, run = (items + 7) >> 3;
     const int64_t item = (blockIdx.x & 7) * run + (blockIdx.x >> 3);
     if ((int64_t)(blockIdx.x >> 3) >= run || item >= items) return;
-    for (int e = threadIdx.x; e <= E; e += S::kThreads)
-        if (item >= (int64_t)p.tile[e] * mblocks && item < (int64_t)p.tile[e + 1] * mblocks) found = e;
-    __syncthreads();
-    const int e = __builtin_amdgcn_readfirstlane(found);
+    int e = 0;
+    for (int e0 = 0; e0 <= E; e0 += 64) {
+        const int x = min(e0 + (int)(threadIdx.x & 63), E);
+        const uint64_t at = __ballot(item >= (int64_t)p.tile[x] * mblocks && item < (int64_t)p.tile[x + 1] * mblocks);
+        if (at) e = min(e0 + __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)at)) - 1, E);
+    }
     const int t0 = p.tile[e], nt = p.tile[e + 1] - t0;
     const int in = (int)(item - (int64_t)t0 * mblocks), tile = in % nt;
     job.mb = in / nt;
@@ -566,11 +571,11 @@ hipError_t launch_both(const Plan &p, hipStream_t s) {
 template <bool FP8>
 hipError_t launch_products(const Plan &p, hipStream_t s) {
     if (p.a.f32) {
-        if (p.tn == 32) return launch_both<FP8, 3, 64, 32, 4, 1, 81664>(p, s);
-        return launch_both<FP8, 3, 128, 128, 2, 4, 163328>(p, s);
+        if (p.tn == 32) return launch_both<FP8, 3, 64, 32, 4, 1, 81920>(p, s);
+        return launch_both<FP8, 3, 128, 128, 2, 4, 163840>(p, s);
     }
-    if (p.tn == 32) return launch_both<FP8, 1, 64, 32, 4, 1, 81664>(p, s);
-    return launch_both<FP8, 1, 256, 256, 2, 4, 163328>(p, s);
+    if (p.tn == 32) return launch_both<FP8, 1, 64, 32, 4, 1, 81920>(p, s);
+    return launch_both<FP8, 1, 256, 256, 2, 4, 163840>(p, s);
 }
 
 // Rows of a product tile, by the rows that an expert has on average.
