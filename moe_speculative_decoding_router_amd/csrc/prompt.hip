@@ -8,6 +8,7 @@ namespace moe {
 namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
@@ -109,7 +110,9 @@ __global__ __launch_bounds__(kThreads, groups(D, NT)) void prompt_kernel(PromptA
     const int row = u.row0 + wave * 32 + c;
     const size_t tok = (size_t)a.q_off[u.s] + min(row, u.n - 1);
     const unsigned flip = a.scale < 0.f ? 0x80008000u : 0u;
-    const float sl = fabsf(a.scale) * 1.44269504088896341f;
+    // above 0, so that hidden keys' -inf stays what it is, and by no more than a subnormal number,
+    // which leaves all finite scores at 0
+    const float sl = fmaxf(fabsf(a.scale) * 1.44269504088896341f, 1.4e-45f);
     bf16x8 q[NT][KS];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
@@ -147,20 +150,29 @@ __global__ __launch_bounds__(kThreads, groups(D, NT)) void prompt_kernel(PromptA
         vb = kb + 3 * plane;
     }
     const unsigned lds0 = lds_address(lds);
+    unsigned ko[LPW], vo[LPW];  // byte offsets of a lane's chunks from the step's first row
+#pragma unroll
+    for (int j = 0; j < LPW; ++j) {
+        const int r = (wave * LPW + j) * RPL + lane / CPR, ch = lane % CPR;
+        ko[j] = (unsigned)(r * (int)kst + (ch ^ swizzle_k<D>(r)) * 8) * 2u;
+        vo[j] = (unsigned)(r * (int)vst + (ch ^ swizzle_v<D>(r)) * 8) * 2u;
+    }
     auto issue = [&](int step, int buf) {
         const uint16_t *kt = kb + (size_t)step * BK * kst, *vt = vb + (size_t)step * BK * vst;
-        const int left = u.m - 1 - step * BK;  // rows behind the last key are copies of it
+        const unsigned at = lds0 + buf * (2 * NT * TB) + wave * LPW * 1024;
+        const int over = step * BK + BK - u.m;  // rows behind the last key are copies of it
 #pragma unroll
         for (int j = 0; j < LPW; ++j) {
-            const int r = (wave * LPW + j) * RPL + lane / CPR, ch = lane % CPR;
-            const int rr = min(r, left);
-            const unsigned at = lds0 + buf * (2 * NT * TB) + (wave * LPW + j) * 1024;
-            const unsigned ko = (unsigned)(rr * (int)kst + (ch ^ swizzle_k<D>(r)) * 8) * 2u;
-            const unsigned vo = (unsigned)(rr * (int)vst + (ch ^ swizzle_v<D>(r)) * 8) * 2u;
+            unsigned kj = ko[j], vj = vo[j];
+            if (over > 0) {
+                const int r = (wave * LPW + j) * RPL + lane / CPR, back = max(r - (BK - 1 - over), 0);
+                kj -= (unsigned)(back * (int)kst) * 2u;
+                vj -= (unsigned)(back * (int)vst) * 2u;
+            }
 #pragma unroll
             for (int p = 0; p < NT; ++p) {
-                dma16(kt + p * plane, ko, at + p * TB);
-                dma16(vt + p * plane, vo, at + (NT + p) * TB);
+                dma16(kt + p * plane, kj, at + p * TB + j * 1024);
+                dma16(vt + p * plane, vj, at + (NT + p) * TB + j * 1024);
             }
         }
     };
@@ -190,39 +202,67 @@ __global__ __launch_bounds__(kThreads, groups(D, NT)) void prompt_kernel(PromptA
         if (st * BK <= wave_first + 31) {  // some row of the wave sees a key of the step
             f32x16 s[KT];
 #pragma unroll
-            for (int t = 0; t < KT; ++t) {
+            for (int t = 0; t < KT; ++t)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) s[t][i] = 0.f;
+            auto key = [&](int x, int t, int ks) {
+                return *reinterpret_cast<const bf16x8 *>(b + x * TB + t * 32 * D * 2 + ka + ((kx ^ (2 * ks)) << 4));
+            };
+            if constexpr (NT == 1) {  // keys kAhead products ahead
+                constexpr int kAhead = 4;
+                bf16x8 kf[kAhead];
 #pragma unroll
-                for (int y = NT - 1; y >= 0; --y)  // the smaller terms first
+                for (int i = 0; i < kAhead; ++i) kf[i] = key(0, i % KT, i / KT);
 #pragma unroll
-                    for (int x = NT - 1 - y; x >= 0; --x)
+                for (int i = 0; i < KS * KT; ++i) {
+                    s[i % KT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[i % kAhead], q[0][i / KT], s[i % KT], 0, 0, 0);
+                    if (i + kAhead < KS * KT) kf[i % kAhead] = key(0, (i + kAhead) % KT, (i + kAhead) / KT);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            } else {
 #pragma unroll
-                        for (int ks = 0; ks < KS; ++ks) {
-                            const bf16x8 kf = *reinterpret_cast<const bf16x8 *>(b + x * TB + t * 32 * D * 2 + ka + ((kx ^ (2 * ks)) << 4));
-                            s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[y][ks], s[t], 0, 0, 0);
-                        }
+                for (int t = 0; t < KT; ++t)
+#pragma unroll
+                    for (int y = NT - 1; y >= 0; --y)  // the smaller terms first
+#pragma unroll
+                        for (int x = NT - 1 - y; x >= 0; --x)
+#pragma unroll
+                            for (int ks = 0; ks < KS; ++ks)
+                                s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key(x, t, ks), q[y][ks], s[t], 0, 0, 0);
             }
-            const bool masked = st * BK + BK - 1 > wave_first;
-            if (masked) {
+            auto value = [&](int x, int kk, int d) {
+                typedef __attribute__((address_space(3))) s16x4 *lp;
+                const uint8_t *at = b + (NT + x) * TB + kk * 16 * D * 2 + va + ((vx ^ (4 * d)) << 4);
+                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(s16x4 *)at);
+                const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(s16x4 *)(at + 8 * D * 2));
+                const s16x8 vf = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                return __builtin_bit_cast(bf16x8, vf);
+            };
+            // where registers hold them, the values come while the probabilities are made
+            constexpr bool kEarly = NT == 1 && D <= 128;
+            bf16x8 vf[kEarly ? 2 * KT : 1][kEarly ? DT : 1];
+            if constexpr (kEarly) {
+#pragma unroll
+                for (int kk = 0; kk < 2 * KT; ++kk)
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) vf[kk][d] = value(0, kk, d);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (st * BK + BK - 1 > wave_first) {  // some row of the wave does not see all keys
 #pragma unroll
                 for (int t = 0; t < KT; ++t)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int p = st * BK + t * 32 + 8 * (i >> 2) + 4 * half + (i & 3);
-                        s[t][i] = p <= sees ? s[t][i] * sl : -__builtin_inff();
+                        s[t][i] = p <= sees ? s[t][i] : -__builtin_inff();
                     }
-            } else {
-#pragma unroll
-                for (int t = 0; t < KT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) s[t][i] *= sl;
             }
             float top = s[0][0];
 #pragma unroll
             for (int t = 0; t < KT; ++t)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
+            top *= sl;
             if (__any(top > m + kSlack)) {
                 const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
                 const float to = fmaxf(m, fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1])));
@@ -239,13 +279,21 @@ __global__ __launch_bounds__(kThreads, groups(D, NT)) void prompt_kernel(PromptA
             for (int t = 0; t < KT; ++t)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float p = __builtin_amdgcn_exp2f(s[t][i] - m);
-                    l += p;
+                    const float p = __builtin_amdgcn_exp2f(fmaf(s[t][i], sl, -m));
+                    if (NT > 1) l += p;
                     __bf16 z[NT];
                     split<NT>(p, z);
 #pragma unroll
                     for (int y = 0; y < NT; ++y) pb[y][2 * t + (i >> 3)][i & 7] = z[y];
                 }
+            if constexpr (NT == 1) {  // the sum of what enters the second product, two at a time
+                const bf16x2 ones = {(__bf16)1.f, (__bf16)1.f};
+#pragma unroll
+                for (int x = 0; x < KT * 2; ++x)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{pb[0][x][2 * i], pb[0][x][2 * i + 1]}, ones, l, false);
+            }
             // lane slot j of half h in a 16-key product is key 8 (j / 4) + 4 h + j % 4 in both operands
 #pragma unroll
             for (int y = NT - 1; y >= 0; --y)
@@ -255,12 +303,10 @@ __global__ __launch_bounds__(kThreads, groups(D, NT)) void prompt_kernel(PromptA
                     for (int kk = 0; kk < 2 * KT; ++kk)
 #pragma unroll
                         for (int d = 0; d < DT; ++d) {
-                            typedef __attribute__((address_space(3))) s16x4 *lp;
-                            const uint8_t *at = b + (NT + x) * TB + kk * 16 * D * 2 + va + ((vx ^ (4 * d)) << 4);
-                            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(s16x4 *)at);
-                            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(s16x4 *)(at + 8 * D * 2));
-                            const s16x8 vf = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf), pb[y][kk], o[d], 0, 0, 0);
+                            bf16x8 v;
+                            if constexpr (kEarly) v = vf[kk][d];
+                            else v = value(x, kk, d);
+                            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, pb[y][kk], o[d], 0, 0, 0);
                         }
         }
         if (NB == 1) {
