@@ -191,6 +191,8 @@ __global__ __launch_bounds__(kThreads, groups(D, NT)) void prompt_kernel(PromptA
     float m = kNone, l = 0.f;
     const int sees = row + first;  // the last key of this lane's row
     const int wave_first = u.row0 + wave * 32 + first;  // of the wave's first row
+    const int wave_last = min(u.row0 + wave * 32 + 31, u.n - 1) + first;
+    const bool some = u.row0 + wave * 32 < u.n;
 
     if (s0 < s1) issue(s0, 0);
     int buf = 0;
@@ -199,7 +201,7 @@ __global__ __launch_bounds__(kThreads, groups(D, NT)) void prompt_kernel(PromptA
         dma_barrier();  // this step's tiles are there, and the last step's were read by all
         if (NB > 1 && st + 1 < s1) issue(st + 1, buf ^ 1);
         const uint8_t *b = lds + buf * (2 * NT * TB);
-        if (st * BK <= wave_first + 31) {  // some row of the wave sees a key of the step
+        if (some && st * BK <= wave_last) {  // some row of the wave sees a key of the step
             f32x16 s[KT];
 #pragma unroll
             for (int t = 0; t < KT; ++t)
@@ -416,12 +418,20 @@ size_t prompt_plan(PromptArgs &a, int n_cu) {
     }
     a.units = blocks * a.Hq;
     a.parts = 1;
-    // few units over many keys: shares of at least 256 keys, as many as fill the card
-    const int want = 2 * n_cu;
-    if (a.units > 0 && a.units < want) {
-        const int by_units = (want + a.units - 1) / a.units, by_keys = keys / 256;
-        a.parts = by_units < by_keys ? by_units : by_keys;
-        if (a.parts < 1) a.parts = 1;
+    // Units that fill the workgroups that run at once a few times over at most leave some idle in the
+    // last round.  Their keys are cut into as many shares of at least 256 as take the least time, by
+    // what a step of 64 keys costs a workgroup (1.6 us at D = 128 where two share a compute unit) and
+    // the join of a share's rows.  (515 rows, 32 heads, 60516 keys: 570 us with three shares, 680 with
+    // the four that fill every workgroup, 571 with sixteen.)
+    const int slots = n_cu * (a.f32 ? 1 : 2);
+    if (a.units > 0 && a.units < 4 * slots) {
+        const double step = 1.6 * a.D / 128 * (a.f32 ? 3 : 1), join = (double)a.units * kRows * (a.D + 2) * 8 / 4.5e6;
+        double best = 1e30;
+        for (int p = 1; p <= 64 && (p == 1 || p <= keys / 256); ++p) {
+            const int64_t rounds = ((int64_t)a.units * p + slots - 1) / slots;
+            const double cost = rounds * (keys / 64.0 / p) * step + (p > 1 ? 4 + join * p : 0);
+            if (cost < 0.98 * best) best = cost, a.parts = p;
+        }
     }
     size_t ws = a.f32 ? (size_t)a.k_off[a.nseq] * a.Hkv * a.D * 12 : 0;
     ws = (ws + 255) & ~(size_t)255;
