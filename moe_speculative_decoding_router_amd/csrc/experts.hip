@@ -83,7 +83,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_tokens_kernel(const float
 // their outputs, combine the tokens' weighted sums in rank order.
 // ---------------------------------------------------------------------------
 constexpr int kListThreads = 256;
-constexpr int kMinChunk = 4096;  // pairs of a workgroup at least
+constexpr int kMinChunk = 2048;  // pairs of a workgroup at least
+constexpr int kPerRound = 8;     // pairs of a thread at a time
 constexpr int kMaxChunks = 256;
 
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
@@ -111,9 +112,13 @@ __global__ __launch_bounds__(kListThreads) void count_pairs_kernel(Plan p) {
     for (int e = threadIdx.x; e < p.a.E; e += kListThreads) n[e] = 0;
     __syncthreads();
     const int64_t end = min((int64_t)(blockIdx.x + 1) * p.chunk, (int64_t)p.pairs);
-    for (int64_t i = (int64_t)blockIdx.x * p.chunk + threadIdx.x; i < end; i += kListThreads) {
-        const int e = p.a.idx[i];
-        if (e >= 0 && e < p.a.E) atomicAdd(&n[e], 1);
+    for (int64_t i = (int64_t)blockIdx.x * p.chunk + threadIdx.x; i < end; i += kPerRound * kListThreads) {
+        int e[kPerRound];
+#pragma unroll
+        for (int j = 0; j < kPerRound; ++j) e[j] = i + j * kListThreads < end ? p.a.idx[i + j * kListThreads] : -1;
+#pragma unroll
+        for (int j = 0; j < kPerRound; ++j)
+            if (e[j] >= 0 && e[j] < p.a.E) atomicAdd(&n[e[j]], 1);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < p.a.E; e += kListThreads) p.counts[(size_t)blockIdx.x * p.a.E + e] = n[e];
@@ -127,6 +132,7 @@ __global__ __launch_bounds__(kListThreads) void place_pairs_kernel(Plan p) {
     for (int e = tid; e < E; e += kListThreads) {
         int before = 0, n = 0;
         if (p.chunks > 1) {
+#pragma unroll 8
             for (int c = 0; c < p.chunks; ++c) {
                 const int v = p.counts[(size_t)c * E + e];
                 before += c < (int)blockIdx.x ? v : 0;
@@ -167,14 +173,21 @@ __global__ __launch_bounds__(kListThreads) void place_pairs_kernel(Plan p) {
         }
     }
     __syncthreads();
-    for (int64_t i = begin + tid; i < end; i += kListThreads) {
-        const int e = p.a.idx[i];
-        int r = -1;
-        if (e >= 0 && e < E) {
-            r = atomicAdd(&at[e], 1);
-            p.row_token[r] = (int)(i / p.a.k);
+    for (int64_t i = begin + tid; i < end; i += kPerRound * kListThreads) {
+        int e[kPerRound];
+#pragma unroll
+        for (int j = 0; j < kPerRound; ++j) e[j] = i + j * kListThreads < end ? p.a.idx[i + j * kListThreads] : -1;
+#pragma unroll
+        for (int j = 0; j < kPerRound; ++j) {
+            const int64_t at_pair = i + j * kListThreads;
+            if (at_pair >= end) break;
+            int r = -1;
+            if (e[j] >= 0 && e[j] < E) {
+                r = atomicAdd(&at[e[j]], 1);
+                p.row_token[r] = (int)((unsigned)at_pair / (unsigned)p.a.k);
+            }
+            p.row_of[at_pair] = r;
         }
-        p.row_of[i] = r;
     }
     if (p.a.shared)
         for (int64_t t = (int64_t)blockIdx.x * kListThreads + tid; t < p.a.T; t += (int64_t)gridDim.x * kListThreads)

@@ -14,7 +14,10 @@ constexpr int kThreads = 256;
 // Read.  The inverse of append: a lane holds 8 consecutive elements of a row
 // (4 code bytes in, 16 or 32 bytes out), a wave 512 / D consecutive rows of
 // one head, kReadAhead times over so that its loads are under way together.
-// K and V are the grid's z.
+// K and V are the grid's z.  Memory bounds it: 100001 bf16 rows of 8 heads of 128
+// (109 MB read, 409 MB written) take 87 us, 5.9 TB/s.  The results are stored past the
+// caches: through them the same rows take 155 us.  With 2 or 8 in the place of
+// kReadAhead 87 and 88 us.
 // ---------------------------------------------------------------------------
 constexpr int kReadAhead = 4;
 
@@ -69,81 +72,76 @@ __global__ __launch_bounds__(kThreads) void read_kernel(KvReadArgs a) {
             f32x4 y0, y1;
             dequant8_f32(word[u], s, y0, y1);
             f32x4 *p = reinterpret_cast<f32x4 *>((float *)dst + o);
-            p[0] = y0;
-            p[1] = y1;
+            __builtin_nontemporal_store(y0, p);
+            __builtin_nontemporal_store(y1, p + 1);
         } else {
-            *reinterpret_cast<bf16x8 *>((uint16_t *)dst + o) = dequant8(word[u], s);
+            __builtin_nontemporal_store(__builtin_bit_cast(u32x4, dequant8(word[u], s)), reinterpret_cast<u32x4 *>((uint16_t *)dst + o));
         }
     }
 }
 
 // ---------------------------------------------------------------------------
-// Page bookkeeping.  Lists of at most 64 sequences: one workgroup, whose
-// accesses to the counts bypass its L1 (agent scope), since its own atomics
-// change them in between.  Everything is integers and chosen by rank, so
+// Page bookkeeping.  Lists of at most 64 sequences: one workgroup.  Everything is integers and chosen by rank, so
 // results do not depend on the order in which atomics arrive.
 // ---------------------------------------------------------------------------
 constexpr int kBookThreads = 1024;
 constexpr int kScan = 8;  // counts of a thread at a time in the search for free pages
 
-__device__ __forceinline__ int count_of(const int32_t *refs, int p) {
-    return __hip_atomic_load(refs + p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-
 struct Take {  // what the list's entries need, in LDS
-    int need[kMaxSegments];   // fresh pages
-    int start[kMaxSegments];  // rank of the first of them among the pages taken, -1: not served
+    int need[kMaxSegments];      // fresh pages
+    int start[kMaxSegments];     // rank of the first of them among the pages taken, -1: not served
     long long at[kMaxSegments];  // table index of the first
-    int total, found;
+    int total;
     int wave[kBookThreads / 64];
 };
 
-// Number of free pages before this thread's run of the chunk at `base`, and
-// the mask of its free ones.
+// Number of free pages before this thread's run of the chunk at `base`, the
+// mask of its free ones, and the chunk's number.
 __device__ int free_before(const PoolArgs &a, int base, Take &t, unsigned &mask, int &all) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     mask = 0;
     const int p0 = base + threadIdx.x * kScan;
     int v[kScan];
 #pragma unroll
-    for (int i = 0; i < kScan; ++i) v[i] = p0 + i < a.num_pages ? count_of(a.refs, p0 + i) : 1;
+    for (int i = 0; i < kScan; ++i)  // past the L1, which may hold older counts
+        v[i] = p0 + i < a.num_pages ? __hip_atomic_load(a.refs + p0 + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 1;
 #pragma unroll
     for (int i = 0; i < kScan; ++i) mask |= (unsigned)(v[i] <= 0) << i;
     const int mine = __popc(mask), incl = wave_incl_scan(mine);
     __syncthreads();  // the last chunk's sums are read
     if (lane == 63) t.wave[wave] = incl;
     __syncthreads();
-    int before = incl - mine;
-    all = 0;
-    for (int w = 0; w < kBookThreads / 64; ++w) {
-        const int x = t.wave[w];
-        if (w < wave) before += x;
-        all += x;
-    }
-    return before;
+    const int w = lane < kBookThreads / 64 ? t.wave[lane] : 0, before = wave_incl_scan(w) - w;
+    all = wave_sum_int(w);
+    return __builtin_amdgcn_readlane(before, __builtin_amdgcn_readfirstlane(wave)) + incl - mine;
 }
 
 // Gives entry i of the list its need[i] lowest free pages, the entries in
 // order, each whole or not at all; writes them to table[at[i]...] with a count
 // of 1 and sets start[i] (-1: not enough pages).
 __device__ void take_pages(const PoolArgs &a, Take &t) {
+    // This workgroup's atomics have arrived in the L2, which is all that its own later accesses need.
+    // (A fence would write the whole L2 back as well: the
+    // fork of a prompt into 15 then takes 25 us instead of 20.)
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (threadIdx.x == 0) {
-        long long sum = 0;
-        for (int i = 0; i < a.n; ++i) sum += t.need[i];
-        t.total = (int)(sum < a.num_pages ? sum : a.num_pages);
-    }
-    __syncthreads();
-    // how many are free, up to the number that is needed
-    unsigned mask;
-    int all, found = 0, end = 0;
-    for (int base = 0; base < a.num_pages && found < t.total; base += kBookThreads * kScan) {
-        free_before(a, base, t, mask, all);
+    const int lane = threadIdx.x & 63;
+    // every wave for itself: how many pages are needed
+    const int mine = lane < a.n ? t.need[lane] : 0;
+    const long long sum = ((long long)wave_sum_int(mine >> 12) << 12) + wave_sum_int(mine & 4095);
+    const int total = (int)(sum < a.num_pages ? sum : a.num_pages);
+    unsigned mask = 0;
+    int all = 0, found = 0, end = 0, rank = 0;
+    for (int base = 0; base < a.num_pages && found < total; base += kBookThreads * kScan) {
+        rank = found + free_before(a, base, t, mask, all);
         found += all;
         end = base + kBookThreads * kScan;
     }
-    __syncthreads();
-    if (threadIdx.x == 0) {
+    if (sum <= found) {  // all are served
+        const int incl = wave_incl_scan(mine);  // sum <= num_pages
+        if (threadIdx.x < a.n) t.start[lane] = incl - mine;
+        if (threadIdx.x == 0) t.total = total;
+    } else if (threadIdx.x == 0) {
         int used = 0;
         for (int i = 0; i < a.n; ++i) {
             const bool fits = t.need[i] <= found - used;
@@ -153,9 +151,10 @@ __device__ void take_pages(const PoolArgs &a, Take &t) {
         t.total = used;
     }
     __syncthreads();
+    const bool once = end <= kBookThreads * kScan;  // the last search's ranks are still there
     int before = 0;
     for (int base = 0; base < end && before < t.total; base += kBookThreads * kScan) {
-        int rank = before + free_before(a, base, t, mask, all);
+        if (!once) rank = before + free_before(a, base, t, mask, all);
         for (int i = 0; i < kScan; ++i) {
             if (!((mask >> i) & 1)) continue;
             if (rank < t.total) {
@@ -165,7 +164,6 @@ __device__ void take_pages(const PoolArgs &a, Take &t) {
                 const int p = base + threadIdx.x * kScan + i;
                 a.table[t.at[e] + (rank - t.start[e])] = p;
                 a.refs[p] = 1;
-                t.found = p;
             }
             ++rank;
         }
@@ -179,16 +177,13 @@ __global__ __launch_bounds__(kBookThreads) void reserve_kernel(PoolArgs a) {
     __shared__ Take t;
     __shared__ int seq[kMaxSegments], want[kMaxSegments], have[kMaxSegments];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    if (threadIdx.x < a.n) {
-        const int i = threadIdx.x, rows = a.rows[i];
-        seq[i] = a.dst[i];
+    if (wave == 0) {
+        const int rows = lane < a.n ? a.rows[lane] : 0, s = lane < a.n ? a.dst[lane] : -1;
         const int64_t pages = ((int64_t)max(rows, 0) + (1 << a.page_shift) - 1) >> a.page_shift;
-        want[i] = pages <= a.max_pages && seq[i] >= 0 && seq[i] < a.nseq ? (int)pages : -1;
+        bool ok = pages <= a.max_pages && s >= 0 && s < a.nseq;
+        for (int j = 0; j < a.n; ++j) ok &= j >= lane || __builtin_amdgcn_readlane(s, j) != s;
+        if (lane < a.n) seq[lane] = s, want[lane] = ok ? (int)pages : -1;
     }
-    __syncthreads();
-    if (threadIdx.x < a.n)
-        for (int j = 0; j < (int)threadIdx.x; ++j)
-            if (seq[j] == seq[threadIdx.x]) want[threadIdx.x] = -1;
     __syncthreads();
     for (int i = wave; i < a.n; i += kBookThreads / 64) {
         int run = 0;  // leading entries that name a page
@@ -217,20 +212,18 @@ __global__ __launch_bounds__(kBookThreads) void fork_kernel(PoolArgs a) {
     __shared__ Take t;
     __shared__ int src[kMaxSegments], dst[kMaxSegments], full[kMaxSegments], last[kMaxSegments], valid[kMaxSegments];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    if (tid < a.n) {
-        const int rows = a.rows[tid], page = 1 << a.page_shift;
-        src[tid] = a.src[tid];
-        dst[tid] = a.dst[tid];
-        full[tid] = max(rows, 0) >> a.page_shift;
-        last[tid] = max(rows, 0) & (page - 1) ? 0 : -1;  // whether a page is filled in part
-        const int64_t pages = ((int64_t)max(rows, 0) + page - 1) >> a.page_shift;
-        valid[tid] = pages <= a.max_pages && src[tid] >= 0 && src[tid] < a.nseq && dst[tid] >= 0 && dst[tid] < a.nseq;
-    }
-    __syncthreads();
-    if (tid < a.n) {
-        int v = valid[tid];
-        for (int j = 0; j < a.n; ++j) v &= src[j] != dst[tid] && (j >= tid || dst[j] != dst[tid]);
-        valid[tid] = v;
+    if (wave == 0) {
+        const int rows = lane < a.n ? max(a.rows[lane], 0) : 0, page = 1 << a.page_shift;
+        const int f = lane < a.n ? a.src[lane] : -1, to = lane < a.n ? a.dst[lane] : -1;
+        const int64_t pages = ((int64_t)rows + page - 1) >> a.page_shift;
+        bool ok = pages <= a.max_pages && f >= 0 && f < a.nseq && to >= 0 && to < a.nseq;
+        for (int j = 0; j < a.n; ++j)
+            ok &= __builtin_amdgcn_readlane(f, j) != to && (j >= lane || __builtin_amdgcn_readlane(to, j) != to);
+        if (lane < a.n) {
+            src[lane] = f, dst[lane] = to, valid[lane] = ok;
+            full[lane] = rows >> a.page_shift;
+            last[lane] = rows & (page - 1) ? 0 : -1;  // whether a page is filled in part
+        }
     }
     __syncthreads();
     // the former pages of the slots that are filled are let go, the shared ones counted
@@ -257,7 +250,6 @@ __global__ __launch_bounds__(kBookThreads) void fork_kernel(PoolArgs a) {
             t.at[i] = (long long)(valid[i] ? dst[i] : 0) * a.max_pages + full[i];
         }
     }
-    __threadfence();
     take_pages(a, t);
     for (int i = wave; i < a.n; i += kBookThreads / 64) {
         if (!valid[i] || t.start[i] >= 0) continue;  // no page was left for this one: its slot stays empty
@@ -292,56 +284,79 @@ __global__ __launch_bounds__(kThreads) void release_kernel(PoolArgs a) {
 // ---------------------------------------------------------------------------
 // Compaction.  The i-th lowest free page takes the i-th highest used one
 // while it lies below it: the fewest moves that leave the used pages together
-// at the front, and no page is both read and written.  Three launches: used
-// pages of each chunk; ranks; pairs, counts and tables.
+// at the front, and no page is both read and written.  Two launches: ranks, then
+// pairs, counts and tables; in a large pool the chunks' used pages before them.
 // ---------------------------------------------------------------------------
-constexpr int kChunk = kThreads * 16;  // pages of a workgroup
+constexpr int kPerThread = 16;
+constexpr int kChunk = kThreads * kPerThread;  // pages of a workgroup
+constexpr int kDirect = 16384;  // pages up to which every workgroup counts the used ones of all chunks for itself
+
+__device__ __forceinline__ int block_sum(int v, int *part) {
+    v = wave_sum_int(v);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return part[0] + part[1] + part[2] + part[3];
+}
 
 __global__ __launch_bounds__(kThreads) void count_kernel(CompactArgs a) {
     __shared__ int part[kThreads / 64];
     int n = 0;
-    for (int i = 0; i < kChunk / kThreads; ++i) {
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
         const int p = blockIdx.x * kChunk + i * kThreads + threadIdx.x;
         n += p < a.num_pages && a.refs[p] > 0;
     }
-    n = wave_sum_int(n);
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = n;
-    __syncthreads();
-    if (threadIdx.x == 0) a.chunk[blockIdx.x] = part[0] + part[1] + part[2] + part[3];
+    n = block_sum(n, part);
+    if (threadIdx.x == 0) a.chunk[blockIdx.x] = n;
 }
 
 __global__ __launch_bounds__(kThreads) void rank_kernel(CompactArgs a) {
-    __shared__ int part[2][kThreads / 64], run[kThreads / 64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int before = 0, all = 0;
-    for (int c = threadIdx.x; c < a.chunks; c += kThreads) {
-        const int n = a.chunk[c];
-        all += n;
-        before += c < (int)blockIdx.x ? n : 0;
-    }
-    all = wave_sum_int(all);
-    before = wave_sum_int(before);
-    if (lane == 0) part[0][wave] = all, part[1][wave] = before;
-    __syncthreads();
-    all = part[0][0] + part[0][1] + part[0][2] + part[0][3];
-    before = part[1][0] + part[1][1] + part[1][2] + part[1][3];
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.chunk[a.chunks] = all;
-    for (int i = 0; i < kChunk / kThreads; ++i) {
-        const int p = blockIdx.x * kChunk + i * kThreads + threadIdx.x;
-        const bool used = p < a.num_pages && a.refs[p] > 0;
-        const int incl = wave_incl_scan(used);
-        if (lane == 63) run[wave] = incl;
-        __syncthreads();
-        int u = before + incl - used;  // used pages below p
-        for (int w = 0; w < kThreads / 64; ++w) {
-            if (w < wave) u += run[w];
-            before += run[w];
+    constexpr int kWaves = kThreads / 64;
+    static_assert(kPerThread * kWaves == 64, "one wave scans the counts of all 64 runs of 64 pages");
+    __shared__ int part[2][kWaves], run[kPerThread * kWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, p0 = blockIdx.x * kChunk + threadIdx.x;
+    int v[kPerThread];
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) v[i] = p0 + i * kThreads < a.num_pages ? a.refs[p0 + i * kThreads] : 0;
+    int below = 0, all = 0;  // used pages of the chunks before this one, and of all
+    if (a.num_pages <= kDirect) {
+        for (int b = 0; b < a.num_pages; b += kChunk) {
+            int x[kPerThread];
+#pragma unroll
+            for (int i = 0; i < kPerThread; ++i) x[i] = b + i * kThreads + (int)threadIdx.x < a.num_pages ? a.refs[b + i * kThreads + threadIdx.x] : 0;
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < kPerThread; ++i) n += x[i] > 0;
+            all += n;
+            below += b < (int)blockIdx.x * kChunk ? n : 0;
         }
-        __syncthreads();
+    } else {
+        for (int c = threadIdx.x; c < a.chunks; c += kThreads) {
+            const int n = a.chunk[c];
+            all += n;
+            below += c < (int)blockIdx.x ? n : 0;
+        }
+    }
+    uint64_t used[kPerThread];
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+        used[i] = __ballot(v[i] > 0);
+        if (lane == 0) run[i * kWaves + wave] = __popcll(used[i]);
+    }
+    all = block_sum(all, part[0]);
+    below = block_sum(below, part[1]);
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.chunk[a.chunks] = all;
+    const int mine = run[lane], before = below + wave_incl_scan(mine) - mine;  // of run `lane`
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+        const int p = p0 + i * kThreads;
+        // used pages below p
+        const int u = __shfl(before, i * kWaves + wave) + __popcll(used[i] & ((1ull << lane) - 1));
         if (p >= a.num_pages) continue;
-        const int rank = used ? all - 1 - u : p - u;  // from the top, or from the bottom
-        a.rank[p] = used ? rank : -1;
-        if (rank < a.most) (used ? a.high : a.low)[rank] = p;
+        const bool is = (used[i] >> lane) & 1;
+        const int rank = is ? all - 1 - u : p - u;  // from the top, or from the bottom
+        a.rank[p] = is ? rank : -1;
+        if (rank < a.most) (is ? a.high : a.low)[rank] = p;
     }
 }
 
@@ -388,12 +403,12 @@ __global__ __launch_bounds__(kThreads) void copy_kernel(CopyArgs a) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const size_t at = in + (j * kThreads + threadIdx.x) * 16;
-            if (at < a.page_bytes) v[j] = *reinterpret_cast<const u32x4 *>(s + at);
+            if (at < a.page_bytes) v[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(s + at));
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const size_t at = in + (j * kThreads + threadIdx.x) * 16;
-            if (at < a.page_bytes) *reinterpret_cast<u32x4 *>(d + at) = v[j];
+            if (at < a.page_bytes) __builtin_nontemporal_store(v[j], reinterpret_cast<u32x4 *>(d + at));
         }
     }
 }
@@ -441,7 +456,7 @@ hipError_t launch_compact(CompactArgs a, int32_t *ws, hipStream_t s) {
     a.low = a.chunk + a.chunks + 1;
     a.high = a.low + a.most;
     a.rank = a.high + a.most;
-    hipLaunchKernelGGL(count_kernel, dim3(a.chunks), dim3(kThreads), 0, s, a);
+    if (a.num_pages > kDirect) hipLaunchKernelGGL(count_kernel, dim3(a.chunks), dim3(kThreads), 0, s, a);
     hipLaunchKernelGGL(rank_kernel, dim3(a.chunks), dim3(kThreads), 0, s, a);
     const int64_t n = (int64_t)a.nseq * a.max_pages > a.max_moves ? (int64_t)a.nseq * a.max_pages : a.max_moves;
     hipLaunchKernelGGL(move_kernel, dim3((unsigned)((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, s, a);
