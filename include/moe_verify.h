@@ -499,7 +499,8 @@ int kv4_copy_pages(const moe_kv4_cache *cache, const int32_t *pairs, int32_t n, 
  * results; a k or v that is no finite number may make any result of its
  * sequence and head NaN.
  * Limits: 0 <= T, Tk <= 2^22, D 64, 128 or 256, Hq a multiple of Hkv, at most
- * 8192, strides up to 2^24 elements. */
+ * 8192, strides of k and v up to 2^24 elements, below 2^23 blocks of 128 rows of
+ * a head, float32 K below 2^33 elements.  Errors: EINVAL, ENOTSUP, EWORKSPACE. */
 size_t prompt_attend_workspace_bytes(int32_t nseq, const int32_t *q_off, const int32_t *k_off, int32_t Hq, int32_t Hkv,
                                      int32_t D, int32_t dtype);
 int prompt_attend(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
@@ -533,7 +534,8 @@ int route_tokens(const float *logits, int64_t stride, int32_t T, int32_t E, int3
  * activations enter the products as three bf16 terms (24 bits).  An fp8 block scale of 0 or below 2^-126 counts as
  * 2^-127.  Results do not depend on the order in which a call's workgroups run.
  * Limits: 0 <= T <= 2^20, 1 <= k <= min(E, MOE_MAX_TOPK), E <= MOE_MAX_EXPERTS; bf16: H a multiple of 64 and I of
- * 32; fp8: H, I multiples of 128.  Errors: EINVAL, ENOTSUP (float32 weights), EWORKSPACE. */
+ * 32; fp8: H, I multiples of 128; T * H below 2^33.  Errors: EINVAL, ENOTSUP
+ * (float32 weights, a call too large for one grid), EWORKSPACE. */
 size_t moe_experts_workspace_bytes(const moe_layer *layer, int32_t T, int32_t dtype);
 int moe_experts(const moe_layer *layer, const void *x, int64_t x_stride, int32_t T, int32_t dtype,
                 const int32_t *topk_idx, const float *topk_w, void *y, void *ws, size_t ws_bytes, void *stream);

@@ -968,6 +968,12 @@ def accept_drafts(logits, tokens, offsets, u, *, parent=None, draft_probs=None, 
 # ---------------------------------------------------------------------------
 # Prompts: rows and pages of the cache, experts of many tokens
 # ---------------------------------------------------------------------------
+def _cache_device(cache: KV4Cache):
+    if not getattr(cache.data, "is_cuda", False):
+        raise ValueError("cache.data must be a device tensor")
+    return cache.data.device
+
+
 def kv4_read(cache: KV4Cache, table, start, offsets, *, dtype=None, out=None, stream=None):
     """Rows of the cache as dense (k, v) [T, Hkv, D], the values that the
     codes stand for: row t = offsets[s] + j is position start[s] + j of
@@ -976,7 +982,7 @@ def kv4_read(cache: KV4Cache, table, start, offsets, *, dtype=None, out=None, st
     float32 or bfloat16 (the default).  out: a pair of dense tensors to write
     to (their dtype counts)."""
     import torch
-    dev = cache.data.device
+    dev = _cache_device(cache)
     c = cache._c(dev)
     r, _ = _kv_rows(table, start, offsets, dev)
     T = r._keep[len(r._keep) - 1]
@@ -1080,7 +1086,7 @@ def kv4_copy_pages(cache: KV4Cache, pairs, *, stream=None) -> None:
     """Copy page pairs[i][0] of the cache to page pairs[i][1] (int32 [n, 2]
     device tensor); pairs outside the pool copy nothing."""
     import torch
-    dev = cache.data.device
+    dev = _cache_device(cache)
     c = cache._c(dev)
     n = pairs.shape[0] if hasattr(pairs, "shape") and len(pairs.shape) else 0
     _dense(pairs, "pairs", torch.int32, (n, 2), dev)

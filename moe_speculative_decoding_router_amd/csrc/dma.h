@@ -18,7 +18,7 @@ __device__ __forceinline__ unsigned lds_address(const void *p) {
     return __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)(const __attribute__((address_space(3))) void *)p);
 }
 
-// 16 bytes a lane from base + offset (a byte offset below 2^31 of each lane's
+// 16 bytes a lane from base + offset (a byte offset below 2^32 of each lane's
 // own) to LDS address at + 16 lane.
 __device__ __forceinline__ void dma16(const void *base, unsigned offset, unsigned at) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(offset), "s"(base) : "memory");

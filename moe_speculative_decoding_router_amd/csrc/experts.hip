@@ -4,6 +4,7 @@
 #include "dma.h"
 #include "prompt.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace moe {
@@ -559,17 +560,21 @@ __global__ __launch_bounds__(kListThreads) void combine_rows_kernel(Plan p) {
     }
 }
 
+// Workgroups of a product: tiles at most, since every used expert's last one is filled in part.
+int64_t product_grid(const ExpertArgs &a, bool gate_up, int TM, int TN) {
+    const int64_t M = gate_up ? 2 * (int64_t)a.I : a.H, mblocks = (M + TM - 1) / TM, pairs = (int64_t)a.T * a.k;
+    const int64_t used = a.E < pairs ? a.E : pairs;
+    const int64_t tiles = pairs / TN + used + (a.shared ? (a.T + TN - 1) / TN : 0);
+    return (tiles * mblocks + 7) / 8 * 8;
+}
+
 template <typename S>
 hipError_t launch_product(const Plan &p, hipStream_t s) {
     if (S::kLds > 65536) {
         const hipError_t e = allow_lds<product_kernel<S>>(S::kLds);
         if (e != hipSuccess) return e;
     }
-    const int64_t M = S::kGateUp ? 2 * p.a.I : p.a.H, mblocks = (M + S::TM - 1) / S::TM;
-    // tiles at most: every used expert's last one is filled in part
-    const int64_t used = p.a.E < p.pairs ? p.a.E : p.pairs;
-    const int64_t tiles = p.pairs / S::TN + used + (p.a.shared ? (p.a.T + S::TN - 1) / S::TN : 0);
-    const int64_t grid = (tiles * mblocks + 7) / 8 * 8;
+    const int64_t grid = product_grid(p.a, S::kGateUp, S::TM, S::TN);
     hipLaunchKernelGGL(product_kernel<S>, dim3((unsigned)grid), dim3(S::kThreads), S::kLds, s, p);
     return hipGetLastError();
 }
@@ -627,6 +632,12 @@ size_t lay_out(const ExpertArgs &a, uint8_t *ws, Plan *p) {
 }
 
 }  // namespace
+
+bool experts_fit(const ExpertArgs &a) {
+    const int TN = tile_rows(a), TM = TN == 32 ? 64 : TN == 128 ? 128 : 256;
+    const int64_t grid = std::max(product_grid(a, true, TM, TN), product_grid(a, false, TM, TN));
+    return grid < 1 << 22 && (int64_t)a.T * a.H < (int64_t)1 << 33;
+}
 
 size_t experts_ws_bytes(const ExpertArgs &a) { return lay_out(a, nullptr, nullptr); }
 

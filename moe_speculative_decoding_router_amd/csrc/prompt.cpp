@@ -54,7 +54,10 @@ int plan_prompt(int nseq, const int32_t *q_off, const int32_t *k_off, int Hq, in
     a->G = Hq / Hkv;
     a->D = D;
     a->f32 = dtype == MOE_F32;
+    if (a->f32 && (int64_t)a->k_off[nseq] * Hkv * D >= ((int64_t)1 << 33))
+        return fail(MOE_ENOTSUP, "float32 K and V of 2^33 elements or more");
     *need = prompt_plan(*a, device_cu_count());
+    if (a->units >= 1 << 23) return fail(MOE_ENOTSUP, "rows and heads of one call above 2^23 blocks of 128 rows");
     return MOE_OK;
 }
 
@@ -82,6 +85,7 @@ int check_experts(const moe_layer *L, int T, int dtype, ExpertArgs *a) {
     a->s_d = L->s_d;
     a->ssh_gu = L->ssh_gu;
     a->ssh_d = L->ssh_d;
+    if (!experts_fit(*a)) return fail(MOE_ENOTSUP, "T=%d tokens of this layer are more than one call's grid holds", T);
     return MOE_OK;
 }
 

@@ -84,6 +84,7 @@ struct ExpertArgs {
     const float *s_gu, *s_d, *ssh_gu, *ssh_d;
     void *ws;
 };
+bool experts_fit(const ExpertArgs &a);  // whether the grids of a call are below HIP's limit
 size_t experts_ws_bytes(const ExpertArgs &a);
 hipError_t launch_experts(const ExpertArgs &a, hipStream_t s);
 

@@ -416,7 +416,7 @@ size_t prompt_plan(PromptArgs &a, int n_cu) {
         a.blocks[s + 1] = blocks;
         if (n > 0 && m > keys) keys = m;
     }
-    a.units = blocks * a.Hq;
+    a.units = (int64_t)blocks * a.Hq < INT32_MAX ? blocks * a.Hq : INT32_MAX;
     a.parts = 1;
     // Units that fill the workgroups that run at once a few times over at most leave some idle in the
     // last round.  Their keys are cut into as many shares of at least 256 as take the least time, by
