@@ -408,7 +408,7 @@ int kv4_attend(const moe_kv4_cache *cache, const moe_kv4_rows *rows, const void 
  * row t = seg_off[s] + j is position len[s] + j of sequence s (the beginning
  * of a prompt that stands already: len 0), rows without a page are zeros.
  *   k, v [T, Hkv, D] out in dtype MOE_F32 or MOE_BF16 (exact in both), dense
- * Limits: 0 <= T <= 2^22.  Errors: EINVAL, ENOTSUP (D, dtype). */
+ * Limits: 0 <= T <= 2^22, T * Hkv <= 2^28.  Errors: EINVAL, ENOTSUP. */
 int kv4_read(const moe_kv4_cache *cache, const moe_kv4_rows *rows, void *k, void *v, int32_t T, int32_t dtype,
              void *stream);
 

@@ -14,10 +14,12 @@ constexpr int kThreads = 256;
 // Read.  The inverse of append: a lane holds 8 consecutive elements of a row
 // (4 code bytes in, 16 or 32 bytes out), a wave 512 / D consecutive rows of
 // one head, kReadAhead times over so that its loads are under way together.
-// K and V are the grid's z.  Memory bounds it: 100001 bf16 rows of 8 heads of 128
-// (109 MB read, 409 MB written) take 87 us, 5.9 TB/s.  The results are stored past the
-// caches: through them the same rows take 155 us.  With 2 or 8 in the place of
-// kReadAhead 87 and 88 us.
+// Memory bounds it, cold: 100001 bf16 rows of 8 heads of 128 (109 MB read, 409 MB
+// written) take 139 us (3.7 TB/s) where the pages come from HBM, 87 (5.9 TB/s)
+// where they are still in the last-level cache.  The heads of the same rows run
+// side by side, so that what is written lies together (one head after the other
+// 148 us), and results are stored past the caches (through them 153; 155 instead of
+// 87).  With 8 or 16 in the place of kReadAhead 141 and 149 us.
 // ---------------------------------------------------------------------------
 constexpr int kReadAhead = 4;
 
@@ -25,10 +27,10 @@ template <int D, bool F32>
 __global__ __launch_bounds__(kThreads) void read_kernel(KvReadArgs a) {
     constexpr int LPR = D / 8, RPW = 64 / LPR, W = D / 32;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int h = blockIdx.y;
-    const bool isv = blockIdx.z != 0;
+    const int h = blockIdx.x % a.r.Hkv;  // the heads of the same rows run side by side
+    const bool isv = blockIdx.y != 0;
     const int l = lane % LPR;
-    const int t0 = (blockIdx.x * (kThreads / 64) + wave) * RPW * kReadAhead + lane / LPR;
+    const int t0 = (blockIdx.x / a.r.Hkv * (kThreads / 64) + wave) * RPW * kReadAhead + lane / LPR;
     unsigned word[kReadAhead], sc[kReadAhead];
 #pragma unroll
     for (int u = 0; u < kReadAhead; ++u) {
@@ -417,7 +419,7 @@ __global__ __launch_bounds__(kThreads) void copy_kernel(CopyArgs a) {
 
 hipError_t launch_kv4_read(const KvReadArgs &a, hipStream_t s) {
     const int rows = kThreads / 64 * (512 / a.r.D) * kReadAhead;
-    const dim3 grid((a.T + rows - 1) / rows, a.r.Hkv, 2);
+    const dim3 grid((a.T + rows - 1) / rows * a.r.Hkv, 2);
     void (*k)(KvReadArgs) = nullptr;
     if (a.r.D == 64) k = a.f32 ? read_kernel<64, true> : read_kernel<64, false>;
     else if (a.r.D == 128) k = a.f32 ? read_kernel<128, true> : read_kernel<128, false>;

@@ -112,6 +112,7 @@ int kv4_read(const moe_kv4_cache *cache, const moe_kv4_rows *rows, void *k, void
     if (rc == MOE_OK) rc = check_dtype(dtype);
     if (rc != MOE_OK) return rc;
     if (T == 0) return MOE_OK;
+    if ((int64_t)T * a.r.Hkv > (1 << 28)) return fail(MOE_ENOTSUP, "T * Hkv above 2^28");
     if (!k || !v) return fail(MOE_EINVAL, "k and v must be non-NULL");
     if (misaligned(k, 16) || misaligned(v, 16)) return fail(MOE_EINVAL, "k and v must be 16-byte aligned");
     a.k = k;

@@ -118,6 +118,7 @@ def test_read_and_copy(lib):
            ({"c": cache(Hkv=0)}, -1, b"Hkv"), ({"c": cache(data=None)}, -1, b"data"), ({"c": cache(data=P + 8)}, -1, b"aligned")]
     refused(lib, read, bad + [({"k": None}, -1, b"k and v"), ({"v": P + 8}, -1, b"aligned"), ({"T": 4}, -1, b"seg_off"), ({"T": -1}, -1, b"T=-1"),
                               ({"T": (1 << 22) + 1}, -1, b"2^22"), ({"dtype": 2}, -2, b"dtype"), ({"r": rows(0, 3, table=None)}, -1, b"table"),
+                              ({"c": cache(Hkv=1024), "r": rows(0, 1 << 22), "T": 1 << 22}, -2, b"2^28"),
                               ({"r": rows(0, 3, start=None)}, -1, b"len"), ({"r": rows(0, 3, max_pages=0)}, -1, b"max_pages")])
     refused(lib, copy, bad + [({"pairs": None}, -1, b"pairs"), ({"n": -1}, -1, b"n=-1"), ({"n": (1 << 24) + 1}, -1, b"2^24")])
     assert read(lib, r=rows(0, 0), T=0, k=None, v=None) == 0 and copy(lib, n=0, pairs=None) == 0
