@@ -15,6 +15,7 @@ namespace {
 // floats'; k rounds of a wave maximum, each taking the lowest index that holds
 // it, so that lane r ends with rank r.
 // ---------------------------------------------------------------------------
+// Latency bounds it: 65 tokens of 128 experts take 3.7 us, 16384 of 256 (17 MB) 10.
 constexpr int kRouteThreads = 256;
 
 // Monotone image of a float: NaN as -inf, +inf as the largest, both zeros the
@@ -82,6 +83,32 @@ __global__ __launch_bounds__(kRouteThreads) void route_tokens_kernel(const float
 // The experts' products.  The (token, rank) pairs are grouped by expert (rows
 // of the products); gate-up makes the hidden activations of every row, down
 // their outputs, combine the tokens' weighted sums in rank order.
+//
+// Weights are the A operand of v_mfma_f32_16x16x32_bf16: the packed tiles come
+// into LDS as they are and are read from it 16 bytes a lane, without a bank met
+// twice; activations are the B operand, gathered by row straight into LDS, 128 bytes
+// a row and load.  An fp8 tile is converted to bf16 in registers, exactly, times
+// the power of two of its block's scale; what is left of the scale, a factor in
+// [1, 2), is kept out of the sums, which are multiplied by the quotient of two
+// blocks' factors when the block changes, every 128 k: no second set of
+// accumulators, and no quotient that overflows.
+//
+// What is rounded in bf16 calls: the hidden activations (each by at most 2^-8) and
+// the result.  The experts' outputs stay float32 until they are added: as bf16
+// they would save 90 MB of the 378 that 16396 rows of 2880 write and read, but the
+// results would be off by 0.0029 of their norm instead of 0.0023 (plain float32 ones that
+// are rounded once: 0.0017).
+//
+// What bounds it: 4099 tokens, 4 of 32 experts of 2880 x 2880 (816 GFLOP) take 900 to
+// 930 us, of which gate-up 560 (970 TFLOP/s) and down 330 (825), where a large bf16
+// product reaches 1352; 40 go to adding 190 MB of outputs, 9 to the lists.  Matrix
+// instructions are under way 52% of the cycles: compute units idle 20% of the
+// time behind the last of their six or seven tiles, and the clock falls to 1.9 GHz.
+// fp8, 1024 tokens, 8 of 32 experts of 7168 x 2048 and a shared one (812 GFLOP): 960 to 1040.
+// Tried and slower: workgroups that stay and draw tiles by ticket (bf16 964), tiles
+// of half the rows at the end of the list (958), 128 x 512 tiles (1055; the
+// activations no longer stay in the L2), v_mfma_f32_32x32x16_bf16 (940), row blocks
+// dealt to the XCDs in turn (908), outputs stored past the caches (962).
 // ---------------------------------------------------------------------------
 constexpr int kListThreads = 256;
 constexpr int kMinChunk = 2048;  // pairs of a workgroup at least
@@ -281,6 +308,9 @@ struct Frags {
 
 template <typename S, int JN>
 __device__ __forceinline__ void multiply(const Plan &p, const Job &job, uint8_t *lds) {
+    // A row's place among its expert's tiles, and so the loop that it goes through, is left to the order
+    // of atomics: all loops have to round alike, so none may fuse a product into the rest it leaves.
+#pragma clang fp contract(off)
     constexpr bool GU = S::kGateUp, FP8 = S::FP8;
     constexpr int NT = S::NT, MT = S::MT, NA = S::NA(JN), NB = S::NB(JN), PA = S::PA, PB = S::PB(JN), kLoads = PA + PB * NT;
     constexpr int kPlane = PB * S::kWaves * 1024, kB0 = NA * S::A;  // the activations' buffers lie behind the weights'
@@ -596,10 +626,17 @@ hipError_t launch_products(const Plan &p, hipStream_t s) {
     return launch_both<FP8, 1, 256, 256, 2, 4, 163840>(p, s);
 }
 
-// Rows of a product tile, by the rows that an expert has on average.
+// Rows of a product tile: large ones where experts have some rows on average and
+// their tiles are enough to fill half the card, small ones (32 rows by 64
+// weight rows) else.  us a call, small and large: 32 experts of 2048 x 1024, bf16, 24
+// rows each 90 and 89, 48 rows 110 and 94, 128 rows 196 and 109 (float32 111 and 101, 142
+// and 111, 287 and 215); 60 of 1024 x 512, 24 rows 45.6 and 46.3, 32 rows 50.9 and 47.8;
+// 8 of 1024 x 512 (32 large tiles), 32 rows 21.2 and 24.6, 160 rows 28.1 and 42.7.
 int tile_rows(const ExpertArgs &a) {
-    const int64_t avg = (int64_t)a.T * a.k / a.E;
-    return avg <= 48 ? 32 : a.f32 ? 128 : 256;
+    const int64_t pairs = (int64_t)a.T * a.k;
+    const int large = a.f32 ? 128 : 256;
+    const int64_t tiles = std::max(pairs / large, (int64_t)a.E) * ((2 * (int64_t)a.I + large - 1) / large);
+    return pairs / a.E < 28 || tiles < 128 ? 32 : large;
 }
 
 size_t lay_out(const ExpertArgs &a, uint8_t *ws, Plan *p) {

@@ -87,6 +87,36 @@ __global__ __launch_bounds__(kThreads) void split_kernel(const float *k, const f
     }
 }
 
+// ---------------------------------------------------------------------------
+// One workgroup takes 128 query rows of a head, 32 a wave, and goes over their
+// keys in steps of 64 (32 at D = 256 and for float32) with a running maximum
+// and sum.  S^T = K Q^T leaves lane (half, c) with the scores of query c, keys
+// 8 x + 4 half .. + 3 of each 32; O^T += V^T P^T takes its operand in just that order
+// once V's rows are read in it too (ds_read_b64_tr_b16, which transposes 4 rows
+// of 16 columns), so probabilities never leave the lane, and the maximum and sum belong
+// to column c in both products.  The maximum moves only when a score passes it by
+// 2^8, so most steps need no exchange between lanes.  K and V tiles come
+// straight into LDS a step ahead; V is read before the softmax and K four products
+// ahead, so that their latency is hidden.  Hidden keys are masked in the steps that
+// hold some; a wave whose rows see none of a step's keys leaves it out.
+//
+// Probabilities are rounded to bf16 for the second product, each by at most 2^-8
+// of itself, and the sum is taken of the rounded ones (two at a time, v_dot2): the
+// results are off by 0.0020 to 0.0023 of their norm, plain float32 ones that are
+// rounded to bf16 by 0.0016 to 0.0017.  float32 operands are three bf16 terms each
+// (K and V in planes that split_kernel writes), of whose nine products the six
+// above 2^-24 are taken: 1e-7 of the norm.
+//
+// What bounds it: matrix and vector instructions of the two workgroups of a
+// compute unit hardly overlap.  12000 rows of six prompts, 64 heads on 4 of 128
+// (614 GFLOP) take 671 us, 915 TFLOP/s, where a large bf16 product reaches 1352;
+// matrix instructions are under way 50% of the cycles and vector instructions
+// 46%, and each 32 rows read a step's whole K and V from LDS (61% of its rate).
+// 64 rows a wave would halve that, at one wave a SIMD and with the softmax
+// placed by hand.  Wave priorities, of the softmax over the products or the other
+// way, cost 1% to 3%.  515 rows behind 60001 (508 GFLOP) take 570 to 595 us in three
+// shares a unit.  float32 at D = 256 spills 200 registers a lane, which is left.
+// ---------------------------------------------------------------------------
 template <int D, int NT>
 __global__ __launch_bounds__(kThreads, groups(D, NT)) void prompt_kernel(PromptArgs a) {
     constexpr int BK = tile_keys(D, NT), NB = buffers(D, NT), TB = tile_bytes(D, NT);

@@ -187,6 +187,20 @@ def test_strides_in_place_guards_and_repeats():
     assert m.experts(x[:0], L.w, idx[:0], w[:0]).shape == (0, 192)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("wdtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("T,E", [(37, 4), (400, 8), (1500, 40)])
+def test_every_call_gives_the_same_bits(T, E, wdtype, dtype):
+    """Rows lie in another place of their expert's tiles in every call, in tiles filled to any part."""
+    L = Layer(18, 256, 256, E, 2, wdtype, shared=True)
+    x, idx, w = L.inputs(9, T, dtype)
+    ref = L.check(x, idx, w)
+    for _ in range(15):
+        assert torch.equal(m.experts(x, L.w, idx, w), ref)
+    order = torch.randperm(T, device=DEV)
+    assert torch.equal(m.experts(x[order].contiguous(), L.w, idx[order].contiguous(), w[order].contiguous()), ref[order])
+
+
 def test_neighbours_that_are_no_numbers():
     """A token's NaN stays its own."""
     L = Layer(15, 128, 64, 3, 1)
