@@ -497,7 +497,10 @@ int kv4_copy_pages(const moe_kv4_cache *cache, const int32_t *pairs, int32_t n, 
  * second product rounded to bf16.  float32: all operands enter the products as
  * three bf16 terms (24 bits).  Rows of one sequence do not touch another's
  * results; a k or v that is no finite number may make any result of its
- * sequence and head NaN.
+ * sequence and head NaN.  A row of a head whose query holds NaN or an infinity, or whose
+ * visible scores hold NaN, +inf or nothing but -inf in float32, is NaN, and
+ * touches no other row; rows that see nothing are zeros all the same.  Above
+ * 2^29 in magnitude a row's scores may make it NaN.
  * Limits: 0 <= T, Tk <= 2^22, D 64, 128 or 256, Hq a multiple of Hkv, at most
  * 8192, strides of k and v up to 2^24 elements, below 2^23 blocks of 128 rows of
  * a head, float32 K below 2^33 elements.  Errors: EINVAL, ENOTSUP, EWORKSPACE. */

@@ -1099,8 +1099,8 @@ def prompt_attend(q, k, v, offsets, k_offsets=None, *, scale: Optional[float] = 
     keep their distance between tokens), sequences packed one behind the other:
     offsets (host) [nseq + 1] of the query rows, k_offsets of the keys (None:
     the same).  Row j of a sequence with n rows and m keys sees its first
-    j + 1 + (m - n) keys; a row that sees none gets zeros.  scale: default
-    D ** -0.5.  Returns out [T, Hq, D] in q's type.  workspace: a uint8 device
+    j + 1 + (m - n) keys; a row that sees none gets zeros, one whose query
+    holds NaN gives NaN.  scale: default D ** -0.5.  Returns out [T, Hq, D] in q's type.  workspace: a uint8 device
     tensor of prompt_attend_workspace_bytes, one per stream; None allocates."""
     import torch
     dtype, qs = _rows_dtype(q, "q", 3)

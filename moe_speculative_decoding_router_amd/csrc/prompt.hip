@@ -366,7 +366,8 @@ __global__ __launch_bounds__(kThreads, groups(D, NT)) void prompt_kernel(PromptA
             }
         return;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    // Zeros are for rows that see no key; a sum that is NaN, or 0 because every score is -inf, gives NaN.
+    const float inv = 1.f / l;
     const size_t at = (tok * a.Hq + u.h) * D + 4 * half;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
@@ -374,7 +375,7 @@ __global__ __launch_bounds__(kThreads, groups(D, NT)) void prompt_kernel(PromptA
         for (int g = 0; g < 4; ++g) {
             f32x4 y;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = l > 0.f ? o[d][4 * g + i] * inv : 0.f;
+            for (int i = 0; i < 4; ++i) y[i] = sees >= 0 ? o[d][4 * g + i] * inv : 0.f;
             if constexpr (NT > 1) {
                 *reinterpret_cast<f32x4 *>((float *)a.out + at + d * 32 + 8 * g) = y;
             } else {
@@ -406,10 +407,11 @@ __global__ __launch_bounds__(kThreads) void join_kernel(PromptArgs a) {
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] += f * w[p * step + e * 64 + lane];
     }
+    const int sees = u.row0 + i + u.m - u.n;  // the row's last key
     const size_t at = ((size_t)(a.q_off[u.s] + u.row0 + i) * a.Hq + u.h) * D + lane;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        const float y = l > 0.f ? o[e] / l : 0.f;
+        const float y = sees >= 0 ? o[e] / l : 0.f;  // as in prompt_kernel
         if constexpr (F32) ((float *)a.out)[at + e * 64] = y;
         else ((__bf16 *)a.out)[at + e * 64] = (__bf16)y;
     }
