@@ -447,9 +447,10 @@ int kv4_reserve(const moe_kv4_pool *pool, const int32_t *seq, const int32_t *row
  *   pairs [n, 2] i32 out: (page, fresh page) for kv4_copy_pages; (-1, -1) where
  *         nothing is to be copied
  *   ok    [n] i32 out: 1 done.  0 if no page was free (dst[i] then holds
- *         nothing), or nothing was done: a name outside [0, nseq), rows[i] above
- *         a table's row, a dst[i] that an earlier entry names too, or that any
- *         entry names as its source. */
+ *         nothing), or nothing was done and dst[i] keeps what it held: a name outside
+ *         [0, nseq), rows[i] above a table's row, a source that has no page for
+ *         some of the rows, a dst[i] that an earlier entry names too, or that
+ *         any entry names as its source. */
 int kv4_fork(const moe_kv4_pool *pool, const int32_t *src, const int32_t *dst, const int32_t *rows, int32_t n,
              int32_t *pairs, int32_t *ok, void *stream);
 

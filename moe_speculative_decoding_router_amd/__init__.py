@@ -1049,7 +1049,8 @@ def kv4_fork(refs, table, page: int, src, dst, rows, *, stream=None):
     """Make sequence dst[i] hold the first rows[i] rows of sequence src[i]:
     whole pages are shared, one that is filled in part is replaced by a fresh
     page.  Returns (pairs [n, 2], ok [n]) int32: the pages to copy in each
-    layer's cache (kv4_copy_pages) and whether the entry was done."""
+    layer's cache (kv4_copy_pages) and whether the entry was done (not, among
+    other things, where the source does not hold all the rows)."""
     import torch
     p, dev = _pool(refs, table, page)
     n = _list(dev, src=src, dst=dst, rows=rows)

@@ -88,6 +88,7 @@ __global__ __launch_bounds__(kThreads) void read_kernel(KvReadArgs a) {
 // ---------------------------------------------------------------------------
 constexpr int kBookThreads = 1024;
 constexpr int kScan = 8;  // counts of a thread at a time in the search for free pages
+constexpr int kAhead = 8;  // table entries of a lane at a time in the search for missing ones
 
 struct Take {  // what the list's entries need, in LDS
     int need[kMaxSegments];      // fresh pages
@@ -231,25 +232,35 @@ __global__ __launch_bounds__(kBookThreads) void fork_kernel(PoolArgs a) {
     // the former pages of the slots that are filled are let go, the shared ones counted
     for (int i = wave; i < a.n; i += kBookThreads / 64) {
         int part = -1;
-        if (valid[i]) {
+        bool ok = valid[i];
+        const int32_t *from = a.table + (size_t)(ok ? src[i] : 0) * a.max_pages;
+        if (ok) {  // whether the source holds all the rows; no entry of the list writes to a source
+            const int pages = full[i] + (last[i] == 0);
+            bool miss = false;
+            for (int j0 = lane; j0 < pages; j0 += 64 * kAhead) {
+                int p[kAhead];
+#pragma unroll
+                for (int x = 0; x < kAhead; ++x) p[x] = j0 + 64 * x < pages ? from[j0 + 64 * x] : 0;
+#pragma unroll
+                for (int x = 0; x < kAhead; ++x) miss |= p[x] < 0 || p[x] >= a.num_pages;
+            }
+            ok = !__any(miss);
+        }
+        if (ok) {
             int32_t *to = a.table + (size_t)dst[i] * a.max_pages;
-            const int32_t *from = a.table + (size_t)src[i] * a.max_pages;
             for (int j = lane; j < a.max_pages; j += 64) {
-                const int old = to[j], p = from[j];
+                const int old = to[j], p = j < full[i] ? from[j] : -1;
                 if (old >= 0 && old < a.num_pages) atomicSub(a.refs + old, 1);
-                const bool live = p >= 0 && p < a.num_pages, share = live && j < full[i];
-                if (share) atomicAdd(a.refs + p, 1);
-                to[j] = share ? p : -1;
+                if (p >= 0 && p < a.num_pages) atomicAdd(a.refs + p, 1);
+                to[j] = p;
             }
-            if (last[i] == 0) {
-                const int p = from[full[i]];
-                part = p >= 0 && p < a.num_pages ? p : -1;
-            }
+            if (last[i] == 0) part = from[full[i]];
         }
         if (lane == 0) {
+            valid[i] = ok;
             last[i] = part;
             t.need[i] = part >= 0;
-            t.at[i] = (long long)(valid[i] ? dst[i] : 0) * a.max_pages + full[i];
+            t.at[i] = (long long)(ok ? dst[i] : 0) * a.max_pages + full[i];
         }
     }
     take_pages(a, t);

@@ -34,7 +34,8 @@ def reserve(refs, table, page, seq, rows):
 def fork(refs, table, page, src, dst, rows):
     n, width = len(src), len(table[0])
     valid = [0 <= src[i] < len(table) and 0 <= dst[i] < len(table) and dst[i] not in src and dst[i] not in dst[:i]
-             and -(-max(rows[i], 0) // page) <= width for i in range(n)]
+             and -(-max(rows[i], 0) // page) <= width
+             and all(_held(p, refs) for p in table[src[i]][:-(-max(rows[i], 0) // page)]) for i in range(n)]
     for i in range(n):
         if valid[i]:
             release(refs, table, page, [dst[i]], [0])
@@ -44,10 +45,9 @@ def fork(refs, table, page, src, dst, rows):
         if valid[i]:
             full = max(rows[i], 0) // page
             for j in range(full):
-                if _held(table[src[i]][j], refs):
-                    table[dst[i]][j] = table[src[i]][j]
-                    refs[table[src[i]][j]] += 1
-            if max(rows[i], 0) % page and _held(table[src[i]][full], refs):
+                table[dst[i]][j] = table[src[i]][j]
+                refs[table[src[i]][j]] += 1
+            if max(rows[i], 0) % page:
                 part[i] = table[src[i]][full]
     empty = []
     for i in range(n):
