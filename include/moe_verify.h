@@ -436,8 +436,9 @@ typedef struct {
  * its first one without a page on get the lowest free pages.  Entries of the
  * list are served in order, each whole or not at all.
  *   ok [n] i32 out: 1 if the sequence holds pages for its rows now; 0 if too
- *      few pages are free, or the table's row is too short, or seq[i] names no
- *      sequence or one that an earlier entry names */
+ *      few pages are free, or the table's row is too short, or has a page behind
+ *      a gap among the entries that the rows need (these calls leave no gaps), or
+ *      seq[i] names no sequence or one that an earlier entry names */
 int kv4_reserve(const moe_kv4_pool *pool, const int32_t *seq, const int32_t *rows, int32_t n, int32_t *ok, void *stream);
 
 /* Makes sequence dst[i] hold the first rows[i] rows of sequence src[i]: whole

@@ -178,7 +178,7 @@ __device__ void take_pages(const PoolArgs &a, Take &t) {
 
 __global__ __launch_bounds__(kBookThreads) void reserve_kernel(PoolArgs a) {
     __shared__ Take t;
-    __shared__ int seq[kMaxSegments], want[kMaxSegments], have[kMaxSegments];
+    __shared__ int seq[kMaxSegments], want[kMaxSegments];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     if (wave == 0) {
         const int rows = lane < a.n ? a.rows[lane] : 0, s = lane < a.n ? a.dst[lane] : -1;
@@ -189,22 +189,26 @@ __global__ __launch_bounds__(kBookThreads) void reserve_kernel(PoolArgs a) {
     }
     __syncthreads();
     for (int i = wave; i < a.n; i += kBookThreads / 64) {
-        int run = 0;  // leading entries that name a page
-        if (want[i] > 0) {
-            const int32_t *row = a.table + (size_t)seq[i] * a.max_pages;
-            for (; run < want[i]; run += 64) {
-                const int p = run + lane < want[i] ? row[run + lane] : -1;
-                const uint64_t bad = __ballot(p < 0 || p >= a.num_pages);
-                if (bad) {
-                    run += __ffsll((unsigned long long)bad) - 1;
-                    break;
-                }
+        const int n = want[i];
+        const int32_t *row = a.table + (size_t)(n > 0 ? seq[i] : 0) * a.max_pages;
+        int run = max(n, 0), held = -1;  // leading entries that name a page, and the last that does
+        for (int j0 = lane; j0 < n; j0 += 64 * kAhead) {
+            int p[kAhead];
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x) p[x] = j0 + 64 * x < n ? row[j0 + 64 * x] : -1;
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x) {
+                const int j = j0 + 64 * x;
+                if (p[x] >= 0 && p[x] < a.num_pages) held = j;
+                else run = min(run, j);
             }
         }
+        for (int x = 32; x > 0; x >>= 1) run = min(run, __shfl_xor(run, x)), held = max(held, __shfl_xor(held, x));
+        const bool gap = held > run;  // the pages behind it would be lost
         if (lane == 0) {
-            have[i] = run;
-            t.need[i] = want[i] > run ? want[i] - run : 0;
-            t.at[i] = (long long)(want[i] < 0 ? 0 : seq[i]) * a.max_pages + run;
+            if (gap) want[i] = -1;
+            t.need[i] = gap ? 0 : max(n, 0) - run;
+            t.at[i] = (long long)(n > 0 ? seq[i] : 0) * a.max_pages + run;
         }
     }
     take_pages(a, t);

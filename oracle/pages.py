@@ -22,6 +22,9 @@ def reserve(refs, table, page, seq, rows):
         have = 0
         while have < want and _held(table[s][have], refs):
             have += 1
+        if any(_held(p, refs) for p in table[s][have:want]):  # behind a gap
+            ok.append(0)
+            continue
         fresh = _free(refs)[:want - have]
         ok.append(int(len(fresh) == want - have))
         if ok[-1]:

@@ -1,5 +1,7 @@
 """Page calls that would lose rows or pages: forks of rows that the source does
-not hold."""
+not hold, and reservations in a row of the table with a gap."""
+import random
+
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -43,3 +45,54 @@ def test_one_missing_page_of_a_long_source(at, part):
     if part:
         p = pool_of(refs, [row[:800] + [-1], [-1] * W, [-1] * W], page)
         assert p.fork([0], [1], [rows]) == [0]
+
+
+@pytest.mark.parametrize("gap,behind", [(0, 1), (1, 799), (62, 64), (63, 65), (300, 301), (700, 799)])
+def test_reserve_in_a_row_with_a_gap(gap, behind):
+    """Nothing is taken where a page behind the gap would be overwritten; entries of the list around it are served."""
+    W, page = 801, 16
+    row = list(range(gap)) + [-1] * (W - gap)
+    row[behind] = behind
+    refs = [int(p in row) for p in range(W)] + [0] * 900
+    p = pool_of(refs, [[-1] * W, row, [-1] * W], page)
+    assert p.reserve([0, 1, 2], [40, page * 800, 33]) == [1, 0, 1]
+    assert p.reserve([1], [page * behind]) == [1]  # the gap filled up to the page behind it
+    assert p.reserve([1], [page * 801]) == [1]
+    counts = [0] * len(p.refs)
+    for r in p.table:
+        for x in r:
+            if x >= 0:
+                counts[x] += 1
+    assert counts == p.refs
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_random_tables_with_gaps(seed):
+    """Tables of any entries, counts that are theirs: after every call they still are, and equal to the oracle's."""
+    rnd = random.Random(seed)
+    P, S, W, page = rnd.choice([30, 400]), rnd.randint(2, 20), rnd.choice([3, 70, 130]), 16
+    table = [[rnd.choice([-1, rnd.randint(-2, P + 2)]) for _ in range(W)] for _ in range(S)]
+    refs = [0] * P
+    for r in table:
+        for x in r:
+            if 0 <= x < P:
+                refs[x] += 1
+    p = pool_of(refs, table, page)
+    for _ in range(20):
+        k = rnd.randint(1, 20)
+        names, rows = [rnd.randint(-1, S) for _ in range(k)], [rnd.randint(0, W * page) // rnd.choice([1, 9, 60]) for _ in range(k)]
+        what = rnd.randint(0, 3)
+        if what == 0:
+            p.reserve(names, rows)
+        elif what == 1:
+            p.fork([rnd.randint(0, S // 2) for _ in range(k)], [rnd.randint(S // 4, S) for _ in range(k)], rows)
+        elif what == 2:
+            p.release(names[:3], rows[:3])
+        else:
+            p.compact(rnd.choice([None, 2]))
+        counts = [0] * P
+        for r in p.table:
+            for x in r:
+                if 0 <= x < P:
+                    counts[x] += 1
+        assert counts == p.refs
