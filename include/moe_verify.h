@@ -415,7 +415,8 @@ int kv4_read(const moe_kv4_cache *cache, const moe_kv4_rows *rows, void *k, void
 /* The pages of a pool and who holds them.  A table entry inside [0,
  * num_pages) holds its page; refs counts the entries that hold each page, and
  * a page is free while its count is 0 or below.  Sequences may share the pages
- * of a common beginning.  The calls below keep counts and table in step; all
+ * of a common beginning; rows are to be written only into pages whose count is
+ * 1 (kv4_append does not look).  The calls below keep counts and table in step; all
  * layers' caches share one pool and differ in their data only, so that the
  * data is moved by kv4_copy_pages, once for each layer.
  *   refs  [num_pages] i32 (device), 0 for a new pool
@@ -456,7 +457,13 @@ int kv4_fork(const moe_kv4_pool *pool, const int32_t *src, const int32_t *dst, c
              int32_t *pairs, int32_t *ok, void *stream);
 
 /* Lets go the pages of sequence seq[i] behind its first keep[i] rows (0: all
- * of them); their entries become -1.  A sequence named twice keeps the fewer. */
+ * of them); their entries become -1.  A sequence named twice keeps the fewer.
+ * A page that is kept in part stays as it is, also where other sequences hold it
+ * (a fork, or its parent, cut back below the rows at which they parted): rows
+ * appended behind keep[i] would then overwrite theirs.  Nothing in these calls
+ * sees that.  Such a sequence is continued in a slot of its own: kv4_fork with it as
+ * src, a free slot as dst and keep[i] rows, kv4_copy_pages of the pair in every
+ * layer's cache, and kv4_release of the old slot. */
 int kv4_release(const moe_kv4_pool *pool, const int32_t *seq, const int32_t *keep, int32_t n, void *stream);
 
 /* Moves used pages to the pool's front: the i-th lowest free page takes the

@@ -1062,7 +1062,10 @@ def kv4_fork(refs, table, page: int, src, dst, rows, *, stream=None):
 
 
 def kv4_release(refs, table, page: int, seq, keep, *, stream=None) -> None:
-    """Let go the pages of sequence seq[i] behind its first keep[i] rows."""
+    """Let go the pages of sequence seq[i] behind its first keep[i] rows.  A
+    page that is kept in part and that other sequences hold too (after a fork)
+    stays shared: before rows are appended behind keep[i], fork the sequence into
+    a free slot, copy the pair, and continue there."""
     p, dev = _pool(refs, table, page)
     n = _list(dev, seq=seq, keep=keep)
     _call(lib().kv4_release, dev, stream, [], ctypes.byref(p), seq.data_ptr(), keep.data_ptr(), n)

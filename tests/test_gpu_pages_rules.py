@@ -1,8 +1,11 @@
 """Page calls that would lose rows or pages: forks of rows that the source does
-not hold, and reservations in a row of the table with a gap."""
+not hold, reservations in a row of the table with a gap, and sequences that are
+cut back into a page which others hold too."""
 import random
 
 import pytest
+
+from oracle import pages as op
 
 pytestmark = pytest.mark.gpu
 
@@ -10,6 +13,7 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("no GPU", allow_module_level=True)
 
+import moe_speculative_decoding_router_amd as m  # noqa: E402
 from test_gpu_pages import DEV, Pool, dev  # noqa: E402
 
 
@@ -96,3 +100,35 @@ def test_random_tables_with_gaps(seed):
                 if 0 <= x < P:
                     counts[x] += 1
         assert counts == p.refs
+
+
+@pytest.mark.parametrize("who", [0, 1])
+@pytest.mark.parametrize("keep", [0, 5, 16, 20, 32, 40])
+def test_cut_back_into_a_shared_page(keep, who):
+    """A prompt of 40 rows and its fork: one of the two is cut back below the fork's rows and continued, as the
+    header describes, in a slot of its own.  The other's rows stay what they were."""
+    page, n, more = 16, 40, 9
+    g = torch.Generator(device=DEV).manual_seed(keep + who)
+    p = Pool(30, 4, 6, page)
+    cache = m.kv4_cache(30, page, 2, 64, device=DEV)
+    rows = torch.randn((2, n + more, 2, 64), generator=g, device=DEV)
+    append = lambda slot, a, b, at: m.kv4_append(cache, rows[0, a:b], rows[1, a:b], p.dtable[slot:slot + 1].contiguous(),  # noqa: E731
+                                                 dev([at]), [0, b - a], return_stored=True)[0]
+    read = lambda slot, r: m.kv4_read(cache, p.dtable[slot:slot + 1].contiguous(), dev([0]), [0, r], dtype=torch.float32)[0]  # noqa: E731
+    p.reserve([0], [n])
+    stored = append(0, 0, n, 0)
+    pairs, ok = m.kv4_fork(p.drefs, p.dtable, page, dev([0]), dev([1]), dev([n]))
+    assert op.fork(p.refs, p.table, page, [0], [1], [n]) == (pairs.tolist(), ok.tolist())
+    m.kv4_copy_pages(cache, pairs)
+    p.release([who], [keep])
+    # continued in slot 2
+    pairs, ok = m.kv4_fork(p.drefs, p.dtable, page, dev([who]), dev([2]), dev([keep]))
+    assert op.fork(p.refs, p.table, page, [who], [2], [keep]) == (pairs.tolist(), ok.tolist()) and ok.tolist() == [1]
+    m.kv4_copy_pages(cache, pairs)
+    p.release([who], [0])
+    p.reserve([2], [keep + more])
+    written = {p.table[2][j] for j in range(keep // page, -(-(keep + more) // page))}
+    assert all(p.refs[x] == 1 for x in written)
+    own = append(2, n, n + more, keep)
+    assert torch.equal(read(2, keep + more), torch.cat([stored[:keep], own]))
+    assert torch.equal(read(1 - who, n), stored)
