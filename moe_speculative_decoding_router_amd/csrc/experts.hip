@@ -2,9 +2,8 @@
 // logits, and the experts' products over any number of tokens.
 #include "common.h"
 #include "dma.h"
-#include "prompt.h"
+#include "plan.h"
 
-#include <algorithm>
 #include <type_traits>
 
 namespace moe {
@@ -111,9 +110,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_tokens_kernel(const float
 // dealt to the XCDs in turn (908), outputs stored past the caches (962).
 // ---------------------------------------------------------------------------
 constexpr int kListThreads = 256;
-constexpr int kMinChunk = 2048;  // pairs of a workgroup at least
-constexpr int kPerRound = 8;     // pairs of a thread at a time
-constexpr int kMaxChunks = 256;
+constexpr int kPerRound = 8;  // pairs of a thread at a time
 
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
@@ -590,21 +587,13 @@ __global__ __launch_bounds__(kListThreads) void combine_rows_kernel(Plan p) {
     }
 }
 
-// Workgroups of a product: tiles at most, since every used expert's last one is filled in part.
-int64_t product_grid(const ExpertArgs &a, bool gate_up, int TM, int TN) {
-    const int64_t M = gate_up ? 2 * (int64_t)a.I : a.H, mblocks = (M + TM - 1) / TM, pairs = (int64_t)a.T * a.k;
-    const int64_t used = a.E < pairs ? a.E : pairs;
-    const int64_t tiles = pairs / TN + used + (a.shared ? (a.T + TN - 1) / TN : 0);
-    return (tiles * mblocks + 7) / 8 * 8;
-}
-
 template <typename S>
 hipError_t launch_product(const Plan &p, hipStream_t s) {
     if (S::kLds > 65536) {
         const hipError_t e = allow_lds<product_kernel<S>>(S::kLds);
         if (e != hipSuccess) return e;
     }
-    const int64_t grid = product_grid(p.a, S::kGateUp, S::TM, S::TN);
+    const int64_t grid = plan::product_grid(p.a, S::kGateUp, S::TM, S::TN);
     hipLaunchKernelGGL(product_kernel<S>, dim3((unsigned)grid), dim3(S::kThreads), S::kLds, s, p);
     return hipGetLastError();
 }
@@ -626,61 +615,36 @@ hipError_t launch_products(const Plan &p, hipStream_t s) {
     return launch_both<FP8, 1, 256, 256, 2, 4, 163840>(p, s);
 }
 
-// Rows of a product tile: large ones where experts have some rows on average and
-// their tiles are enough to fill half the card, small ones (32 rows by 64
-// weight rows) else.  us a call, small and large: 32 experts of 2048 x 1024, bf16, 24
-// rows each 90 and 89, 48 rows 110 and 94, 128 rows 196 and 109 (float32 111 and 101, 142
-// and 111, 287 and 215); 60 of 1024 x 512, 24 rows 45.6 and 46.3, 32 rows 50.9 and 47.8;
-// 8 of 1024 x 512 (32 large tiles), 32 rows 21.2 and 24.6, 160 rows 28.1 and 42.7.
-int tile_rows(const ExpertArgs &a) {
-    const int64_t pairs = (int64_t)a.T * a.k;
-    const int large = a.f32 ? 128 : 256;
-    const int64_t tiles = std::max(pairs / large, (int64_t)a.E) * ((2 * (int64_t)a.I + large - 1) / large);
-    return pairs / a.E < 28 || tiles < 128 ? 32 : large;
-}
-
-size_t lay_out(const ExpertArgs &a, uint8_t *ws, Plan *p) {
-    Plan q{};
-    q.a = a;
-    q.pairs = a.T * a.k;
-    q.rows = q.pairs + (a.shared ? a.T : 0);
-    q.chunk = (q.pairs + kMaxChunks - 1) / kMaxChunks;
-    if (q.chunk < kMinChunk) q.chunk = kMinChunk;
-    q.chunks = (q.pairs + q.chunk - 1) / q.chunk;
-    q.tn = tile_rows(a);
-    q.Ip = (a.I + 63) / 64 * 64;
-    const int NT = a.f32 ? 3 : 1;
-    size_t off = 0;
-    auto take = [&](size_t bytes) {
-        uint8_t *at = ws + off;
-        off += (bytes + 255) & ~(size_t)255;
-        return at;
-    };
-    q.counts = (int *)take((size_t)q.chunks * a.E * 4);
-    q.first = (int *)take((a.E + 2) * 4);
-    q.tile = (int *)take((a.E + 2) * 4);
-    q.row_token = (int *)take((size_t)q.rows * 4);
-    q.row_of = (int *)take((size_t)q.pairs * 4);
-    q.x = (__bf16 *)take(a.f32 ? (size_t)a.T * a.H * 6 : 0);
-    q.h = (__bf16 *)take((size_t)NT * q.rows * q.Ip * 2);
-    q.out = (float *)take((size_t)q.rows * a.H * 4);
-    if (p) *p = q;
-    return off;
+Plan lay_out(const ExpertArgs &a) {
+    const plan::Experts q = plan::experts(a);
+    uint8_t *ws = (uint8_t *)a.ws;
+    Plan p{};
+    p.a = a;
+    p.pairs = q.pairs;
+    p.rows = q.rows;
+    p.chunk = q.chunk;
+    p.chunks = q.chunks;
+    p.tn = q.tn;
+    p.Ip = q.Ip;
+    p.counts = (int *)(ws + q.counts);
+    p.first = (int *)(ws + q.first);
+    p.tile = (int *)(ws + q.tile);
+    p.row_token = (int *)(ws + q.row_token);
+    p.row_of = (int *)(ws + q.row_of);
+    p.x = (__bf16 *)(ws + q.x);
+    p.h = (__bf16 *)(ws + q.h);
+    p.out = (float *)(ws + q.out);
+    return p;
 }
 
 }  // namespace
 
-bool experts_fit(const ExpertArgs &a) {
-    const int TN = tile_rows(a), TM = TN == 32 ? 64 : TN == 128 ? 128 : 256;
-    const int64_t grid = std::max(product_grid(a, true, TM, TN), product_grid(a, false, TM, TN));
-    return grid < 1 << 22 && (int64_t)a.T * a.H < (int64_t)1 << 33;
-}
+bool experts_fit(const ExpertArgs &a) { return plan::experts_fit(a); }
 
-size_t experts_ws_bytes(const ExpertArgs &a) { return lay_out(a, nullptr, nullptr); }
+size_t experts_ws_bytes(const ExpertArgs &a) { return plan::experts(a).bytes; }
 
 hipError_t launch_experts(const ExpertArgs &a, hipStream_t s) {
-    Plan p;
-    lay_out(a, (uint8_t *)a.ws, &p);
+    const Plan p = lay_out(a);
     if (p.chunks > 1) hipLaunchKernelGGL(count_pairs_kernel, dim3(p.chunks), dim3(kListThreads), 0, s, p);
     hipLaunchKernelGGL(place_pairs_kernel, dim3(p.chunks), dim3(kListThreads), 0, s, p);
     if (a.f32) {

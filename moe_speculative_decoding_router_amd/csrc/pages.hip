@@ -3,7 +3,7 @@
 // Layout and semantics in include/moe_verify.h.
 #include "common.h"
 #include "kv4.h"
-#include "prompt.h"
+#include "plan.h"
 
 namespace moe {
 namespace {
@@ -306,6 +306,7 @@ __global__ __launch_bounds__(kThreads) void release_kernel(PoolArgs a) {
 // ---------------------------------------------------------------------------
 constexpr int kPerThread = 16;
 constexpr int kChunk = kThreads * kPerThread;  // pages of a workgroup
+static_assert(kChunk == plan::kCompactChunk, "");
 constexpr int kDirect = 16384;  // pages up to which every workgroup counts the used ones of all chunks for itself
 
 __device__ __forceinline__ int block_sum(int v, int *part) {
@@ -459,15 +460,10 @@ hipError_t launch_release(const PoolArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Workspace: used pages of each chunk and of all, the lowest free and the
-// highest used pages, the used pages' ranks.
-size_t compact_ws_bytes(int num_pages, int max_moves) {
-    const int most = max_moves < num_pages / 2 ? max_moves : num_pages / 2;
-    return 4 * ((size_t)(num_pages + kChunk - 1) / kChunk + 1 + 2 * (size_t)most + num_pages);
-}
+size_t compact_ws_bytes(int num_pages, int max_moves) { return plan::compact_bytes(num_pages, max_moves); }
 
 hipError_t launch_compact(CompactArgs a, int32_t *ws, hipStream_t s) {
-    a.most = a.max_moves < a.num_pages / 2 ? a.max_moves : a.num_pages / 2;
+    a.most = plan::compact_most(a.num_pages, a.max_moves);
     a.chunks = (a.num_pages + kChunk - 1) / kChunk;
     a.chunk = ws;
     a.low = a.chunk + a.chunks + 1;

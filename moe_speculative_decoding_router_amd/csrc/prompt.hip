@@ -2,7 +2,7 @@
 // sequences.  Semantics in include/moe_verify.h.
 #include "common.h"
 #include "dma.h"
-#include "prompt.h"
+#include "plan.h"
 
 namespace moe {
 namespace {
@@ -15,6 +15,7 @@ typedef short s16x8 __attribute__((ext_vector_type(8)));
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kRows = 32 * kWaves;         // query rows of a workgroup, 32 a wave
+static_assert(kRows == plan::kRows, "");
 constexpr float kNone = -3.402823466e38f;  // running maximum before the first score
 constexpr float kSlack = 8.f;              // a score may pass the maximum by this (log2) before it moves
 
@@ -439,38 +440,7 @@ hipError_t launch(const PromptArgs &a, hipStream_t s) {
 
 }  // namespace
 
-size_t prompt_plan(PromptArgs &a, int n_cu) {
-    int blocks = 0, keys = 0;
-    a.blocks[0] = 0;
-    for (int s = 0; s < a.nseq; ++s) {
-        const int n = a.q_off[s + 1] - a.q_off[s], m = a.k_off[s + 1] - a.k_off[s];
-        blocks += (n + kRows - 1) / kRows;
-        a.blocks[s + 1] = blocks;
-        if (n > 0 && m > keys) keys = m;
-    }
-    a.units = (int64_t)blocks * a.Hq < INT32_MAX ? blocks * a.Hq : INT32_MAX;
-    a.parts = 1;
-    // Units that fill the workgroups that run at once a few times over at most leave some idle in the
-    // last round.  Their keys are cut into as many shares of at least 256 as take the least time, by
-    // what a step of 64 keys costs a workgroup (1.6 us at D = 128 where two share a compute unit) and
-    // the join of a share's rows.  (515 rows, 32 heads, 60516 keys: 570 us with three shares, 680 with
-    // the four that fill every workgroup, 571 with sixteen.)
-    const int slots = n_cu * (a.f32 ? 1 : 2);
-    if (a.units > 0 && a.units < 4 * slots) {
-        const double step = 1.6 * a.D / 128 * (a.f32 ? 3 : 1), join = (double)a.units * kRows * (a.D + 2) * 8 / 4.5e6;
-        double best = 1e30;
-        for (int p = 1; p <= 64 && (p == 1 || p <= keys / 256); ++p) {
-            const int64_t rounds = ((int64_t)a.units * p + slots - 1) / slots;
-            const double cost = rounds * (keys / 64.0 / p) * step + (p > 1 ? 4 + join * p : 0);
-            if (cost < 0.98 * best) best = cost, a.parts = p;
-        }
-    }
-    size_t ws = a.f32 ? (size_t)a.k_off[a.nseq] * a.Hkv * a.D * 12 : 0;
-    ws = (ws + 255) & ~(size_t)255;
-    a.part_at = ws;
-    if (a.parts > 1) ws += (size_t)a.units * a.parts * kRows * (a.D + 2) * 4;
-    return ws;
-}
+size_t prompt_plan(PromptArgs &a, int n_cu) { return plan::prompt(a, n_cu); }
 
 hipError_t launch_prompt(const PromptArgs &a, hipStream_t s) {
     if (a.D == 64) return a.f32 ? launch<64, 3>(a, s) : launch<64, 1>(a, s);
