@@ -12,6 +12,7 @@ if not torch.cuda.is_available():
     pytest.skip("no GPU", allow_module_level=True)
 
 import moe_speculative_decoding_router_amd as m  # noqa: E402
+import norms  # noqa: E402
 from plan_rules import tile_rows  # noqa: E402
 from test_gpu_experts import DEV, DT, Layer  # noqa: E402
 
@@ -93,3 +94,17 @@ def test_strides_and_a_graph(wdtype, dtype):
         got = y.clone()
         assert torch.equal(got, m.experts(a[0], L.w, a[1], a[2]))
         L.check(*a, y=got)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,I,E,T,large", [(8320, 128, 3, 50, False), (8320, 128, 128, 3700, True), (128, 8320, 1, 20, False), (128, 8320, 4, 150, True)])
+def test_more_blocks_than_a_wave_has_lanes(H, I, E, T, large, dtype):
+    """fp8 sums of 65 blocks of 128 k: a lane holds the scales of every 64th block, the second set one block alone.
+    Scales differ by block, over a factor of 16 and by sign."""
+    L = Layer(H + E, H, I, E, 1, "fp8")
+    takes(L, T, dtype, LARGE[dtype] if large else 32)
+    x, idx, w = L.inputs(T, T, dtype)
+    y = L.check(x, idx, w)
+    ref = L.reference(x, idx, w)[0]
+    assert norms.off(y, ref) <= (norms.experts_f32(H, I, True) if dtype == "f32" else norms.experts_bf16())
+    assert torch.equal(m.experts(x, L.w, idx, w), y)
