@@ -533,7 +533,7 @@ int route_tokens(const float *logits, int64_t stride, int32_t T, int32_t E, int3
  * (route_tokens', or any other):
  *   y[t] = sum_j topk_w[t][j] FFN_{topk_idx[t][j]}(x_t) (+ shared expert)
  * with the layer of moe_verify_layer (bf16 or fp8 weights, packed; Wr is not
- * read).  Tokens are grouped by expert, whose weights are read once for a tile of
+ * read, but no layer is without it).  Tokens are grouped by expert, whose weights are read once for a tile of
  * up to 256 of them.
  *   x     [T, H] in dtype MOE_F32 or MOE_BF16, tokens x_stride elements apart,
  *         16-byte aligned rows

@@ -98,8 +98,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_tokens_kernel(const float
 // results would be off by 0.0029 of their norm instead of 0.0023 (plain float32 ones that
 // are rounded once: 0.0017).
 //
-// What bounds it: 4099 tokens, 4 of 32 experts of 2880 x 2880 (816 GFLOP) take 900 to
-// 930 us, of which gate-up 560 (970 TFLOP/s) and down 330 (825), where a large bf16
+// What bounds it: 4099 tokens, 4 of 32 experts of 2880 x 2880 (816 GFLOP) take 877 to
+// 930 us, of which gate-up 543 (1000 TFLOP/s) and down 325 (835), where a large bf16
 // product reaches 1352; 40 go to adding 190 MB of outputs, 9 to the lists.  Matrix
 // instructions are under way 52% of the cycles: compute units idle 20% of the
 // time behind the last of their six or seven tiles, and the clock falls to 1.9 GHz.

@@ -122,10 +122,13 @@ __device__ int free_before(const PoolArgs &a, int base, Take &t, unsigned &mask,
 // Gives entry i of the list its need[i] lowest free pages, the entries in
 // order, each whole or not at all; writes them to table[at[i]...] with a count
 // of 1 and sets start[i] (-1: not enough pages).
+// Latency bounds it, 8192 counts a step: a page for each of 64 sequences takes 57 us in a pool of 8192
+// pages, where few threads find all and look up whose they are, and 121 and 156 behind 60000 and 96000
+// used pages, which both passes go over from page 0.
 __device__ void take_pages(const PoolArgs &a, Take &t) {
     // This workgroup's atomics have arrived in the L2, which is all that its own later accesses need.
     // (A fence would write the whole L2 back as well: the
-    // fork of a prompt into 15 then takes 25 us instead of 20.)
+    // fork of a prompt into 15 then takes 25 us instead of 21.)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     const int lane = threadIdx.x & 63;

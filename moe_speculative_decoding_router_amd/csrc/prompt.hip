@@ -110,13 +110,14 @@ __global__ __launch_bounds__(kThreads) void split_kernel(const float *k, const f
 //
 // What bounds it: matrix and vector instructions of the two workgroups of a
 // compute unit hardly overlap.  12000 rows of six prompts, 64 heads on 4 of 128
-// (614 GFLOP) take 671 us, 915 TFLOP/s, where a large bf16 product reaches 1352;
+// (614 GFLOP) take 620 to 671 us, 915 to 990 TFLOP/s, where a large bf16 product reaches 1352;
 // matrix instructions are under way 50% of the cycles and vector instructions
 // 46%, and each 32 rows read a step's whole K and V from LDS (61% of its rate).
 // 64 rows a wave would halve that, at one wave a SIMD and with the softmax
 // placed by hand.  Wave priorities, of the softmax over the products or the other
-// way, cost 1% to 3%.  515 rows behind 60001 (508 GFLOP) take 570 to 595 us in three
-// shares a unit.  float32 at D = 256 spills 200 registers a lane, which is left.
+// way, cost 1% to 3%.  515 rows behind 60001 (508 GFLOP) take 553 to 600 us in three
+// shares a unit.  At D = 256 float32 spills 219 registers a lane (4000 rows, 16 heads on 4: 1824 us, with
+// D = 128 398, where six products at the large one's rate would take 582 and 291), bf16 three.
 // ---------------------------------------------------------------------------
 template <int D, int NT>
 __global__ __launch_bounds__(kThreads, groups(D, NT)) void prompt_kernel(PromptArgs a) {
